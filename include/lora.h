@@ -9,7 +9,11 @@
  *     lora_da_dx_update_wrapper, lora_db_kernel / lora_db_update_wrapper;
  *   - slot-addressed multi-adapter serving ops, as defined by the API page
  *     "mstar.engine.resources.lora.ops" (M* engine), class LoraOpsBackend:
- *     shrink, expand_fused, gather_shrink.
+ *     shrink, expand_fused, gather_shrink;
+ *   - the operators of a training step around the adapter linears: embedding
+ *     lookup and its gradient, token log probabilities with the preference
+ *     and policy losses on them and the gradient of the logits, and an AdamW
+ *     step over many tensors.
  *
  * Conventions (all entry points):
  *   - Every tensor pointer is a DEVICE pointer. Sizes, strides, out_slices and
@@ -359,6 +363,194 @@ int lora_apply_linear_noalloc(const lora_mat* x, const lora_t3* a, const lora_t3
  */
 int lora_gather_shrink(const int32_t* ids, const lora_t3* a, const lora_addressing* addr, const int32_t* ranks,
                        int32_t r_max, const lora_t3* h, void* stream);
+
+/*
+ * Embedding lookup with scaling:
+ *     out[t] = scale * table[ids[t]], zeros for an id outside [0, V)
+ *   ids    int32[T] device.
+ *   table  V x D, bf16 or f32.
+ *   out    T x D, f32, or bf16 with a bf16 table (the float32 product rounded
+ *          once).
+ *   table and out: stride_col 1, stride_row at least D, aligned to their
+ *   elements (any D and any row pitch).
+ */
+int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lora_mat* out, void* stream);
+
+/*
+ * Gradient of the lookup for its table:
+ *     dtable[v] = scale * (sum of dy[t] over the tokens t with ids[t] = v)
+ *   dy      T x D, bf16 or f32; dtable V x D, f32, or bf16 with bf16 dy (the
+ *           float32 sum rounded once); layouts as for lora_embed.
+ *   accumulate 0: every row is written, zeros where no token names it;
+ *           otherwise the rows that tokens name are added to and the others
+ *           left alone.
+ *   Ids outside [0, V) add no term. The tokens are sorted by id on the device
+ *   and each id's terms added in an order that depends on the ids alone (no
+ *   float atomics). T, V below 2^31 - 4096.
+ *   workspace: lora_embed_grad_workspace_bytes(T, V, D), 256-byte aligned.
+ */
+size_t lora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);
+int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float scale, const lora_mat* dtable, int32_t accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Losses on next-token logits. For all of them:
+ *   logits   T x V, bf16 or f32, stride_col 1, stride_row at least V, aligned
+ *            to its elements (any V and any row pitch); T below 2^25, V below
+ *            2^31 - 8192.
+ *   targets  int32[T] device: the token whose log probability counts. A
+ *            target outside [0, V) masks its row: the row is not read, its
+ *            log probability is 0 and its gradient zeros.
+ *   dlogits  T x V of the logits' dtype, layout rules as for logits; it may
+ *            be the logits themselves (same pointer and strides), otherwise
+ *            it must not overlap them. Every element is written.
+ *   workspace: lora_loss_workspace_bytes(T, V), 256-byte aligned.
+ * A row whose logits are all -inf, or that holds +inf or NaN, gives NaN.
+ *
+ * Workspace of the calls below; 0 for sizes beyond the limits.
+ */
+size_t lora_loss_workspace_bytes(int64_t T, int64_t V);
+
+/*
+ * Log probabilities of the targets and each row's softmax statistics:
+ *   logp   float[T]: x[t, y_t] - log(sum_j exp(x[t, j])).
+ *   stats  float[T][2]: the row's largest logit m and sum_j exp(x[t, j] - m)
+ *          (0 and 1 for a masked row), which lora_logit_grad takes.
+ */
+int lora_token_logp(const lora_mat* logits, const int32_t* targets, float* logp, float* stats, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Preference loss of paired sequences from their tokens' log probabilities:
+ *   seq_offsets  int32[2 * pairs + 1] device, not decreasing: sequence s is the
+ *                tokens [seq_offsets[s], seq_offsets[s + 1]) (offsets are
+ *                clamped to [0, T]); sequence 2p is the preferred one of pair
+ *                p, 2p + 1 the other. An empty sequence has log probability 0.
+ *   ref_logp     float[2 * pairs]: the sequences' log probabilities under the
+ *                reference model.
+ *   z_p  = beta * ((S_2p - ref_2p) - (S_2p+1 - ref_2p+1))
+ *   loss = mean_p of -(1 - eps) * log sigmoid(z_p) - eps * log sigmoid(-z_p)
+ *          with eps = label_smoothing; one float, out.
+ *   seq_logp     float[2 * pairs], out or NULL: the sums S.
+ *   coef         float[T], out or NULL: d loss / d logp of each token (0
+ *                outside the sequences).
+ *   Sums and z are kept in float64. Also with T = 0 the loss is written.
+ */
+int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_offsets, int64_t pairs, const float* ref_logp,
+                   float beta, float label_smoothing, float* loss, float* seq_logp, float* coef, void* stream);
+
+/* Inputs of the policy loss for each token (device arrays of T). */
+typedef struct {
+  const int32_t* targets;  /* the sampled tokens; outside [0, V): masked */
+  const float* old_logp;   /* log probabilities when the tokens were sampled */
+  const float* ref_logp;   /* under the reference model; may be NULL if kl_coef is 0 */
+  const float* advantages;
+  const float* weights;    /* the token's share of the loss, e.g. 1 / number of tokens */
+  float clip_low, clip_high, kl_coef;
+} lora_policy;
+
+/*
+ * Clipped policy loss with a KL term, from the tokens' log probabilities:
+ *   r_t  = exp(logp_t - old_logp_t), k_t = ref_logp_t - logp_t
+ *   loss = sum over the unmasked tokens of weights_t *
+ *          (-min(r_t A_t, clamp(r_t, 1 - clip_low, 1 + clip_high) A_t)
+ *           + kl_coef * (exp(k_t) - k_t - 1))
+ *   loss  one float, out (summed in float64; also written with T = 0).
+ *   coef  float[T], out or NULL: d loss / d logp (0 for masked tokens, whose
+ *         other inputs are not used).
+ */
+int lora_policy_loss(const float* logp, int64_t T, int64_t V, const lora_policy* policy, float* loss, float* coef,
+                     void* stream);
+
+/*
+ * Gradient of the logits of a loss with d loss / d logp = coef:
+ *   dlogits[t, j] = g * coef_t * ([j = y_t] - softmax(x[t])_j)
+ *   with g = scale, times *grad_out (one float on the device) unless that is
+ *   NULL; stats from lora_token_logp on the same logits and targets.
+ */
+int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* coef,
+                    const float* grad_out, float scale, const lora_mat* dlogits, void* stream);
+
+/*
+ * Loss and gradient in one call: lora_token_logp, then the loss, then
+ * lora_logit_grad with the loss's coefficients and scale = grad_scale.
+ * Outputs as for these calls (loss, seq_logp or NULL, logp, dlogits).
+ */
+int lora_pref_step(const lora_mat* logits, const int32_t* targets, const int32_t* seq_offsets, int64_t pairs,
+                   const float* ref_logp, float beta, float label_smoothing, float grad_scale, float* loss,
+                   float* seq_logp, float* logp, const lora_mat* dlogits, void* workspace, size_t workspace_bytes,
+                   void* stream);
+int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float grad_scale, float* loss, float* logp,
+                     const lora_mat* dlogits, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * AdamW over many tensors at once:
+ *   g' = grad_scale * g
+ *   m  = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in float32, t counted on the device so that a captured step replays right.
+ *
+ * One tensor: numel consecutive elements of param (updated in place; f32, or
+ * bf16, rounded once) and grad (f32 or bf16), each aligned to its elements;
+ * shadow: NULL, or numel bf16 elements (aligned to 2 bytes) that receive an
+ * f32 param's new value rounded once (the copy that the forward reads).
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* shadow;
+  int64_t numel;
+  int32_t param_dtype, grad_dtype; /* lora_dtype */
+} lora_adamw_tensor;
+
+/*
+ * Optimizer state of all tensors (device memory, zeros before the first
+ * step). The states of tensor i start at element 256 * sum over the earlier
+ * tensors of ceil(numel / 256); lora_adamw_state_elems gives the length.
+ *   bits 32: m and v are float arrays.
+ *   bits 8:  m and v are arrays of e4m3 codes (one byte each), m_scale and
+ *            v_scale floats, one for every 256 elements: m = code * scale,
+ *            v = (code * scale)^2. A scale is the largest magnitude of its
+ *            block (of m, of sqrt(v)) over 448, codes are rounded to nearest
+ *            even; a v above zero keeps at least the smallest code; a block
+ *            whose largest magnitude is below 1e-30 is stored as zeros. The
+ *            update of a step uses m and v before they are rounded.
+ *   m and v 16-byte aligned. step: one int32, the number of steps taken.
+ */
+typedef struct {
+  int32_t bits;
+  int32_t reserved;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int32_t* step;
+} lora_adamw_state;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  const float* lr_scale;   /* one float on the device that multiplies lr, or NULL */
+  const float* grad_scale; /* one float on the device that multiplies every gradient, or NULL */
+} lora_adamw_hyper;
+
+/*
+ * The table of the tensors (device memory of lora_adamw_table_bytes, 256-byte
+ * aligned), which lora_adamw_table writes on the stream and every later step
+ * over the same tensors takes; it holds their addresses, so it is written
+ * again when one of them moves. At most 2^23 - 1 tensors. The sizes are 0 for
+ * invalid tensors.
+ */
+size_t lora_adamw_table_bytes(const lora_adamw_tensor* tensors, int64_t n);
+int64_t lora_adamw_state_elems(const lora_adamw_tensor* tensors, int64_t n);
+int lora_adamw_table(const lora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes, void* stream);
+
+/*
+ * One step over the tensors of the table: counts the step, updates param,
+ * shadow, m and v. `tensors` are the ones that the table was written from
+ * (their sizes are checked, their addresses come from the table); a table
+ * written from tensors of another number or total size updates nothing but
+ * the count. With no elements nothing is launched.
+ */
+int lora_adamw_step(const lora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
+                    const lora_adamw_state* state, const lora_adamw_hyper* hyper, void* stream);
 
 #ifdef __cplusplus
 }

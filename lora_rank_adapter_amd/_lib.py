@@ -69,6 +69,54 @@ class LoraAddressing(ctypes.Structure):
     ]
 
 
+class LoraPolicy(ctypes.Structure):
+    _fields_ = [
+        ("targets", ctypes.c_void_p),
+        ("old_logp", ctypes.c_void_p),
+        ("ref_logp", ctypes.c_void_p),
+        ("advantages", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("clip_low", ctypes.c_float),
+        ("clip_high", ctypes.c_float),
+        ("kl_coef", ctypes.c_float),
+    ]
+
+
+class LoraAdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("shadow", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+    ]
+
+
+class LoraAdamwState(ctypes.Structure):
+    _fields_ = [
+        ("bits", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("step", ctypes.c_void_p),
+    ]
+
+
+class LoraAdamwHyper(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("lr_scale", ctypes.c_void_p),
+        ("grad_scale", ctypes.c_void_p),
+    ]
+
+
 # exported symbol -> (restype, argtypes)
 _P = ctypes.POINTER
 SIGNATURES = {
@@ -99,6 +147,33 @@ SIGNATURES = {
                                                  ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
     "lora_gather_shrink": (ctypes.c_int, [ctypes.c_void_p, _P(LoraT3), _P(LoraAddressing), ctypes.c_void_p,
                                           ctypes.c_int32, _P(LoraT3), ctypes.c_void_p]),
+    "lora_embed": (ctypes.c_int, [ctypes.c_void_p, _P(LoraMat), ctypes.c_float, _P(LoraMat), ctypes.c_void_p]),
+    "lora_embed_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "lora_embed_grad": (ctypes.c_int, [ctypes.c_void_p, _P(LoraMat), ctypes.c_float, _P(LoraMat), ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "lora_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "lora_token_logp": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "lora_pref_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "lora_policy_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, _P(LoraPolicy),
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "lora_logit_grad": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_float, _P(LoraMat), ctypes.c_void_p]),
+    "lora_pref_step": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                      ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, _P(LoraMat), ctypes.c_void_p,
+                                      ctypes.c_size_t, ctypes.c_void_p]),
+    "lora_policy_step": (ctypes.c_int, [_P(LoraMat), _P(LoraPolicy), ctypes.c_float, ctypes.c_void_p,
+                                        ctypes.c_void_p, _P(LoraMat), ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
+    "lora_adamw_table_bytes": (ctypes.c_size_t, [_P(LoraAdamwTensor), ctypes.c_int64]),
+    "lora_adamw_state_elems": (ctypes.c_int64, [_P(LoraAdamwTensor), ctypes.c_int64]),
+    "lora_adamw_table": (ctypes.c_int, [_P(LoraAdamwTensor), ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
+    "lora_adamw_step": (ctypes.c_int, [_P(LoraAdamwTensor), ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
+                                       _P(LoraAdamwState), _P(LoraAdamwHyper), ctypes.c_void_p]),
     "lora_timing_begin": (ctypes.c_int, []),
     "lora_timing_pause": (ctypes.c_int, []),
     "lora_timing_resume": (ctypes.c_int, []),

@@ -18,8 +18,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "liblora_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 DIGEST_PATH = LIB_PATH + ".digest"   # digest of the sources the library was built from
-SOURCES = ["lora_single.hip", "lora_multi.hip"]
-HEADERS = ["lora_device.hpp", "lora_host.hpp"]
+SOURCES = ["lora_single.hip", "lora_multi.hip", "lora_embed.hip", "lora_loss.hip", "lora_optim.hip"]
+HEADERS = ["lora_device.hpp", "lora_host.hpp", "lora_rows.hpp"]
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

@@ -1,0 +1,514 @@
+// Token log probabilities, the preference loss over paired sequences, the
+// clipped policy loss with a KL term, and the gradient of their logits.
+//
+//   lse_t = log sum_j exp(x[t, j]),  logp_t = x[t, y_t] - lse_t
+//   dx[t, j] = c_t * ([j = y_t] - exp(x[t, j] - lse_t))
+//
+// Both losses depend on the logits only through logp, so every gradient is
+// the same rank-one correction of a softmax with a coefficient c_t for each
+// token. A token whose target lies outside [0, V) is masked: its row is never
+// read, its logp is 0 and its gradient row is zeros.
+//
+// The softmax's statistics of a row are kept as its largest logit m and the
+// sum s of exp(x - m), both float32: exp(x - m) / s keeps the precision that
+// exp(x - lse) would lose to the rounding of a large lse.
+//
+// Kernels:
+//   logp_kernel       one pass over a row (or one piece of it): running max and sum
+//   join_kernel       the pieces of a row joined, one wave per row
+//   pref_kernel       sequence sums, the loss and each token's coefficient
+//   policy_kernel     each token's loss and coefficient, and their sum
+//   grad_kernel       the gradient's rows from the statistics and coefficients
+
+#include <type_traits>
+
+#include "lora_host.hpp"
+#include "lora_rows.hpp"
+
+namespace lora {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_raw(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Running maximum m and sum s of exp(x - m). With nothing seen (or only
+// -inf) m is -inf and s is 0; +inf and NaN give a NaN sum, as the formula
+// does, and values of the type's lowest magnitude are ordinary values.
+struct MaxSum {
+  float m, s;
+};
+__device__ __forceinline__ float at_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
+  const float m = fmaxf(a.m, b.m);
+  const float z = at_max(m);
+  return {m, a.s * exp2_raw((a.m - z) * kLog2e) + b.s * exp2_raw((b.m - z) * kLog2e)};
+}
+
+template <int N>
+__device__ __forceinline__ void add_values(MaxSum& r, const float* f) {
+  float m = r.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
+  const float z = at_max(m);
+  float s = r.s * exp2_raw((r.m - z) * kLog2e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += exp2_raw((f[i] - z) * kLog2e);
+  r = {m, s};
+}
+
+__device__ __forceinline__ MaxSum wave_join(MaxSum v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = join(v, MaxSum{__shfl_xor(v.m, d, 64), __shfl_xor(v.s, d, 64)});
+  return v;
+}
+
+// logp of the target from the row's statistics
+__device__ __forceinline__ float target_logp(float x, MaxSum v) { return (x - v.m) - logf(v.s); }
+
+template <class E>
+__global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
+                                                   const int32_t* __restrict__ targets, int V, int splits, int piece,
+                                                   float* __restrict__ logp, float2* __restrict__ stats,
+                                                   float2* __restrict__ part) {
+  constexpr int N = Vec<E>::N, U = 4;
+  __shared__ MaxSum waves[4];
+  const int64_t row = (int64_t)blockIdx.x / splits;
+  const int sp = (int)((int64_t)blockIdx.x % splits);
+  const int tid = threadIdx.x;
+  const int y = targets[row];
+  if (y < 0 || y >= V) {
+    if (splits == 1 && tid == 0) {
+      logp[row] = 0.0f;
+      stats[row] = make_float2(0.0f, 1.0f);
+    }
+    return;
+  }
+  const E* src = x + row * stride;
+  const int lo = sp * piece;
+  const int n = V - lo < piece ? V - lo : piece;
+  const E* p = src + lo;
+  const int vecs = n / N;
+  MaxSum r{-INFINITY, 0.0f};
+  int i = tid;
+  for (; i + (U - 1) * 256 < vecs; i += U * 256) {
+    float f[U * N];
+    typename Vec<E>::type w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(i + u * 256) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) Vec<E>::unpack(w[u], f + u * N);
+    add_values<U * N>(r, f);
+  }
+  for (; i < vecs; i += 256) {
+    float f[N];
+    Vec<E>::unpack(vload_nt(p + (int64_t)i * N), f);
+    add_values<N>(r, f);
+  }
+  if (tid < n - vecs * N) {
+    const float f = Vec<E>::value(p[vecs * N + tid]);
+    add_values<1>(r, &f);
+  }
+  r = wave_join(r);
+  if ((tid & 63) == 0) waves[tid >> 6] = r;
+  __syncthreads();
+  if (tid != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) r = join(r, waves[w]);
+  if (splits > 1) {
+    part[row * splits + sp] = make_float2(r.m, r.s);
+  } else {
+    logp[row] = target_logp(Vec<E>::value(src[y]), r);
+    stats[row] = make_float2(r.m, r.s);
+  }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void join_kernel(const E* __restrict__ x, int64_t stride,
+                                                   const int32_t* __restrict__ targets, int64_t T, int V, int splits,
+                                                   const float2* __restrict__ part, float* __restrict__ logp,
+                                                   float2* __restrict__ stats) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  const int lane = threadIdx.x & 63;
+  if (row >= T) return;
+  const int y = targets[row];
+  if (y < 0 || y >= V) {
+    if (lane == 0) {
+      logp[row] = 0.0f;
+      stats[row] = make_float2(0.0f, 1.0f);
+    }
+    return;
+  }
+  const float2 v = lane < splits ? part[row * splits + lane] : make_float2(-INFINITY, 0.0f);
+  const MaxSum r = wave_join(MaxSum{v.x, v.y});
+  if (lane == 0) {
+    logp[row] = target_logp(Vec<E>::value(x[row * stride + y]), r);
+    stats[row] = make_float2(r.m, r.s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// losses on the log probabilities (one workgroup: a few values per token)
+// ---------------------------------------------------------------------------
+
+// The sum of v over the workgroup's 16 waves, in the order of the waves.
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double total = 0.0;
+  for (int w = 0; w < 16; ++w) total += lds[w];
+  __syncthreads();
+  return total;
+}
+
+// z = beta * ((S_c - ref_c) - (S_r - ref_r)); loss = mean of
+// -(1 - eps) log sigmoid(z) - eps log sigmoid(-z), whose derivative by z is
+// eps - sigmoid(-z). Sequence sums and z are float64: z is a small
+// difference of long sums. One wave per pair; its two sequences' tokens get
+// the coefficients beta * dz / pairs and minus that.
+__global__ __launch_bounds__(1024) void pref_kernel(const float* __restrict__ logp, int64_t T,
+                                                    const int32_t* __restrict__ offsets, int64_t pairs,
+                                                    const float* __restrict__ ref, float beta, float eps,
+                                                    float* __restrict__ loss, float* __restrict__ seq_logp,
+                                                    float* __restrict__ coef) {
+  __shared__ double lds[16];
+  const int lane = threadIdx.x & 63;
+  auto offset = [&](int64_t i) -> int64_t {
+    const int64_t o = offsets[i];
+    return o < 0 ? 0 : (o > T ? T : o);
+  };
+  if (coef != nullptr) {
+    // tokens before the first sequence and after the last
+    const int64_t a = offset(0), b = offset(2 * pairs);
+    for (int64_t t = threadIdx.x; t < a; t += 1024) coef[t] = 0.0f;
+    for (int64_t t = b + threadIdx.x; t < T; t += 1024) coef[t] = 0.0f;
+  }
+  double total = 0.0;
+  for (int64_t p = wave_id(); p < pairs; p += 16) {
+    const int64_t o[3] = {offset(2 * p), offset(2 * p + 1), offset(2 * p + 2)};
+    double s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      double v = 0.0;
+      for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) v += logp[t];
+      s[k] = wave_sum(v);
+      if (lane == 0 && seq_logp != nullptr) seq_logp[2 * p + k] = static_cast<float>(s[k]);
+    }
+    const double z = (double)beta * ((s[0] - ref[2 * p]) - (s[1] - ref[2 * p + 1]));
+    const double e = exp(-fabs(z)), l = log1p(e);
+    // a weight of zero drops its term, also where that is infinite
+    if (eps != 1.0f) total += (1.0 - (double)eps) * (l + fmax(-z, 0.0));
+    if (eps != 0.0f) total += (double)eps * (l + fmax(z, 0.0));
+    if (coef != nullptr) {
+      const double down = (z >= 0.0 ? e : 1.0) / (1.0 + e);  // sigmoid(-z)
+      const double d = ((double)eps - down) * (double)beta / (double)pairs;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) coef[t] = static_cast<float>(k == 0 ? d : -d);
+    }
+  }
+  total = block_sum(lane == 0 ? total : 0.0, lds);
+  if (threadIdx.x == 0) *loss = static_cast<float>(total / (double)pairs);
+}
+
+struct PolicyArgs {
+  const int32_t* targets;
+  const float *old_logp, *ref_logp, *advantages, *weights;
+  float clip_low, clip_high, kl;
+};
+
+// One token of the policy loss: its weighted loss and d loss / d logp.
+__device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, float lp) {
+  const float ratio = expf(lp - a.old_logp[t]);
+  const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
+  const float adv = a.advantages[t], w = a.weights[t];
+  const bool clipped = ratio * adv > held * adv;  // the clipped surrogate is the smaller one
+  float l = -(clipped ? held * adv : ratio * adv);
+  float d = clipped ? 0.0f : -ratio * adv;
+  if (a.ref_logp != nullptr) {
+    const float k = a.ref_logp[t] - lp;
+    const float e = expm1f(k);
+    l += a.kl * (e - k);
+    d -= a.kl * e;
+  }
+  return make_float2(w * l, w * d);
+}
+
+__global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ logp, int64_t T, int64_t V,
+                                                      PolicyArgs a, float* __restrict__ loss,
+                                                      float* __restrict__ coef) {
+  __shared__ double lds[16];
+  double sum = 0.0;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    const int y = a.targets[t];
+    float2 v = make_float2(0.0f, 0.0f);
+    if (y >= 0 && y < V) v = policy_token(a, t, logp[t]);
+    sum += v.x;
+    if (coef != nullptr) coef[t] = v.y;
+  }
+  sum = block_sum(sum, lds);
+  if (threadIdx.x == 0) *loss = static_cast<float>(sum);
+}
+
+// ---------------------------------------------------------------------------
+// gradient: a workgroup takes 256 * U vectors of one row
+// ---------------------------------------------------------------------------
+constexpr int kGradVecs = 1024;
+
+template <class E>
+__global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t stride,
+                                                         const int32_t* __restrict__ targets,
+                                                         const float2* __restrict__ stats,
+                                                         const float* __restrict__ coef,
+                                                         const float* __restrict__ grad_out, float scale, int V,
+                                                         int pieces, E* dx, int64_t dx_stride) {
+  constexpr int N = Vec<E>::N, U = kGradVecs / 256;
+  const int64_t row = (int64_t)blockIdx.x / pieces;
+  const int lo = (int)((int64_t)blockIdx.x % pieces) * kGradVecs * N;
+  const int n = V - lo < kGradVecs * N ? V - lo : kGradVecs * N;
+  const int tid = threadIdx.x;
+  const int y = targets[row];
+  const bool live = y >= 0 && y < V;
+  // dx may be x: no restrict on it, and a vector is stored by the lane that loaded it
+  const E* p = x + row * stride + lo;
+  E* q = dx + row * dx_stride + lo;
+  const int vecs = n / N;
+  if (!live) {
+    const typename Vec<E>::type zero = {0u, 0u, 0u, 0u};
+    for (int i = tid; i < vecs; i += 256) vstore_nt(q + i * N, zero);
+    if (tid < n - vecs * N) q[vecs * N + tid] = Vec<E>::round(0.0f);
+    return;
+  }
+  float c = coef[row] * scale;
+  if (grad_out != nullptr) c *= *grad_out;
+  const float2 st = stats[row];
+  const float m = at_max(st.x), cs = c / st.y;
+  const int hit = y - lo;
+  auto value = [&](float v, int j) {
+    const float g = -cs * exp2_raw((v - m) * kLog2e);
+    return j == hit ? g + c : g;
+  };
+  typename Vec<E>::type w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid + u * 256 < vecs) w[u] = vload_nt(p + (tid + u * 256) * N);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = tid + u * 256;
+    if (i < vecs) {
+      float f[N];
+      Vec<E>::unpack(w[u], f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] = value(f[e], i * N + e);
+      vstore_nt(q + i * N, Vec<E>::pack(f));
+    }
+  }
+  const int rest = vecs * N + tid;
+  if (rest < n) q[rest] = Vec<E>::round(value(Vec<E>::value(p[rest]), rest));
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxLogitRows = 0x7FFFFFFF;
+constexpr int kMaxSplits = 64;  // pieces of one row: one per lane of join_kernel
+
+// Pieces per row: one while the rows alone give 2048 workgroups (8 per CU),
+// else enough for that, of at least 4096 logits.
+static int row_splits(int64_t T, int64_t V) {
+  int64_t s = ceil_div(2048, T < 1 ? 1 : T);
+  const int64_t most = ceil_div(V, 4096);
+  s = s < most ? s : most;
+  return static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+}
+
+struct LossPlan {
+  float2 *stats, *part;
+  float* coef;
+  size_t bytes;
+};
+
+static LossPlan plan_loss(int64_t T, int64_t V, void* ws) {
+  LossPlan l{};
+  Carver w(ws);
+  l.part = static_cast<float2*>(w.take(row_splits(T, V) > 1 ? T * row_splits(T, V) * sizeof(float2) : 0));
+  l.stats = static_cast<float2*>(w.take(T * sizeof(float2)));
+  l.coef = static_cast<float*>(w.take(T * sizeof(float)));
+  l.bytes = w.used;
+  return l;
+}
+
+static int check_logits(const lora_mat* m) {
+  if (!float_dtype_ok(m->dtype)) return LORA_ERR_DTYPE;
+  if (!valid_dims(m)) return LORA_ERR_SHAPE;
+  if (m->cols > 1 && m->stride_col != 1) return LORA_ERR_STRIDE;
+  if (m->rows > 1 && m->stride_row < m->cols) return LORA_ERR_STRIDE;
+  if (!aligned(m->ptr, elem_size(m->dtype))) return LORA_ERR_STRIDE;
+  if (m->rows > kMaxLogitRows / kMaxSplits || m->cols > 0x7FFFFFFF - 8 * kGradVecs) return LORA_ERR_LIMIT;
+  return LORA_OK;
+}
+
+static int check_workspace(const LossPlan& l, void* ws, size_t bytes) {
+  return !ws || bytes < l.bytes || !aligned(ws, 256) ? LORA_ERR_WORKSPACE : LORA_OK;
+}
+
+static void run_logp(const lora_mat* x, const int32_t* targets, float* logp, float2* stats, const LossPlan& l,
+                     hipStream_t st) {
+  const int64_t T = x->rows;
+  const int V = static_cast<int>(x->cols);
+  const int splits = row_splits(T, V);
+  auto go = [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    const int piece = static_cast<int>(round_up(ceil_div(V, splits), Vec<E>::N));
+    launch(logp_kernel<E>, dim3(T * splits), dim3(256), 0, st, (const E*)e, x->stride_row, targets, V, splits, piece,
+           logp, stats, l.part);
+    if (splits > 1)
+      launch(join_kernel<E>, dim3(ceil_div(T, 4)), dim3(256), 0, st, (const E*)e, x->stride_row, targets, T, V,
+             splits, (const float2*)l.part, logp, stats);
+  };
+  if (x->dtype == LORA_F32)
+    go(static_cast<float*>(x->ptr));
+  else
+    go(static_cast<uint16_t*>(x->ptr));
+}
+
+static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
+  if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;
+  if (dx->dtype != x->dtype) return LORA_ERR_DTYPE;
+  if (int e = check_logits(dx)) return e;
+  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
+  return x->rows * pieces > 0x7FFFFFFF ? LORA_ERR_LIMIT : LORA_OK;
+}
+
+static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* coef,
+                           const float* grad_out, float scale, const lora_mat* dx, hipStream_t st) {
+  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
+  auto go = [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    launch(logit_grad_kernel<E>, dim3(x->rows * pieces), dim3(256), 0, st, (const E*)e, x->stride_row, targets, stats,
+           coef, grad_out, scale, static_cast<int>(x->cols), static_cast<int>(pieces), static_cast<E*>(dx->ptr),
+           dx->stride_row);
+  };
+  if (x->dtype == LORA_F32)
+    go(static_cast<float*>(x->ptr));
+  else
+    go(static_cast<uint16_t*>(x->ptr));
+}
+
+static int check_pref(const int32_t* offsets, int64_t pairs, const float* ref, float beta, float eps,
+                      const float* loss) {
+  if (!offsets || !ref || !loss) return LORA_ERR_NULL;
+  if (pairs < 1 || pairs > (int64_t(1) << 30)) return LORA_ERR_SHAPE;
+  return LORA_OK;
+}
+
+static int check_policy(const lora_policy* p, int64_t T, const float* loss) {
+  if (!p || !loss) return LORA_ERR_NULL;
+  if (T > 0 && (!p->targets || !p->old_logp || !p->advantages || !p->weights)) return LORA_ERR_NULL;
+  if (T > 0 && p->kl_coef != 0.0f && !p->ref_logp) return LORA_ERR_NULL;
+  return LORA_OK;
+}
+
+static PolicyArgs policy_args(const lora_policy* p) {
+  return {p->targets,  p->old_logp,  p->kl_coef != 0.0f ? p->ref_logp : nullptr, p->advantages, p->weights,
+          p->clip_low, p->clip_high, p->kl_coef};
+}
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" size_t lora_loss_workspace_bytes(int64_t T, int64_t V) {
+  if (T < 0 || V < 0 || T > kMaxLogitRows / kMaxSplits || V > 0x7FFFFFFF - 8 * kGradVecs) return 0;
+  return plan_loss(T, V, nullptr).bytes;
+}
+
+extern "C" int lora_token_logp(const lora_mat* logits, const int32_t* targets, float* logp, float* stats,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!logits) return LORA_ERR_NULL;
+  if (int e = check_logits(logits)) return e;
+  const int64_t T = logits->rows;
+  if (T == 0) return LORA_OK;
+  if (!targets || !logp || !stats || (logits->cols > 0 && !logits->ptr)) return LORA_ERR_NULL;
+  const LossPlan l = plan_loss(T, logits->cols, workspace);
+  if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
+  run_logp(logits, targets, logp, reinterpret_cast<float2*>(stats), l, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+extern "C" int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_offsets, int64_t pairs,
+                              const float* ref_logp, float beta, float label_smoothing, float* loss, float* seq_logp,
+                              float* coef, void* stream) {
+  if (int e = check_pref(seq_offsets, pairs, ref_logp, beta, label_smoothing, loss)) return e;
+  if (T < 0) return LORA_ERR_SHAPE;
+  if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
+  if (T > 0 && !logp) return LORA_ERR_NULL;
+  launch(pref_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, seq_offsets, pairs, ref_logp,
+         beta, label_smoothing, loss, seq_logp, coef);
+  return launch_status();
+}
+
+extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const lora_policy* policy, float* loss,
+                                float* coef, void* stream) {
+  if (int e = check_policy(policy, T, loss)) return e;
+  if (T < 0 || V < 0) return LORA_ERR_SHAPE;
+  if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
+  if (T > 0 && !logp) return LORA_ERR_NULL;
+  launch(policy_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, V, policy_args(policy),
+         loss, coef);
+  return launch_status();
+}
+
+extern "C" int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* coef,
+                               const float* grad_out, float scale, const lora_mat* dlogits, void* stream) {
+  if (!logits || !dlogits) return LORA_ERR_NULL;
+  if (int e = check_logits(logits)) return e;
+  if (int e = check_dlogits(logits, dlogits)) return e;
+  if (logits->rows == 0 || logits->cols == 0) return LORA_OK;
+  if (!targets || !stats || !coef || !logits->ptr || !dlogits->ptr) return LORA_ERR_NULL;
+  run_logit_grad(logits, targets, reinterpret_cast<const float2*>(stats), coef, grad_out, scale, dlogits,
+                 static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, const int32_t* seq_offsets,
+                              int64_t pairs, const float* ref_logp, float beta, float label_smoothing,
+                              float grad_scale, float* loss, float* seq_logp, float* logp, const lora_mat* dlogits,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!logits || !dlogits) return LORA_ERR_NULL;
+  if (int e = check_pref(seq_offsets, pairs, ref_logp, beta, label_smoothing, loss)) return e;
+  if (int e = check_logits(logits)) return e;
+  if (int e = check_dlogits(logits, dlogits)) return e;
+  const int64_t T = logits->rows, V = logits->cols;
+  if (T > 0 && (!targets || !logp || (V > 0 && (!logits->ptr || !dlogits->ptr)))) return LORA_ERR_NULL;
+  const LossPlan l = plan_loss(T, V, workspace);
+  if (T > 0)
+    if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
+  auto st = static_cast<hipStream_t>(stream);
+  if (T > 0) run_logp(logits, targets, logp, l.stats, l, st);
+  launch(pref_kernel, dim3(1), dim3(1024), 0, st, (const float*)logp, T, seq_offsets, pairs, ref_logp, beta,
+         label_smoothing, loss, seq_logp, l.coef);
+  if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
+  return launch_status();
+}
+
+extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float grad_scale, float* loss,
+                                float* logp, const lora_mat* dlogits, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  if (!logits || !dlogits) return LORA_ERR_NULL;
+  const int64_t T = logits->rows, V = logits->cols;
+  if (int e = check_policy(policy, T, loss)) return e;
+  if (int e = check_logits(logits)) return e;
+  if (int e = check_dlogits(logits, dlogits)) return e;
+  if (T > 0 && (!logp || (V > 0 && (!logits->ptr || !dlogits->ptr)))) return LORA_ERR_NULL;
+  const LossPlan l = plan_loss(T, V, workspace);
+  if (T > 0)
+    if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
+  auto st = static_cast<hipStream_t>(stream);
+  if (T > 0) run_logp(logits, policy->targets, logp, l.stats, l, st);
+  launch(policy_kernel, dim3(1), dim3(1024), 0, st, (const float*)logp, T, V, policy_args(policy), loss, l.coef);
+  if (T > 0 && V > 0) run_logit_grad(logits, policy->targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
+  return launch_status();
+}

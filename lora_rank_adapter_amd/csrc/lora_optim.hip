@@ -1,0 +1,328 @@
+// AdamW over many tensors in one launch.
+//
+//   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Everything is read and written once: the step is bound by HBM. The tensors
+// are described by a table in device memory (their pointers, and for every
+// chunk of kChunk elements the tensor it belongs to), so that one grid covers
+// all of them whatever their sizes. The states of all tensors are one flat
+// array each; a tensor's states start at a multiple of 256 elements.
+//
+// 8-bit states: 256 elements share a float32 scale, the block's largest
+// magnitude over 448, and each element is an e4m3 code (4 significant bits
+// over 17 binades). The second moment is stored as its square root, which
+// halves its range in binades, and an element above zero never gets the code
+// of zero: the step divides by it, and a zero would leave eps alone there.
+//
+// Kernels:
+//   table_kernel   table entries and the chunks' tensors
+//   begin_kernel   the step count and the constants that depend on it
+//   step_kernel    the update, 256 elements per wave at a time
+
+#include "lora_host.hpp"
+#include "lora_rows.hpp"
+
+namespace lora {
+
+constexpr int kStateBlock = 256;  // elements that share a scale; one wave's step
+constexpr int kChunk = 2048;      // elements of one workgroup
+constexpr int kTableBatch = 48;   // entries passed to one table_kernel launch
+constexpr int64_t kTableMagic = 0x4164616D57303146;
+
+struct TableHead {
+  int64_t magic, elems, tensors, chunks;
+  // written by begin_kernel for each step
+  float lr, alpha, inv_root, decay;
+};
+struct TableEntry {
+  void* param;
+  const void* grad;
+  uint16_t* shadow;
+  int64_t numel, state;  // elements, first element of its states
+  int32_t first_chunk;
+  uint8_t param_bf16, grad_bf16, vec, unused;
+};
+constexpr int64_t kHeadBytes = 256;
+
+struct TableBatch {
+  TableEntry e[kTableBatch];
+};
+
+__device__ __forceinline__ TableEntry* table_entries(void* table) {
+  return reinterpret_cast<TableEntry*>(static_cast<char*>(table) + kHeadBytes);
+}
+__host__ __device__ inline int64_t chunk_map_offset(int64_t n) {
+  return kHeadBytes + (n * (int64_t)sizeof(TableEntry) + 255) / 256 * 256;
+}
+
+__global__ __launch_bounds__(256) void table_kernel(TableBatch batch, int first, int64_t n, int64_t elems,
+                                                    int64_t chunks, void* __restrict__ table) {
+  const TableEntry e = batch.e[blockIdx.x];
+  if (threadIdx.x == 0) {
+    table_entries(table)[first + blockIdx.x] = e;
+    if (first + blockIdx.x == 0) {
+      auto* h = static_cast<TableHead*>(table);
+      h->magic = kTableMagic;
+      h->elems = elems;
+      h->tensors = n;
+      h->chunks = chunks;
+    }
+  }
+  auto* map = reinterpret_cast<int32_t*>(static_cast<char*>(table) + chunk_map_offset(n));
+  const int64_t own = (e.numel + kChunk - 1) / kChunk;
+  for (int64_t i = threadIdx.x; i < own; i += 256) map[e.first_chunk + i] = first + (int)blockIdx.x;
+}
+
+// The constants need powers in float64; one thread computes them once.
+__global__ void begin_kernel(void* table, int32_t* step, double lr, double beta1, double beta2, double decay,
+                             const float* lr_scale) {
+  const int t = *step + 1;
+  *step = t;
+  if (lr_scale != nullptr) lr *= (double)*lr_scale;
+  auto* h = static_cast<TableHead*>(table);
+  h->alpha = static_cast<float>(lr / (1.0 - pow(beta1, (double)t)));
+  h->inv_root = static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, (double)t)));
+  h->decay = static_cast<float>(1.0 - lr * decay);
+}
+
+struct StepArgs {
+  void *m, *v;
+  float *m_scale, *v_scale;
+  const float* grad_scale;
+  float b1, c1, b2, c2, eps;  // c = 1 - b, rounded from float64
+};
+
+struct StepConst {
+  float alpha, inv_root, decay, gs;
+};
+
+__device__ __forceinline__ void adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
+  g *= k.gs;
+  m = a.b1 * m + a.c1 * g;
+  v = a.b2 * v + a.c2 * (g * g);
+  p = p * k.decay - k.alpha * m / (sqrtf(v) * k.inv_root + a.eps);
+}
+
+// four codes of one word as values, and back (rounded to nearest even)
+__device__ __forceinline__ void fp8_values(uint32_t w, float scale, float* f) {
+  f[0] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * scale;
+  f[1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * scale;
+  f[2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * scale;
+  f[3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * scale;
+}
+__device__ __forceinline__ uint32_t fp8_codes(const float* f) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true));
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// x: 4 values of each lane, one block over the wave. Returns the codes.
+__device__ __forceinline__ uint32_t quantise(float* x, bool positive, float* scale) {
+  const float amax = wave_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+  // a block below 1e-30 is stored as zeros (448 / amax stays finite above it)
+  const bool some = amax >= 1e-30f;
+  const float inv = some ? 448.0f / amax : 0.0f;
+  *scale = some ? amax / 448.0f : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q = x[i] * inv;
+    x[i] = positive && q > 0.0f ? fmaxf(q, 0.001953125f) : q;
+  }
+  return fp8_codes(x);
+}
+
+__device__ __forceinline__ void load4(const void* p, bool bf16, int64_t i, bool vec, int count, float* f) {
+  if (vec && count == 4) {
+    const f32x4_t v = bf16 ? Out<uint16_t>::ld4(static_cast<const uint16_t*>(p) + i)
+                           : Out<float>::ld4(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = e < count ? (bf16 ? bf16_value(static_cast<const uint16_t*>(p)[i + e])
+                               : static_cast<const float*>(p)[i + e])
+                       : 0.0f;
+  }
+}
+__device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, bool vec, int count, const float* f) {
+  if (vec && count == 4) {
+    const f32x4_t v = {f[0], f[1], f[2], f[3]};
+    if (bf16)
+      Out<uint16_t>::st4(static_cast<uint16_t*>(p) + i, v);
+    else
+      Out<float>::st4(static_cast<float*>(p) + i, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e >= count) continue;
+      if (bf16)
+        static_cast<uint16_t*>(p)[i + e] = static_cast<uint16_t>(bf16_bits(f[e]));
+      else
+        static_cast<float*>(p)[i + e] = f[e];
+    }
+  }
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
+  const auto* h = static_cast<const TableHead*>(table);
+  // a table of other tensors than the states: leave everything as it is
+  if (h->magic != kTableMagic || h->tensors != n || h->elems != elems || blockIdx.x >= h->chunks) return;
+  const auto* map = reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
+  const TableEntry e = table_entries(table)[map[blockIdx.x]];
+  const StepConst k = {h->alpha, h->inv_root, h->decay, a.grad_scale != nullptr ? *a.grad_scale : 1.0f};
+  const int lane = threadIdx.x & 63;
+  const int64_t chunk = (int64_t)(blockIdx.x - e.first_chunk) * kChunk;
+#pragma unroll
+  for (int it = 0; it < kChunk / (4 * kStateBlock); ++it) {
+    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
+    if (block >= e.numel) break;
+    const int64_t i = block + lane * 4;  // in the tensor
+    const int64_t s = e.state + i;       // in the states
+    const int count = e.numel - i < 4 ? (e.numel - i < 0 ? 0 : (int)(e.numel - i)) : 4;
+    float p[4], g[4], m[4], v[4];
+    load4(e.param, e.param_bf16, i, e.vec, count, p);
+    load4(e.grad, e.grad_bf16, i, e.vec, count, g);
+    if constexpr (BITS == 8) {
+      fp8_values(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s), a.m_scale[s / kStateBlock], m);
+      fp8_values(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s), a.v_scale[s / kStateBlock], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= v[j];
+    } else {
+      load4(a.m, false, s, true, 4, m);
+      load4(a.v, false, s, true, 4, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      adamw(p[j], m[j], v[j], g[j], k, a);
+      // past the tensor's end the states stay zero
+      if (j >= count) m[j] = v[j] = 0.0f;
+    }
+    store4(e.param, e.param_bf16, i, e.vec, count, p);
+    if (e.shadow != nullptr) store4(e.shadow, true, i, e.vec, count, p);
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = sqrtf(v[j]);
+      float ms, vs;
+      const uint32_t mc = quantise(m, false, &ms), vc = quantise(v, true, &vs);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = mc;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = vc;
+      if (lane == 0) {
+        a.m_scale[s / kStateBlock] = ms;
+        a.v_scale[s / kStateBlock] = vs;
+      }
+    } else {
+      store4(a.m, false, s, true, 4, m);
+      store4(a.v, false, s, true, 4, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+struct TableSize {
+  int64_t elems, chunks;
+  size_t bytes;
+};
+
+static int measure(const lora_adamw_tensor* t, int64_t n, TableSize* size) {
+  if (n < 0) return LORA_ERR_SHAPE;
+  if (n > 0x7FFFFF) return LORA_ERR_LIMIT;
+  if (n > 0 && !t) return LORA_ERR_NULL;
+  *size = {};
+  for (int64_t i = 0; i < n; ++i) {
+    if (t[i].numel < 0 || t[i].numel > kMaxOperand / 4) return LORA_ERR_SHAPE;
+    size->elems += round_up(t[i].numel, kStateBlock);
+    size->chunks += ceil_div(t[i].numel, kChunk);
+    if (size->elems > kMaxOperand / 4) return LORA_ERR_SHAPE;
+    if (size->chunks > 0x7FFFFFFF) return LORA_ERR_LIMIT;
+  }
+  size->bytes = static_cast<size_t>(chunk_map_offset(n) + round_up(4 * size->chunks, 256));
+  return LORA_OK;
+}
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" size_t lora_adamw_table_bytes(const lora_adamw_tensor* tensors, int64_t n) {
+  TableSize size;
+  return measure(tensors, n, &size) == LORA_OK ? size.bytes : 0;
+}
+
+extern "C" int64_t lora_adamw_state_elems(const lora_adamw_tensor* tensors, int64_t n) {
+  TableSize size;
+  return measure(tensors, n, &size) == LORA_OK ? size.elems : 0;
+}
+
+extern "C" int lora_adamw_table(const lora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
+                                void* stream) {
+  TableSize size;
+  if (int e = measure(tensors, n, &size)) return e;
+  for (int64_t i = 0; i < n; ++i) {
+    const lora_adamw_tensor& t = tensors[i];
+    if (!float_dtype_ok(t.param_dtype) || !float_dtype_ok(t.grad_dtype)) return LORA_ERR_DTYPE;
+    if (t.shadow && t.param_dtype != LORA_F32) return LORA_ERR_DTYPE;
+    if (t.numel > 0 && (!t.param || !t.grad)) return LORA_ERR_NULL;
+    if (!aligned(t.param, elem_size(t.param_dtype)) || !aligned(t.grad, elem_size(t.grad_dtype)) ||
+        !aligned(t.shadow, 2))
+      return LORA_ERR_STRIDE;
+  }
+  if (size.elems == 0) return LORA_OK;
+  if (!table || table_bytes < size.bytes || !aligned(table, 256)) return LORA_ERR_WORKSPACE;
+  int64_t state = 0, chunk = 0;
+  for (int64_t first = 0; first < n; first += kTableBatch) {
+    TableBatch batch = {};
+    const int count = static_cast<int>(n - first < kTableBatch ? n - first : kTableBatch);
+    for (int i = 0; i < count; ++i) {
+      const lora_adamw_tensor& t = tensors[first + i];
+      // 4 elements of each operand in one access
+      const bool vec = aligned(t.param, 4 * elem_size(t.param_dtype)) && aligned(t.grad, 4 * elem_size(t.grad_dtype)) &&
+                       aligned(t.shadow, 8);
+      batch.e[i] = {t.param,  t.grad, static_cast<uint16_t*>(t.shadow), t.numel, state, static_cast<int32_t>(chunk),
+                    static_cast<uint8_t>(t.param_dtype == LORA_BF16), static_cast<uint8_t>(t.grad_dtype == LORA_BF16),
+                    static_cast<uint8_t>(vec), 0};
+      state += round_up(t.numel, kStateBlock);
+      chunk += ceil_div(t.numel, kChunk);
+    }
+    launch(table_kernel, dim3(count), dim3(256), 0, static_cast<hipStream_t>(stream), batch, static_cast<int>(first),
+           n, size.elems, size.chunks, table);
+  }
+  return launch_status();
+}
+
+extern "C" int lora_adamw_step(const lora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
+                               const lora_adamw_state* state, const lora_adamw_hyper* hyper, void* stream) {
+  TableSize size;
+  if (int e = measure(tensors, n, &size)) return e;
+  if (!state || !hyper) return LORA_ERR_NULL;
+  if (state->bits != 8 && state->bits != 32) return LORA_ERR_DTYPE;
+  if (!state->step) return LORA_ERR_NULL;
+  if (size.elems > 0) {
+    if (!state->m || !state->v || (state->bits == 8 && (!state->m_scale || !state->v_scale))) return LORA_ERR_NULL;
+    if (!aligned(state->m, 16) || !aligned(state->v, 16)) return LORA_ERR_STRIDE;
+    if (!table || table_bytes < size.bytes || !aligned(table, 256)) return LORA_ERR_WORKSPACE;
+  }
+  if (size.elems == 0) return LORA_OK;
+  const StepArgs a = {state->m, state->v, state->m_scale, state->v_scale, hyper->grad_scale,
+                      static_cast<float>(hyper->beta1), static_cast<float>(1.0 - hyper->beta1),
+                      static_cast<float>(hyper->beta2), static_cast<float>(1.0 - hyper->beta2),
+                      static_cast<float>(hyper->eps)};
+  auto st = static_cast<hipStream_t>(stream);
+  launch(begin_kernel, dim3(1), dim3(1), 0, st, table, state->step, hyper->lr, hyper->beta1, hyper->beta2,
+         hyper->weight_decay, hyper->lr_scale);
+  if (state->bits == 8)
+    launch(step_kernel<8>, dim3(size.chunks), dim3(256), 0, st, table, n, size.elems, a);
+  else
+    launch(step_kernel<32>, dim3(size.chunks), dim3(256), 0, st, table, n, size.elems, a);
+  return launch_status();
+}

@@ -1,0 +1,314 @@
+"""Binding of the operators of a training step around the adapter linears:
+embedding lookup and gradient, the losses on next-token logits, AdamW.
+
+As in ``ops``: argument marshalling only. Vectors (ids, targets, log
+probabilities, ...) are checked here for dtype, length and layout, since the
+library takes them as bare pointers; matrices are checked by the library.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import LoraAdamwHyper, LoraAdamwState, LoraAdamwTensor, LoraPolicy, check
+from .ops import _dtype_code, _ptr, _stream, mat
+
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _vector(name: str, t: torch.Tensor, n: int, dtype: torch.dtype, device: torch.device) -> int:
+    """The address of a contiguous vector of n elements of dtype on device."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _queue(device: torch.device):
+    """torch's current stream on a GPU; tensors elsewhere are refused before their addresses get there."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, got {device}")
+    return _stream(device)
+
+
+def _matrix(name: str, t: torch.Tensor, device: torch.device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return ctypes.byref(mat(t))
+
+
+def _given(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+# ---------------------------------------------------------------------------
+# embedding
+# ---------------------------------------------------------------------------
+
+def lora_embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+               dtype: torch.dtype | None = None) -> torch.Tensor:
+    """out[t] = scale * table[ids[t]] (zeros for ids outside [0, V)). ids: int32 [T], table: V x D. Returns out
+    [T x D]: the given tensor, else a new one of `dtype` (default the table's; float32, or bfloat16 with a
+    bfloat16 table)."""
+    lib = _lib.load()
+    T, dev = ids.numel(), table.device
+    p = _vector("ids", ids, T, _I32, dev)
+    if out is None:
+        out = torch.empty((T, table.shape[1]), dtype=dtype or table.dtype, device=dev)
+    elif out.shape[0] != T:
+        raise ValueError(f"out has {out.shape[0]} rows for {T} ids")
+    check("lora_embed", lib.lora_embed(p, _matrix("table", table, dev), float(scale), _matrix("out", out, dev),
+                                       _queue(dev)))
+    return out
+
+
+def lora_embed_grad(ids: torch.Tensor, dy: torch.Tensor, num_rows: int, scale: float = 1.0,
+                    dtable: torch.Tensor | None = None, accumulate: bool = False,
+                    workspace: torch.Tensor | None = None, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """dtable[v] = scale * sum of dy[t] over the tokens with ids[t] = v. ids: int32 [T], dy: T x D. Returns dtable
+    [num_rows x D]: the given tensor (overwritten, or with accumulate added to), else a new one of `dtype`
+    (float32, or bfloat16 with bfloat16 dy)."""
+    lib = _lib.load()
+    T, D = dy.shape
+    dev = dy.device
+    p = _vector("ids", ids, T, _I32, dev)
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dtable to add to")
+        dtable = torch.empty((num_rows, D), dtype=dtype, device=dev)
+    elif dtable.shape[0] != num_rows:
+        raise ValueError(f"dtable has {dtable.shape[0]} rows, expected {num_rows}")
+    ws, nbytes = _given(workspace, lib.lora_embed_grad_workspace_bytes(T, num_rows, D), dev)
+    check("lora_embed_grad", lib.lora_embed_grad(p, _matrix("dy", dy, dev), float(scale),
+                                                 _matrix("dtable", dtable, dev), int(bool(accumulate)), _ptr(ws),
+                                                 nbytes, _queue(dev)))
+    return dtable
+
+
+# ---------------------------------------------------------------------------
+# losses
+# ---------------------------------------------------------------------------
+
+def lora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
+                    workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Log probabilities of the targets (0 where a target lies outside [0, V)) and the rows' softmax statistics.
+    logits: T x V, targets: int32 [T]. Returns (logp [T], stats [T x 2]: the largest logit m and the sum of
+    exp(x - m)), both float32."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev = logits.device
+    y = _vector("targets", targets, T, _I32, dev)
+    logp = torch.empty(T, dtype=_F32, device=dev)
+    stats = torch.empty((T, 2), dtype=_F32, device=dev)
+    ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
+    check("lora_token_logp", lib.lora_token_logp(_matrix("logits", logits, dev), y, _ptr(logp), _ptr(stats), _ptr(ws),
+                                                 nbytes, _queue(dev)))
+    return logp, stats
+
+
+def _pairs(seq_offsets: torch.Tensor) -> int:
+    n = seq_offsets.numel() - 1
+    if n < 2 or n % 2:
+        raise ValueError(f"seq_offsets must hold 2 * pairs + 1 offsets, got {n + 1}")
+    return n // 2
+
+
+def lora_pref_loss(logp: torch.Tensor, seq_offsets: torch.Tensor, ref_logp: torch.Tensor, beta: float,
+                   label_smoothing: float = 0.0) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Preference loss of paired sequences from their tokens' log probabilities. seq_offsets: int32
+    [2 * pairs + 1], sequences 2p (preferred) and 2p + 1 of pair p; ref_logp: float32 [2 * pairs].
+    Returns (loss [], seq_logp [2 * pairs], coef [T]: d loss / d logp)."""
+    lib = _lib.load()
+    T, dev, pairs = logp.numel(), logp.device, _pairs(seq_offsets)
+    loss = torch.empty((), dtype=_F32, device=dev)
+    seq = torch.empty(2 * pairs, dtype=_F32, device=dev)
+    coef = torch.empty(T, dtype=_F32, device=dev)
+    check("lora_pref_loss", lib.lora_pref_loss(
+        _vector("logp", logp, T, _F32, dev), T, _vector("seq_offsets", seq_offsets, 2 * pairs + 1, _I32, dev), pairs,
+        _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), _ptr(loss),
+        _ptr(seq), _ptr(coef), _queue(dev)))
+    return loss, seq, coef
+
+
+def _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev) -> LoraPolicy:
+    if kl_coef != 0.0 and ref_logp is None:
+        raise ValueError("kl_coef needs ref_logp")
+    return LoraPolicy(_vector("targets", targets, T, _I32, dev), _vector("old_logp", old_logp, T, _F32, dev),
+                      None if ref_logp is None else _vector("ref_logp", ref_logp, T, _F32, dev),
+                      _vector("advantages", advantages, T, _F32, dev), _vector("weights", weights, T, _F32, dev),
+                      float(clip_low), float(clip_high), float(kl_coef))
+
+
+def lora_policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_logp: torch.Tensor,
+                     advantages: torch.Tensor, weights: torch.Tensor, clip_low: float, clip_high: float,
+                     ref_logp: torch.Tensor | None = None,
+                     kl_coef: float = 0.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """Clipped policy loss with a KL term from the tokens' log probabilities (all vectors float32 [T], targets
+    int32; a target outside [0, vocab) masks its token). Returns (loss [], coef [T]: d loss / d logp)."""
+    lib = _lib.load()
+    T, dev = logp.numel(), logp.device
+    args = _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev)
+    loss = torch.empty((), dtype=_F32, device=dev)
+    coef = torch.empty(T, dtype=_F32, device=dev)
+    check("lora_policy_loss", lib.lora_policy_loss(_vector("logp", logp, T, _F32, dev), T, int(vocab),
+                                                   ctypes.byref(args), _ptr(loss), _ptr(coef), _queue(dev)))
+    return loss, coef
+
+
+def lora_logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, coef: torch.Tensor,
+                    grad_out: torch.Tensor | None = None, scale: float = 1.0,
+                    dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits[t] = scale * grad_out * coef[t] * (one at targets[t] - softmax(logits[t])). stats from
+    lora_token_logp on the same logits and targets, grad_out: float32 [] on the device or None. Returns dlogits
+    [T x V] of the logits' dtype: the given tensor (it may be the logits), else a new one."""
+    lib = _lib.load()
+    T = logits.shape[0]
+    dev = logits.device
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    check("lora_logit_grad", lib.lora_logit_grad(
+        _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
+        _vector("stats", stats, 2 * T, _F32, dev), _vector("coef", coef, T, _F32, dev),
+        None if grad_out is None else _vector("grad_out", grad_out, 1, _F32, dev), float(scale),
+        _matrix("dlogits", dlogits, dev), _queue(dev)))
+    return dlogits
+
+
+def lora_pref_step(logits: torch.Tensor, targets: torch.Tensor, seq_offsets: torch.Tensor, ref_logp: torch.Tensor,
+                   beta: float, label_smoothing: float = 0.0, grad_scale: float = 1.0,
+                   dlogits: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Preference loss and the gradient of its logits in one call (see lora_pref_loss, lora_logit_grad). Returns
+    (loss [], seq_logp [2 * pairs], logp [T], dlogits [T x V], times grad_scale)."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev, pairs = logits.device, _pairs(seq_offsets)
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    loss = torch.empty((), dtype=_F32, device=dev)
+    seq = torch.empty(2 * pairs, dtype=_F32, device=dev)
+    logp = torch.empty(T, dtype=_F32, device=dev)
+    ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
+    check("lora_pref_step", lib.lora_pref_step(
+        _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
+        _vector("seq_offsets", seq_offsets, 2 * pairs + 1, _I32, dev), pairs,
+        _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), float(grad_scale),
+        _ptr(loss), _ptr(seq), _ptr(logp), _matrix("dlogits", dlogits, dev), _ptr(ws), nbytes, _queue(dev)))
+    return loss, seq, logp, dlogits
+
+
+def lora_policy_step(logits: torch.Tensor, targets: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                     weights: torch.Tensor, clip_low: float, clip_high: float, ref_logp: torch.Tensor | None = None,
+                     kl_coef: float = 0.0, grad_scale: float = 1.0, dlogits: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """Policy loss and the gradient of its logits in one call (see lora_policy_loss, lora_logit_grad). Returns
+    (loss [], logp [T], dlogits [T x V], times grad_scale)."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev = logits.device
+    args = _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev)
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
+    loss = torch.empty((), dtype=_F32, device=dev)
+    logp = torch.empty(T, dtype=_F32, device=dev)
+    ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
+    check("lora_policy_step", lib.lora_policy_step(
+        _matrix("logits", logits, dev), ctypes.byref(args), float(grad_scale), _ptr(loss), _ptr(logp),
+        _matrix("dlogits", dlogits, dev), _ptr(ws), nbytes, _queue(dev)))
+    return loss, logp, dlogits
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+
+class AdamW:
+    """AdamW over many tensors, one launch per step (and one for its constants).
+
+    params: contiguous float32 or bfloat16 tensors, updated in place; grads: their gradients in the caller's
+    buffers (float32 or bfloat16; the ones that lora_bwd_dx_da and lora_bwd_db write); shadows: None, or for each
+    param None or a bfloat16 tensor that receives a float32 param's new value. The object holds these tensors and
+    a device table of their addresses; `bind` replaces the gradients, `step` refuses tensors whose memory moved.
+
+    state_bits 32 keeps both moments in float32, 8 as e4m3 codes with a float32 scale for every 256 elements.
+    state: a dict of the tensors step, m, v (and m_scale, v_scale with 8 bits) to go on from; they are used in
+    place. The new ones are zeros. All of it is in `self.state`, the layout in include/lora.h.
+    """
+
+    def __init__(self, params, grads, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state_bits: int = 32, state: dict | None = None, shadows=None):
+        self.params, self.lr, self.betas, self.eps, self.weight_decay = list(params), lr, betas, eps, weight_decay
+        self.state_bits = state_bits
+        self.shadows = [None] * len(self.params) if shadows is None else list(shadows)
+        if not self.params:
+            raise ValueError("AdamW needs a parameter")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if len(self.shadows) != len(self.params):
+            raise ValueError(f"{len(self.shadows)} shadows for {len(self.params)} params")
+        self._lib = _lib.load()
+        self.device = self.params[0].device
+        self.bind(grads)
+        n = self._lib.lora_adamw_state_elems(self._tensors, len(self.params))
+        codes = torch.float8_e4m3fn if state_bits == 8 else _F32
+        want = {"step": (1, _I32), "m": (n, codes), "v": (n, codes)}
+        if state_bits == 8:
+            want.update(m_scale=(n // 256, _F32), v_scale=(n // 256, _F32))
+        if state is None:
+            state = {k: torch.zeros(c, dtype=_F32 if d is codes else d, device=self.device).to(d)
+                     for k, (c, d) in want.items()}
+        if set(state) != set(want):
+            raise ValueError(f"state must hold {sorted(want)}, got {sorted(state)}")
+        self.state = dict(state)
+        at = {k: _vector(k, self.state[k], c, d, self.device) for k, (c, d) in want.items()}
+        self._addresses_of_state = at
+        self._state = LoraAdamwState(state_bits, 0, at["m"] or None, at["v"] or None, at.get("m_scale"),
+                                     at.get("v_scale"), at["step"])
+
+    def bind(self, grads) -> None:
+        """Takes these gradients from now on (writes the device table on the current stream)."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} grads for {len(self.params)} params")
+        tensors = (LoraAdamwTensor * len(grads))()
+        for i, (p, g, s) in enumerate(zip(self.params, grads, self.shadows)):
+            for name, t in (("param", p), ("grad", g), ("shadow", s)):
+                if t is None and name == "shadow":
+                    continue
+                if t.device != self.device or not t.is_contiguous() or t.numel() != p.numel():
+                    raise ValueError(f"{name} {i} must be contiguous on {self.device} with {p.numel()} elements, "
+                                     f"got {tuple(t.shape)} on {t.device}")
+            if s is not None and s.dtype is not torch.bfloat16:
+                raise ValueError(f"shadow {i} must be bfloat16, got {s.dtype}")
+            tensors[i] = LoraAdamwTensor(p.data_ptr() or None, g.data_ptr() or None,
+                                         None if s is None else s.data_ptr() or None, p.numel(), _dtype_code(p),
+                                         _dtype_code(g))
+        need = self._lib.lora_adamw_table_bytes(tensors, len(grads))
+        table = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
+        check("lora_adamw_table", self._lib.lora_adamw_table(tensors, len(grads), _ptr(table), need,
+                                                             _queue(self.device)))
+        self.grads, self._tensors, self._table, self._table_bytes = grads, tensors, table, need
+        self._held = self.params + grads + [s for s in self.shadows if s is not None]
+        self._addresses = [t.data_ptr() for t in self._held]
+
+    def step(self, lr_scale: torch.Tensor | None = None, grad_scale: torch.Tensor | None = None) -> None:
+        """One step on the current stream. lr_scale, grad_scale: None or float32 [] tensors on the device that
+        multiply lr and every gradient (a schedule, a clipping factor; read when the step runs)."""
+        if [t.data_ptr() for t in self._held] != self._addresses:
+            raise ValueError("a bound tensor's memory moved: bind the gradients again")
+        if any(self.state[k].data_ptr() != a for k, a in self._addresses_of_state.items()):
+            raise ValueError("a state tensor was replaced: copy into it instead")
+        dev = self.device
+        hyper = LoraAdamwHyper(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                               None if lr_scale is None else _vector("lr_scale", lr_scale, 1, _F32, dev),
+                               None if grad_scale is None else _vector("grad_scale", grad_scale, 1, _F32, dev))
+        check("lora_adamw_step", self._lib.lora_adamw_step(self._tensors, len(self.params), _ptr(self._table),
+                                                           self._table_bytes, ctypes.byref(self._state),
+                                                           ctypes.byref(hyper), _queue(dev)))

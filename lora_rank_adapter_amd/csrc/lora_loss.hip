@@ -100,10 +100,18 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
     for (int u = 0; u < U; ++u) Vec<E>::unpack(w[u], f + u * N);
     add_values<U * N>(r, f);
   }
-  for (; i < vecs; i += 256) {
-    float f[N];
-    Vec<E>::unpack(vload_nt(p + (int64_t)i * N), f);
-    add_values<N>(r, f);
+  // at most U - 1 more, all loaded before the first is used
+  typename Vec<E>::type w[U - 1];
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (i + u * 256 < vecs) w[u] = vload_nt(p + (int64_t)(i + u * 256) * N);
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u) {
+    if (i + u * 256 < vecs) {
+      float f[N];
+      Vec<E>::unpack(w[u], f);
+      add_values<N>(r, f);
+    }
   }
   if (tid < n - vecs * N) {
     const float f = Vec<E>::value(p[vecs * N + tid]);
@@ -123,28 +131,50 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   }
 }
 
+// The pieces of a row's statistics, joined by one wave: what remains of the
+// softmax once logp_kernel has written `splits` pieces of each row (at most one per lane).
 template <class E>
-__global__ __launch_bounds__(256) void join_kernel(const E* __restrict__ x, int64_t stride,
-                                                   const int32_t* __restrict__ targets, int64_t T, int V, int splits,
-                                                   const float2* __restrict__ part, float* __restrict__ logp,
-                                                   float2* __restrict__ stats) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
-  const int lane = threadIdx.x & 63;
-  if (row >= T) return;
-  const int y = targets[row];
-  if (y < 0 || y >= V) {
+struct RowPieces {
+  const E* x;
+  int64_t stride;
+  const int32_t* targets;
+  int V, splits;
+  const float2* part;
+  float2* stats;
+};
+
+template <class E>
+__device__ __forceinline__ void join_row(const RowPieces<E>& a, int64_t row, int lane, float* logp) {
+  const int y = a.targets[row];
+  if (y < 0 || y >= a.V) {
     if (lane == 0) {
       logp[row] = 0.0f;
-      stats[row] = make_float2(0.0f, 1.0f);
+      a.stats[row] = make_float2(0.0f, 1.0f);
     }
     return;
   }
-  const float2 v = lane < splits ? part[row * splits + lane] : make_float2(-INFINITY, 0.0f);
+  const float2 v = lane < a.splits ? a.part[row * a.splits + lane] : make_float2(-INFINITY, 0.0f);
+  const float hit = Vec<E>::value(a.x[row * a.stride + y]);
   const MaxSum r = wave_join(MaxSum{v.x, v.y});
   if (lane == 0) {
-    logp[row] = target_logp(Vec<E>::value(x[row * stride + y]), r);
-    stats[row] = make_float2(r.m, r.s);
+    logp[row] = target_logp(hit, r);
+    a.stats[row] = make_float2(r.m, r.s);
   }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void join_kernel(RowPieces<E> a, int64_t T, float* __restrict__ logp) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  if (row < T) join_row(a, row, threadIdx.x & 63, logp);
+}
+
+// The same in a workgroup of 1024 that goes on with the log probabilities.
+template <class E>
+__device__ __forceinline__ void join_rows(const RowPieces<E>& a, int64_t T, float* logp) {
+  if (a.part == nullptr) return;
+#pragma unroll 4
+  for (int64_t row = wave_id(); row < T; row += 16) join_row(a, row, threadIdx.x & 63, logp);
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
@@ -167,12 +197,14 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // eps - sigmoid(-z). Sequence sums and z are float64: z is a small
 // difference of long sums. One wave per pair; its two sequences' tokens get
 // the coefficients beta * dz / pairs and minus that.
-__global__ __launch_bounds__(1024) void pref_kernel(const float* __restrict__ logp, int64_t T,
+template <class E>
+__global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* logp, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
                                                     const float* __restrict__ ref, float beta, float eps,
                                                     float* __restrict__ loss, float* __restrict__ seq_logp,
                                                     float* __restrict__ coef) {
   __shared__ double lds[16];
+  join_rows(pieces, T, logp);
   const int lane = threadIdx.x & 63;
   auto offset = [&](int64_t i) -> int64_t {
     const int64_t o = offsets[i];
@@ -235,10 +267,12 @@ __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, f
   return make_float2(w * l, w * d);
 }
 
-__global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ logp, int64_t T, int64_t V,
+template <class E>
+__global__ __launch_bounds__(1024) void policy_kernel(RowPieces<E> pieces, float* logp, int64_t T, int64_t V,
                                                       PolicyArgs a, float* __restrict__ loss,
                                                       float* __restrict__ coef) {
   __shared__ double lds[16];
+  join_rows(pieces, T, logp);
   double sum = 0.0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int y = a.targets[t];
@@ -247,6 +281,128 @@ __global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ 
     sum += v.x;
     if (coef != nullptr) coef[t] = v.y;
   }
+  sum = block_sum(sum, lds);
+  if (threadIdx.x == 0) *loss = static_cast<float>(sum);
+}
+
+// ---------------------------------------------------------------------------
+// policy step: a token's coefficient needs nothing but its own row, so one
+// workgroup takes a row from its statistics to its gradient. The row's last
+// H vectors per lane stay in registers between the two passes; the others are
+// read again, the most recently read first.
+// ---------------------------------------------------------------------------
+template <class E, int WAVES, int H>
+__global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, int64_t stride, int V, PolicyArgs a,
+                                                                   float scale, float* __restrict__ logp,
+                                                                   float* __restrict__ terms, E* dx,
+                                                                   int64_t dx_stride) {
+  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
+  __shared__ MaxSum waves[WAVES];
+  __shared__ float shared_coef;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int y = a.targets[row];
+  const int vecs = V / N;
+  const int rest = vecs * N + tid;  // the row's last elements, one per lane
+  // dx may be x: no restrict on it, and a vector is stored by the lane that loaded it
+  const E* p = x + row * stride;
+  E* q = dx + row * dx_stride;
+  if (y < 0 || y >= V) {
+    const typename Vec<E>::type zero = {0u, 0u, 0u, 0u};
+    for (int i = tid; i < vecs; i += THREADS) vstore_nt(q + (int64_t)i * N, zero);
+    if (rest < V) q[rest] = Vec<E>::round(0.0f);
+    if (tid == 0) logp[row] = terms[row] = 0.0f;
+    return;
+  }
+  const int body = vecs > H * THREADS ? vecs - H * THREADS : 0;
+  MaxSum r{-INFINITY, 0.0f};
+  int i = tid;
+  for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
+    float f[U * N];
+    typename Vec<E>::type w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = vload(p + (int64_t)(i + u * THREADS) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) Vec<E>::unpack(w[u], f + u * N);
+    add_values<U * N>(r, f);
+  }
+  for (; i < body; i += THREADS) {
+    float f[N];
+    Vec<E>::unpack(vload(p + (int64_t)i * N), f);
+    add_values<N>(r, f);
+  }
+  typename Vec<E>::type held[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (body + tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(body + tid + h * THREADS) * N);
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (body + tid + h * THREADS < vecs) {
+      float f[N];
+      Vec<E>::unpack(held[h], f);
+      add_values<N>(r, f);
+    }
+  }
+  float last = 0.0f;
+  if (rest < V) {
+    last = Vec<E>::value(p[rest]);
+    add_values<1>(r, &last);
+  }
+  r = wave_join(r);
+  if ((tid & 63) == 0) waves[tid >> 6] = r;
+  __syncthreads();
+  r = waves[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) r = join(r, waves[w]);
+  if (tid == 0) {
+    const float lp = target_logp(Vec<E>::value(p[y]), r);
+    const float2 v = policy_token(a, row, lp);
+    logp[row] = lp;
+    terms[row] = v.x;
+    shared_coef = v.y * scale;
+  }
+  __syncthreads();
+  // the second pass unpacks the held vectors anew: their float32 values would take twice the registers
+#pragma unroll
+  for (int h = 0; h < H; ++h) asm volatile("" : "+v"(held[h]));
+  const float c = shared_coef, cs = -c / r.s, m = at_max(r.m);
+  auto grad = [&](typename Vec<E>::type w, int j) {
+    float f[N];
+    Vec<E>::unpack(w, f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = cs * exp2_raw((f[e] - m) * kLog2e);
+    if (static_cast<unsigned>(y - j) < N) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (j + e == y) f[e] += c;
+    }
+    vstore_nt(q + j, Vec<E>::pack(f));
+  };
+  if (rest < V) {
+    const float g = cs * exp2_raw((last - m) * kLog2e);
+    q[rest] = Vec<E>::round(rest == y ? g + c : g);
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (body + tid + h * THREADS < vecs) grad(held[h], (body + tid + h * THREADS) * N);
+  // the lane's vectors of the body, last first
+  i = tid < body ? tid + (body - 1 - tid) / THREADS * THREADS : -1;
+  for (; i - (U - 1) * THREADS >= 0; i -= U * THREADS) {
+    typename Vec<E>::type w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(i - u * THREADS) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) grad(w[u], (i - u * THREADS) * N);
+  }
+  for (; i >= 0; i -= THREADS) grad(vload_nt(p + (int64_t)i * N), i * N);
+}
+
+__global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ terms, int64_t T,
+                                                   float* __restrict__ loss) {
+  __shared__ double lds[16];
+  double sum = 0.0;
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < T; t += 1024) sum += terms[t];
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) *loss = static_cast<float>(sum);
 }
@@ -285,10 +441,7 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t str
   const float2 st = stats[row];
   const float m = at_max(st.x), cs = c / st.y;
   const int hit = y - lo;
-  auto value = [&](float v, int j) {
-    const float g = -cs * exp2_raw((v - m) * kLog2e);
-    return j == hit ? g + c : g;
-  };
+  auto value = [&](float v) { return -cs * exp2_raw((v - m) * kLog2e); };
   typename Vec<E>::type w[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -300,12 +453,20 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t str
       float f[N];
       Vec<E>::unpack(w[u], f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = value(f[e], i * N + e);
+      for (int e = 0; e < N; ++e) f[e] = value(f[e]);
+      if (static_cast<unsigned>(hit - i * N) < N) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (i * N + e == hit) f[e] += c;
+      }
       vstore_nt(q + i * N, Vec<E>::pack(f));
     }
   }
   const int rest = vecs * N + tid;
-  if (rest < n) q[rest] = Vec<E>::round(value(Vec<E>::value(p[rest]), rest));
+  if (rest < n) {
+    const float g = value(Vec<E>::value(p[rest]));
+    q[rest] = Vec<E>::round(rest == hit ? g + c : g);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -354,25 +515,47 @@ static int check_workspace(const LossPlan& l, void* ws, size_t bytes) {
   return !ws || bytes < l.bytes || !aligned(ws, 256) ? LORA_ERR_WORKSPACE : LORA_OK;
 }
 
+// f with a null pointer of the logits' element type
+template <class F>
+static void by_type(const lora_mat* x, F f) {
+  if (x->dtype == LORA_F32)
+    f(static_cast<float*>(nullptr));
+  else
+    f(static_cast<uint16_t*>(nullptr));
+}
+
+template <class E>
+static RowPieces<E> row_pieces(const lora_mat* x, const int32_t* targets, float2* stats, const LossPlan& l) {
+  return {static_cast<const E*>(x->ptr), x->stride_row, targets, static_cast<int>(x->cols), row_splits(x->rows, x->cols),
+          l.part, stats};
+}
+
+// Statistics of the rows, or of their pieces.
 static void run_logp(const lora_mat* x, const int32_t* targets, float* logp, float2* stats, const LossPlan& l,
                      hipStream_t st) {
-  const int64_t T = x->rows;
   const int V = static_cast<int>(x->cols);
-  const int splits = row_splits(T, V);
-  auto go = [&](auto* e) {
+  const int splits = row_splits(x->rows, V);
+  by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
     const int piece = static_cast<int>(round_up(ceil_div(V, splits), Vec<E>::N));
-    launch(logp_kernel<E>, dim3(T * splits), dim3(256), 0, st, (const E*)e, x->stride_row, targets, V, splits, piece,
-           logp, stats, l.part);
-    if (splits > 1)
-      launch(join_kernel<E>, dim3(ceil_div(T, 4)), dim3(256), 0, st, (const E*)e, x->stride_row, targets, T, V,
-             splits, (const float2*)l.part, logp, stats);
-  };
-  if (x->dtype == LORA_F32)
-    go(static_cast<float*>(x->ptr));
-  else
-    go(static_cast<uint16_t*>(x->ptr));
+    launch(logp_kernel<E>, dim3(x->rows * splits), dim3(256), 0, st, (const E*)x->ptr, x->stride_row, targets, V,
+           splits, piece, logp, stats, l.part);
+  });
 }
+
+static void run_join(const lora_mat* x, const int32_t* targets, float* logp, float2* stats, const LossPlan& l,
+                     hipStream_t st) {
+  if (row_splits(x->rows, x->cols) == 1) return;
+  by_type(x, [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    launch(join_kernel<E>, dim3(ceil_div(x->rows, 4)), dim3(256), 0, st, row_pieces<E>(x, targets, stats, l), x->rows,
+           logp);
+  });
+}
+
+// Few rows are joined by the loss's own workgroup, which saves a launch (about
+// 3 us each); beyond 256 rows the many waves of join_kernel are faster.
+static bool join_in_loss(int64_t T, int64_t V) { return row_splits(T, V) > 1 && T <= 256; }
 
 static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;
@@ -385,16 +568,36 @@ static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
 static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* coef,
                            const float* grad_out, float scale, const lora_mat* dx, hipStream_t st) {
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  auto go = [&](auto* e) {
+  by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(logit_grad_kernel<E>, dim3(x->rows * pieces), dim3(256), 0, st, (const E*)e, x->stride_row, targets, stats,
-           coef, grad_out, scale, static_cast<int>(x->cols), static_cast<int>(pieces), static_cast<E*>(dx->ptr),
-           dx->stride_row);
-  };
-  if (x->dtype == LORA_F32)
-    go(static_cast<float*>(x->ptr));
-  else
-    go(static_cast<uint16_t*>(x->ptr));
+    launch(logit_grad_kernel<E>, dim3(x->rows * pieces), dim3(256), 0, st, (const E*)x->ptr, x->stride_row, targets,
+           stats, coef, grad_out, scale, static_cast<int>(x->cols), static_cast<int>(pieces),
+           static_cast<E*>(dx->ptr), dx->stride_row);
+  });
+}
+
+// The policy step by rows (one workgroup takes a row from its statistics to
+// its gradient, one read of it from HBM) or split (statistics, then the
+// gradient, many workgroups to a row). A row of 128256 bfloat16 keeps one CU
+// busy for 20 us: 40 of them take 20 us by rows and 16 split, 128 of them 25
+// and 28, 8192 of them 737 and 1046; a row of 32000 takes 10 us either way.
+static bool policy_by_rows(int64_t T, int64_t V) { return T == 0 || T >= 128 || V <= 49152; }
+
+static void run_policy_rows(const lora_mat* x, const PolicyArgs& a, float scale, float* logp, float* terms,
+                            const lora_mat* dx, hipStream_t st) {
+  const int V = static_cast<int>(x->cols);
+  by_type(x, [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    const int vecs = V / Vec<E>::N;
+    // 8192 rows of bfloat16 by 4, 8 and 16 waves: 4000 columns 28, 41, 82 us; 11000: 66, 67, 110;
+    // 32000: 193, 170, 192; 64000: 401, 374, 345; 128256: 839, 798, 737
+    const int waves = vecs <= 1536 ? 4 : vecs <= 6144 ? 8 : 16;
+    auto* kernel = waves == 4   ? policy_row_kernel<E, 4, 6>
+                   : waves == 8 ? policy_row_kernel<E, 8, 6>
+                                : policy_row_kernel<E, 16, 6>;
+    launch(kernel, dim3(x->rows), dim3(64 * waves), 0, st, (const E*)x->ptr, x->stride_row, V, a, scale, logp, terms,
+           static_cast<E*>(dx->ptr), dx->stride_row);
+  });
 }
 
 static int check_pref(const int32_t* offsets, int64_t pairs, const float* ref, float beta, float eps,
@@ -434,7 +637,9 @@ extern "C" int lora_token_logp(const lora_mat* logits, const int32_t* targets, f
   if (!targets || !logp || !stats || (logits->cols > 0 && !logits->ptr)) return LORA_ERR_NULL;
   const LossPlan l = plan_loss(T, logits->cols, workspace);
   if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
-  run_logp(logits, targets, logp, reinterpret_cast<float2*>(stats), l, static_cast<hipStream_t>(stream));
+  auto st = static_cast<hipStream_t>(stream);
+  run_logp(logits, targets, logp, reinterpret_cast<float2*>(stats), l, st);
+  run_join(logits, targets, logp, reinterpret_cast<float2*>(stats), l, st);
   return launch_status();
 }
 
@@ -445,8 +650,8 @@ extern "C" int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_o
   if (T < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(pref_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, seq_offsets, pairs, ref_logp,
-         beta, label_smoothing, loss, seq_logp, coef);
+  launch(pref_kernel<float>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
+         const_cast<float*>(logp), T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss, seq_logp, coef);
   return launch_status();
 }
 
@@ -456,8 +661,8 @@ extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const l
   if (T < 0 || V < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(policy_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, V, policy_args(policy),
-         loss, coef);
+  launch(policy_kernel<float>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
+         const_cast<float*>(logp), T, V, policy_args(policy), loss, coef);
   return launch_status();
 }
 
@@ -488,8 +693,14 @@ extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, co
     if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
   if (T > 0) run_logp(logits, targets, logp, l.stats, l, st);
-  launch(pref_kernel, dim3(1), dim3(1024), 0, st, (const float*)logp, T, seq_offsets, pairs, ref_logp, beta,
-         label_smoothing, loss, seq_logp, l.coef);
+  const bool join = join_in_loss(T, V);
+  if (T > 0 && !join) run_join(logits, targets, logp, l.stats, l, st);
+  by_type(logits, [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    launch(pref_kernel<E>, dim3(1), dim3(1024), 0, st,
+           join ? row_pieces<E>(logits, targets, l.stats, l) : RowPieces<E>{}, logp, T, seq_offsets, pairs, ref_logp,
+           beta, label_smoothing, loss, seq_logp, l.coef);
+  });
   if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
 }
@@ -507,8 +718,19 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
   if (T > 0)
     if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
-  if (T > 0) run_logp(logits, policy->targets, logp, l.stats, l, st);
-  launch(policy_kernel, dim3(1), dim3(1024), 0, st, (const float*)logp, T, V, policy_args(policy), loss, l.coef);
-  if (T > 0 && V > 0) run_logit_grad(logits, policy->targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
+  const PolicyArgs a = policy_args(policy);
+  if (policy_by_rows(T, V)) {
+    if (T > 0) run_policy_rows(logits, a, grad_scale, logp, l.coef, dlogits, st);
+    launch(sum_kernel, dim3(1), dim3(1024), 0, st, (const float*)l.coef, T, loss);
+    return launch_status();
+  }
+  // so few and such long rows are always in pieces
+  run_logp(logits, a.targets, logp, l.stats, l, st);
+  by_type(logits, [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    launch(policy_kernel<E>, dim3(1), dim3(1024), 0, st, row_pieces<E>(logits, a.targets, l.stats, l), logp, T, V, a,
+           loss, l.coef);
+  });
+  run_logit_grad(logits, a.targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
 }

@@ -12,7 +12,7 @@
 // inside a run; merge_kernel adds the pieces of the ids that span runs.
 //
 // Kernels:
-//   embed_kernel   rows gathered, scaled and stored, 8 elements per lane
+//   embed_kernel   rows gathered, scaled and stored
 //   sort_kernel    stable counting sort of the tokens by id, one launch
 //   grad_kernel    sums of each run's ids, zeros of the rows without tokens
 //   merge_kernel   pieces of an id added in the order of their runs
@@ -22,13 +22,37 @@
 
 namespace lora {
 
-constexpr int kItem = 8;  // elements of a row that one lane handles at a time
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
 
-template <class E, class O>
+// A lane handles one 16-byte vector of the output's row at a time and U of
+// them, `lanes` apart, all loaded before the first is stored. Rows that many
+// tokens name are read again from the caches: the loads keep the default
+// policy, the stores are non-temporal.
+
+// N elements of 8 or 16 bytes as float32
+template <int N, class E>
+__device__ __forceinline__ void load_items(const E* p, float* f) {
+  if constexpr (N * sizeof(E) == 8) {
+    typedef unsigned int half_t __attribute__((ext_vector_type(2), aligned(2)));
+    const half_t w = *reinterpret_cast<const half_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    Vec<E>::unpack(vload(p), f);
+  }
+}
+
+template <class E, class O, int U>
 __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ ids, int64_t T,
                                                     const E* __restrict__ table, int64_t table_stride, int64_t V,
                                                     int64_t D, float scale, O* __restrict__ out, int64_t out_stride,
-                                                    int lanes_log2, int items) {
+                                                    int lanes_log2) {
+  constexpr int N = Vec<O>::N;
   const int lanes = 1 << lanes_log2;
   const int64_t t = (int64_t)blockIdx.x * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
   if (t >= T) return;
@@ -36,14 +60,20 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ 
   const bool live = id >= 0 && id < V;
   const E* src = table + (live ? id : 0) * table_stride;
   O* dst = out + t * out_stride;
-  int64_t c = ((int64_t)blockIdx.y * items * lanes + (threadIdx.x & (lanes - 1))) * kItem;
-  for (int i = 0; i < items; ++i, c += (int64_t)lanes * kItem) {
-    if (c + kItem <= D) {
-      float f[kItem] = {};
-      if (live) load_row<kItem>(src + c, f);
+  const int64_t c0 = ((int64_t)blockIdx.y * U * lanes + (threadIdx.x & (lanes - 1))) * N;
+  float f[U][N];
 #pragma unroll
-      for (int e = 0; e < kItem; ++e) f[e] = live ? f[e] * scale : 0.0f;
-      store_row<kItem>(dst + c, f);
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = c0 + (int64_t)u * lanes * N;
+    if (live && c + N <= D) load_items<N>(src + c, f[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = c0 + (int64_t)u * lanes * N;
+    if (c + N <= D) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[u][e] = live ? f[u][e] * scale : 0.0f;
+      vstore_nt(dst + c, Vec<O>::pack(f[u]));
     } else {
       for (int64_t e = c; e < D; ++e) dst[e] = Vec<O>::round(live ? Vec<E>::value(src[e]) * scale : 0.0f);
     }
@@ -54,17 +84,44 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ 
 // sort: workgroup b owns the ids [b * bins, (b + 1) * bins) and reads every
 // token's id. Wave w takes the w-th part of the tokens and counts its own
 // histogram, so that after a scan over (id, wave) each wave knows where its
-// tokens of each id go; the second pass places them, a token's rank among the
-// equal ids of its 64 found by ballots over the id's bits. The workgroup also
+// tokens of each id go; then it places them, a token's rank among the equal
+// ids of its 64 found by ballots over the id's bits. The workgroup also
 // counts the tokens below its ids, so nothing passes between workgroups.
+//
+// While counting, a wave lists its workgroup's tokens in shared memory and
+// places them from there, 64 at a step. Reading the ids again instead, a
+// load would wait for the stores of the steps before it: 16384 tokens over
+// 128256 ids then take 19 us, from the list @@ us. A wave with more than
+// kList of its tokens in one workgroup's ids reads again.
 // ---------------------------------------------------------------------------
-constexpr int kBins = 512;
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 constexpr int kSortWaves = 16;
+constexpr int kList = 1024;                                // tokens that a wave lists
+constexpr int64_t kListedPart = int64_t(1) << (32 - kBinBits);  // tokens of a wave that an entry can name
+
+// A wave's ids, 64 at a step, loaded four steps ahead of their use.
+struct Ahead {
+  int id[4];
+  static __device__ __forceinline__ int load(const int32_t* ids, int64_t t, int64_t end) { return t < end ? ids[t] : -1; }
+  __device__ __forceinline__ Ahead(const int32_t* ids, int64_t t, int64_t end, int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) id[k] = load(ids, t + 64 * k + lane, end);
+  }
+  // the ids of the step at t
+  __device__ __forceinline__ int next(const int32_t* ids, int64_t t, int64_t end, int lane) {
+    const int now = id[0];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) id[k] = id[k + 1];
+    id[3] = load(ids, t + 256 + lane, end);
+    return now;
+  }
+};
 
 __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ ids, int T, int V, int bins,
                                                     int32_t* __restrict__ order, int32_t* __restrict__ keys,
                                                     int32_t* __restrict__ start) {
   __shared__ int hist[kSortWaves][kBins];
+  __shared__ uint32_t list[kSortWaves][kList];
   __shared__ int below[kSortWaves];
   __shared__ int scan[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
@@ -77,11 +134,20 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   const int begin = (int)(first < T ? first : T);
   const int end = T - begin < part ? T : begin + part;
 
-  int less = 0;
-  for (int t = begin; t < end; t += 64) {
-    const int id = t + lane < end ? ids[t + lane] : -1;
+  int less = 0, listed = 0;
+  Ahead a(ids, begin, end, lane);
+  for (int64_t t = begin; t < end; t += 64) {
+    const int id = a.next(ids, t, end, lane);
     less += __popcll(__ballot(id >= 0 && id < lo));
-    if (id >= lo && id - lo < n) atomicAdd(&hist[wave][id - lo], 1);
+    const bool mine = id >= lo && id - lo < n;
+    const uint64_t live = __ballot(mine);
+    if (live == 0) continue;
+    if (mine) {
+      atomicAdd(&hist[wave][id - lo], 1);
+      const int at = listed + __popcll(live & ((1ull << lane) - 1));
+      if (at < kList) list[wave][at] = (static_cast<uint32_t>(t - begin) + lane) << kBinBits | (id - lo);
+    }
+    listed += __popcll(live);
   }
   if (lane == 0) below[wave] = less;
   __syncthreads();
@@ -89,11 +155,14 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   // exclusive positions: over the waves of an id, then over the ids
   int base = 0;
   for (int w = 0; w < kSortWaves; ++w) base += below[w];
-  int total = 0;
+  int total = 0, before[kSortWaves] = {};  // tokens of the waves before each, of this thread's id
   if (tid < kBins) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) before[w] = hist[w][tid];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int c = hist[w][tid];
-      hist[w][tid] = total;
+      const int c = before[w];
+      before[w] = total;
       total += c;
     }
   }
@@ -108,21 +177,17 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   for (int w = 0; w < wave; ++w) base += scan[w];
   const int at = base + incl - total;
   if (tid < kBins) {
-    for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += at;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) hist[w][tid] = at + before[w];
     if (tid < n) start[lo + tid] = at;
     if (tid == n - 1 && lo + n == V) start[V] = at + total;
   }
   __syncthreads();
 
-  for (int t = begin; t < end; t += 64) {
-    const int id = t + lane < end ? ids[t + lane] : -1;
-    const bool mine = id >= lo && id - lo < n;
-    const uint64_t live = __ballot(mine);
-    if (live == 0) continue;
-    const int bin = mine ? id - lo : 0;
-    uint64_t same = live;
+  auto place = [&](bool mine, int bin, int t) {
+    uint64_t same = __ballot(mine);
 #pragma unroll
-    for (int b = 0; b < 9; ++b) {
+    for (int b = 0; b < kBinBits; ++b) {
       const uint64_t bit = __ballot((bin >> b) & 1);
       same &= (bin >> b) & 1 ? bit : ~bit;
     }
@@ -132,127 +197,208 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
     if (mine && rank == 0) pos = atomicAdd(&hist[wave][bin], __popcll(same));
     pos = __shfl(pos, mine ? head : 0, 64) + rank;
     if (mine) {
-      order[pos] = t + lane;
-      keys[pos] = id;
+      order[pos] = t;
+      keys[pos] = lo + bin;
     }
+  };
+  if (listed <= kList && part <= kListedPart) {
+    for (int i = 0; i < listed; i += 64) {
+      const bool mine = i + lane < listed;
+      const uint32_t w = mine ? list[wave][i + lane] : 0;
+      place(mine, w & (kBins - 1), begin + (int)(w >> kBinBits));
+    }
+    return;
+  }
+  a = Ahead(ids, begin, end, lane);
+  for (int64_t t = begin; t < end; t += 64) {
+    const int id = a.next(ids, t, end, lane);
+    const bool mine = id >= lo && id - lo < n;
+    if (__ballot(mine) != 0) place(mine, mine ? id - lo : 0, static_cast<int>(t) + lane);
   }
 }
 
 // ---------------------------------------------------------------------------
 // sums: a group of 2^lanes_log2 lanes takes one run of kRun sorted tokens and
-// one piece of the columns. An id whose tokens all lie in the run is written
-// at once; one that began before the run leaves its sum in part[run][0], one
-// that goes on after it in part[run][1].
+// one piece of the columns, a vector of dy per lane and token, all of them
+// loaded before the first is added. An id whose tokens all lie in the run is
+// written at once; one that began before the run leaves its sum in
+// part[run][0], one that goes on after it in part[run][1].
 // ---------------------------------------------------------------------------
-constexpr int kRun = 16;
+constexpr int kRun = 8;
 
-template <class O>
+// `count` of N elements
+template <int N, class O>
 __device__ __forceinline__ void put_row(O* p, const float* f, int count, bool add) {
-  if (count == kItem) {
-    float g[kItem];
+  if (count == N) {
+    float g[N];
 #pragma unroll
-    for (int e = 0; e < kItem; ++e) g[e] = f[e];
+    for (int e = 0; e < N; ++e) g[e] = f[e];
     if (add) {
-      float old[kItem];
-      load_row<kItem>(p, old);
+      float old[N];
+      load_row<N>(p, old);
 #pragma unroll
-      for (int e = 0; e < kItem; ++e) g[e] += old[e];
+      for (int e = 0; e < N; ++e) g[e] += old[e];
     }
-    store_row<kItem>(p, g);
+    store_row<N>(p, g);
   } else {
-    for (int e = 0; e < kItem; ++e)
+    for (int e = 0; e < N; ++e)
       if (e < count) p[e] = Vec<O>::round(add ? Vec<O>::value(p[e]) + f[e] : f[e]);
   }
 }
 
-template <class E, class O>
-__global__ __launch_bounds__(256) void grad_kernel(const int32_t* __restrict__ order, const int32_t* __restrict__ keys,
-                                                   const int32_t* __restrict__ start, int64_t V, int64_t D,
-                                                   const E* __restrict__ dy, int64_t dy_stride, float scale,
-                                                   O* __restrict__ out, int64_t out_stride, bool add,
+struct GradLists {
+  const int32_t *order, *keys, *start;
+  int64_t V, D;
+};
+
+// lanes and pieces of a row in the part of the grid that writes zeros
+struct FillShape {
+  int lanes_log2;
+  unsigned pieces;
+};
+
+template <class E, class O, bool ADD>
+__global__ __launch_bounds__(256, 8) void grad_kernel(GradLists l, const E* __restrict__ dy, int64_t dy_stride,
+                                                   float scale, O* __restrict__ out, int64_t out_stride,
                                                    float* __restrict__ part, int64_t part_stride, int lanes_log2,
-                                                   int pieces, int64_t run_blocks) {
+                                                   unsigned pieces, unsigned run_blocks, FillShape fill) {
+  constexpr int N = Vec<E>::N;
   const int lanes = 1 << lanes_log2;
-  const int n = start[V];
-  if ((int64_t)blockIdx.x >= run_blocks) {
-    // zeros of the rows that no token names
-    const int64_t row = ((int64_t)blockIdx.x - run_blocks) * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
-    if (row >= V || start[row] != start[row + 1]) return;
-    const float zero[kItem] = {};
-    for (int64_t c = (int64_t)(threadIdx.x & (lanes - 1)) * kItem; c < D; c += (int64_t)lanes * kItem)
-      put_row(out + row * out_stride + c, zero, D - c < kItem ? (int)(D - c) : kItem, false);
+  if (blockIdx.x >= run_blocks) {
+    // zeros of the rows that no token names, one vector per lane: many short
+    // workgroups in the order of the addresses write 1.05 GB in 153 us, with
+    // four vectors per lane in 175
+    constexpr int M = Vec<O>::N;
+    const unsigned unit = (((unsigned)blockIdx.x - run_blocks) << (8 - fill.lanes_log2)) +
+                          (threadIdx.x >> fill.lanes_log2);
+    const int64_t row = unit / fill.pieces;
+    const int64_t c = (((int64_t)(unit % fill.pieces) << fill.lanes_log2) +
+                       (threadIdx.x & ((1 << fill.lanes_log2) - 1))) * M;
+    if (row >= l.V || c >= l.D || l.start[row] != l.start[row + 1]) return;
+    O* p = out + row * out_stride + c;
+    const typename Vec<O>::type zero = {0u, 0u, 0u, 0u};
+    if (c + M <= l.D) {
+      vstore_nt(p, zero);
+    } else {
+      for (int e = 0; c + e < l.D; ++e) p[e] = Vec<O>::round(0.0f);
+    }
     return;
   }
-  const int64_t group = (int64_t)blockIdx.x * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
+  const int n = l.start[l.V];
+  const unsigned group = (blockIdx.x << (8 - lanes_log2)) + (threadIdx.x >> lanes_log2);
   const int64_t run = group / pieces;
-  const int64_t c = ((group % pieces) * lanes + (threadIdx.x & (lanes - 1))) * kItem;
+  const int64_t c = ((int64_t)(group % pieces) * lanes + (threadIdx.x & (lanes - 1))) * N;
   const int64_t p0 = run * kRun;
-  if (p0 >= n || c >= D) return;
-  const int p1 = n - p0 < kRun ? n : (int)p0 + kRun;
-  const int count = D - c < kItem ? (int)(D - c) : kItem;
-  const bool began = p0 > 0 && keys[p0 - 1] == keys[p0];   // the first id began in an earlier run
-  const bool goes_on = p1 < n && keys[p1 - 1] == keys[p1];  // the last id goes on in the next
-  float sum[kItem] = {};
+  if (p0 >= n || c >= l.D) return;
+  const int tokens = n - p0 < kRun ? n - (int)p0 : kRun;
+  // the lists' ends are padded to whole runs; what lies past n is not used
+  int key[kRun], at[kRun];
+#pragma unroll
+  for (int j = 0; j < kRun; j += 4) {
+    const int4 k = *reinterpret_cast<const int4*>(l.keys + p0 + j), o = *reinterpret_cast<const int4*>(l.order + p0 + j);
+    key[j] = k.x, key[j + 1] = k.y, key[j + 2] = k.z, key[j + 3] = k.w;
+    at[j] = o.x, at[j + 1] = o.y, at[j + 2] = o.z, at[j + 3] = o.w;
+  }
+  const int last_key = l.keys[p0 + tokens - 1];
+  const bool began = p0 > 0 && l.keys[p0 - 1] == key[0];                        // the first id began in an earlier run
+  const bool goes_on = p0 + tokens < n && l.keys[p0 + tokens] == last_key;  // the last id goes on in the next
+  float sum[N] = {};
   bool first = true;
-  for (int p = (int)p0; p < p1; ++p) {
-    const int key = keys[p];
-    const E* src = dy + (int64_t)order[p] * dy_stride + c;
-    float f[kItem] = {};
-    if (count == kItem) {
-      load_row<kItem>(src, f);
+  // after token j of id `key`, the last of its id in this run
+  auto finish = [&](int j, int key, int count) {
+    const bool before = first && began, after = j + 1 == tokens && goes_on;
+    if (!before && !after) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum[e] *= scale;
+      put_row<N>(out + (int64_t)key * out_stride + c, sum, count, ADD);
     } else {
-      for (int e = 0; e < kItem; ++e)
-        if (e < count) f[e] = Vec<E>::value(src[e]);
+      put_row<N>(part + (2 * run + (before ? 0 : 1)) * part_stride + c, sum, count, false);
     }
 #pragma unroll
-    for (int e = 0; e < kItem; ++e) sum[e] += f[e];
-    if (p + 1 < p1 && keys[p + 1] == key) continue;
-    const bool whole = !(first && began) && !(p + 1 == p1 && goes_on);
-    if (whole) {
-#pragma unroll
-      for (int e = 0; e < kItem; ++e) sum[e] *= scale;
-      put_row(out + (int64_t)key * out_stride + c, sum, count, add);
-    } else {
-      float* q = part + (2 * run + (first && began ? 0 : 1)) * part_stride + c;
-      for (int e = 0; e < kItem; ++e)
-        if (e < count) q[e] = sum[e];
-    }
-#pragma unroll
-    for (int e = 0; e < kItem; ++e) sum[e] = 0.0f;
+    for (int e = 0; e < N; ++e) sum[e] = 0.0f;
     first = false;
+  };
+  if (l.D - c < N) {
+    // the row's last elements
+    const int count = (int)(l.D - c);
+    for (int j = 0; j < tokens; ++j) {
+      const int key_j = l.keys[p0 + j];
+      const E* src = dy + (int64_t)l.order[p0 + j] * dy_stride + c;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < count) sum[e] += Vec<E>::value(src[e]);
+      if (j + 1 == tokens || l.keys[p0 + j + 1] != key_j) finish(j, key_j, count);
+    }
+    return;
+  }
+  typename Vec<E>::type w[kRun];
+#pragma unroll
+  for (int j = 0; j < kRun; ++j)
+    if (j < tokens) w[j] = vload_nt(dy + (int64_t)at[j] * dy_stride + c);
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    if (j >= tokens) break;
+    float f[N];
+    Vec<E>::unpack(w[j], f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] += f[e];
+    if (j + 1 == tokens || key[j + 1 < kRun ? j + 1 : j] != key[j]) finish(j, key[j], N);
   }
 }
 
-// One wave per run whose last id began in it and goes on, and 64 columns: the
-// id's pieces are part[run][1] and part[r][0] of the runs r that follow.
+// One workgroup per run whose last id began in it and goes on, and 4 columns
+// for each of `lanes` lanes: the id's pieces are part[run][1] and part[r][0]
+// of the runs r that follow. The workgroup's 256 / lanes groups take every
+// so many-th of them, and the groups' sums are added in order.
 template <class O>
-__global__ __launch_bounds__(256) void merge_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ start,
-                                                    int64_t V, int64_t D, const float* __restrict__ part,
-                                                    int64_t part_stride, float scale, O* __restrict__ out,
-                                                    int64_t out_stride, bool add, int pieces) {
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave_id();
-  const int64_t run = unit / pieces;
-  const int64_t c = (unit % pieces) * 64 + (threadIdx.x & 63);
-  const int n = start[V];
+__global__ __launch_bounds__(256) void merge_kernel(GradLists l, const float* __restrict__ part, int64_t part_stride,
+                                                    float scale, O* __restrict__ out, int64_t out_stride, bool add,
+                                                    int lanes_log2, unsigned pieces) {
+  __shared__ f32x4_t sums[256];
+  const int64_t run = blockIdx.x / pieces;
+  const int n = l.start[l.V];
   const int64_t p1 = (run + 1) * kRun;
-  if (p1 >= n || c >= D) return;
-  const int key = keys[p1 - 1];
-  if (keys[p1] != key || start[key] < run * kRun) return;
-  const int64_t last = (start[key + 1] - 1) / kRun;
-  float sum = part[(2 * run + 1) * part_stride + c];
-  for (int64_t r = run + 1; r <= last; ++r) sum += part[2 * r * part_stride + c];
+  if (p1 >= n) return;
+  const int key = l.keys[p1 - 1];
+  if (l.keys[p1] != key) return;
+  const int from = l.start[key], to = l.start[key + 1];
+  if (from < run * kRun) return;
+  const int lanes = 1 << lanes_log2, groups = 256 >> lanes_log2;
+  const int64_t c = ((int64_t)(blockIdx.x % pieces) * lanes + (threadIdx.x & (lanes - 1))) * 4;
+  const int count = l.D - c < 4 ? (int)(l.D - c) : 4;
+  const int64_t last = (to - 1) / kRun;  // the id's last run
+  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < l.D) {
+    int64_t r = run + (threadIdx.x >> lanes_log2);
+    for (; r <= last; r += 4 * groups) {
+      f32x4_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t k = r + u * groups;
+        v[u] = k <= last ? ld16f(part + (2 * k + (k == run ? 1 : 0)) * part_stride + c) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += v[u];
+    }
+  }
+  sums[threadIdx.x] = sum;
+  __syncthreads();
+  if ((int)threadIdx.x >= lanes || c >= l.D) return;
+  for (int g = 1; g < groups; ++g) sum += sums[(g << lanes_log2) + threadIdx.x];
   O* p = out + (int64_t)key * out_stride + c;
-  *p = Vec<O>::round(add ? Vec<O>::value(*p) + sum * scale : sum * scale);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < count) p[e] = Vec<O>::round(add ? Vec<O>::value(p[e]) + sum[e] * scale : sum[e] * scale);
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
-// lanes that share a row: enough for its items, at most a workgroup
-static int row_lanes_log2(int64_t D) {
+// lanes that share a row of D elements: enough for `item` elements each, at most a workgroup
+static int row_lanes_log2(int64_t D, int item) {
   int l = 0;
-  while (l < 8 && (int64_t(kItem) << l) < D) ++l;
+  while (l < 8 && (int64_t(item) << l) < D) ++l;
   return l;
 }
 
@@ -302,22 +448,30 @@ template <class E, class O>
 static int run_grad(const GradPlan& g, const lora_mat* dy, float scale, const lora_mat* out, bool add,
                     hipStream_t st) {
   const int64_t V = out->rows, D = out->cols;
-  const int ll = row_lanes_log2(D);
-  const int groups = 256 >> ll;
-  const int64_t pieces = ceil_div(D, int64_t(kItem) << ll);
-  const int64_t run_blocks = ceil_div(g.runs * pieces, groups);
-  const int64_t fill_blocks = add ? 0 : ceil_div(V, groups);
-  const int64_t merge_pieces = ceil_div(D, 64);
-  const int64_t merge_blocks = ceil_div(g.runs * merge_pieces, 4);
-  if (run_blocks + fill_blocks > kMaxGrid || merge_blocks > kMaxGrid || pieces > kMaxGrid || merge_pieces > kMaxGrid)
+  const int ll = row_lanes_log2(D, Vec<E>::N);
+  const int64_t pieces = ceil_div(D, int64_t(Vec<E>::N) << ll);
+  const int fl = row_lanes_log2(D, Vec<O>::N);
+  const int64_t fill_pieces = ceil_div(D, int64_t(Vec<O>::N) << fl);
+  int ml = row_lanes_log2(D, 4);
+  ml = ml < 6 ? ml : 6;
+  const int64_t merge_pieces = ceil_div(D, int64_t(4) << ml);
+  // runs, rows and their pieces are counted in 32 bits, rounded up to a workgroup's 256
+  constexpr int64_t kMost = kMaxGrid - 256;
+  if (pieces > kMost || fill_pieces > kMost || g.runs * pieces > kMost || V * fill_pieces > kMost ||
+      g.runs * merge_pieces > kMost)
     return LORA_ERR_LIMIT;
+  const int64_t run_blocks = ceil_div(g.runs * pieces, 256 >> ll);
+  const int64_t fill_blocks = add ? 0 : ceil_div(V * fill_pieces, 256 >> fl);
+  if (run_blocks + fill_blocks > kMaxGrid) return LORA_ERR_LIMIT;
+  const GradLists l = {g.order, g.keys, g.start, V, D};
   auto* o = static_cast<O*>(out->ptr);
-  launch(grad_kernel<E, O>, dim3(run_blocks + fill_blocks), dim3(256), 0, st, (const int32_t*)g.order,
-         (const int32_t*)g.keys, (const int32_t*)g.start, V, D, static_cast<const E*>(dy->ptr), dy->stride_row, scale,
-         o, out->stride_row, add, g.part, g.part_stride, ll, static_cast<int>(pieces), run_blocks);
+  launch(add ? grad_kernel<E, O, true> : grad_kernel<E, O, false>, dim3(run_blocks + fill_blocks), dim3(256), 0, st,
+         l, static_cast<const E*>(dy->ptr), dy->stride_row, scale, o, out->stride_row, g.part, g.part_stride, ll,
+         static_cast<unsigned>(pieces), static_cast<unsigned>(run_blocks),
+         FillShape{fl, static_cast<unsigned>(fill_pieces)});
   if (g.runs > 1)
-    launch(merge_kernel<O>, dim3(merge_blocks), dim3(256), 0, st, (const int32_t*)g.keys, (const int32_t*)g.start, V,
-           D, (const float*)g.part, g.part_stride, scale, o, out->stride_row, add, static_cast<int>(merge_pieces));
+    launch(merge_kernel<O>, dim3(g.runs * merge_pieces), dim3(256), 0, st, l, (const float*)g.part, g.part_stride,
+           scale, o, out->stride_row, add, ml, static_cast<unsigned>(merge_pieces));
   return launch_status();
 }
 
@@ -335,18 +489,20 @@ extern "C" int lora_embed(const int32_t* ids, const lora_mat* table, float scale
   if (T > kMaxTokens || V > kMaxTokens) return LORA_ERR_LIMIT;
   if (T == 0 || D == 0) return LORA_OK;
   if (!ids || !out->ptr || (V > 0 && !table->ptr)) return LORA_ERR_NULL;
-  const int ll = row_lanes_log2(D);
+  const int item = vec_elems(out->dtype);
+  const int ll = row_lanes_log2(D, item);
   const int64_t blocks = ceil_div(T, 256 >> ll);
-  const int64_t steps = ceil_div(D, int64_t(kItem) << ll);
-  const int items = steps >= 4 && blocks >= 512 ? 4 : 1;
-  if (ceil_div(steps, items) > 65535) return LORA_ERR_LIMIT;
-  const dim3 grid(blocks, ceil_div(steps, items));
+  const int64_t steps = ceil_div(D, int64_t(item) << ll);
+  // U vectors of a row per lane where the row has them and the workgroups still fill the card
+  const int u = steps >= 4 && blocks >= 512 ? 4 : steps >= 2 && blocks >= 512 ? 2 : 1;
+  if (blocks > kMaxGrid || ceil_div(steps, u) > 65535) return LORA_ERR_LIMIT;
+  const dim3 grid(blocks, ceil_div(steps, u));
   auto st = static_cast<hipStream_t>(stream);
   auto go = [&](auto* e, auto* o) {
     using E = std::remove_pointer_t<decltype(e)>;
     using O = std::remove_pointer_t<decltype(o)>;
-    launch(embed_kernel<E, O>, grid, dim3(256), 0, st, ids, T, (const E*)e, table->stride_row, V, D, scale, o,
-           out->stride_row, ll, items);
+    launch(u == 4 ? embed_kernel<E, O, 4> : u == 2 ? embed_kernel<E, O, 2> : embed_kernel<E, O, 1>, grid, dim3(256),
+           0, st, ids, T, (const E*)e, table->stride_row, V, D, scale, o, out->stride_row, ll);
   };
   if (table->dtype == LORA_F32)
     go(static_cast<float*>(table->ptr), static_cast<float*>(out->ptr));

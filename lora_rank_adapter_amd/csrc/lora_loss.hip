@@ -15,10 +15,12 @@
 //
 // Kernels:
 //   logp_kernel       one pass over a row (or one piece of it): running max and sum
-//   join_kernel       the pieces of a row joined, one wave per row
+//   join_kernel       the pieces of a row joined, four lanes per row
 //   pref_kernel       sequence sums, the loss and each token's coefficient
 //   policy_kernel     each token's loss and coefficient, and their sum
-//   grad_kernel       the gradient's rows from the statistics and coefficients
+//   policy_row_kernel a row from its statistics to its gradient (policy loss)
+//   sum_kernel        the sum of the tokens' losses
+//   logit_grad_kernel the gradient's rows from the statistics and coefficients
 
 #include <type_traits>
 
@@ -73,8 +75,8 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
                                                    float2* __restrict__ part) {
   constexpr int N = Vec<E>::N, U = 4;
   __shared__ MaxSum waves[4];
-  const int64_t row = (int64_t)blockIdx.x / splits;
-  const int sp = (int)((int64_t)blockIdx.x % splits);
+  const int64_t row = blockIdx.x / (unsigned)splits;
+  const int sp = (int)(blockIdx.x % (unsigned)splits);
   const int tid = threadIdx.x;
   const int y = targets[row];
   if (y < 0 || y >= V) {
@@ -131,8 +133,8 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   }
 }
 
-// The pieces of a row's statistics, joined by one wave: what remains of the
-// softmax once logp_kernel has written `splits` pieces of each row (at most one per lane).
+// What remains of the softmax once logp_kernel has written `splits` pieces of
+// each row: four lanes join a row's.
 template <class E>
 struct RowPieces {
   const E* x;
@@ -143,38 +145,54 @@ struct RowPieces {
   float2* stats;
 };
 
+// The log probability of `row` for the lane of its four whose `sub` is 0.
 template <class E>
-__device__ __forceinline__ void join_row(const RowPieces<E>& a, int64_t row, int lane, float* logp) {
-  const int y = a.targets[row];
-  if (y < 0 || y >= a.V) {
-    if (lane == 0) {
-      logp[row] = 0.0f;
-      a.stats[row] = make_float2(0.0f, 1.0f);
-    }
-    return;
+__device__ __forceinline__ float join_row(const RowPieces<E>& a, int64_t row, int64_t T, int sub, float* logp) {
+  constexpr int U = 8;
+  const int y = row < T ? a.targets[row] : -1;
+  const bool live = y >= 0 && y < a.V;
+  const float hit = live ? Vec<E>::value(a.x[row * a.stride + y]) : 0.0f;
+  MaxSum r{-INFINITY, 0.0f};
+  for (int sp = sub; sp < a.splits; sp += 4 * U) {
+    float2 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = live && sp + 4 * u < a.splits ? a.part[row * a.splits + sp + 4 * u] : make_float2(-INFINITY, 0.0f);
+    float m = r.m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].x);
+    const float z = at_max(m);
+    float s = r.s * exp2_raw((r.m - z) * kLog2e);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += v[u].y * exp2_raw((v[u].x - z) * kLog2e);
+    r = {m, s};
   }
-  const float2 v = lane < a.splits ? a.part[row * a.splits + lane] : make_float2(-INFINITY, 0.0f);
-  const float hit = Vec<E>::value(a.x[row * a.stride + y]);
-  const MaxSum r = wave_join(MaxSum{v.x, v.y});
-  if (lane == 0) {
-    logp[row] = target_logp(hit, r);
-    a.stats[row] = make_float2(r.m, r.s);
+  r = join(r, MaxSum{__shfl_xor(r.m, 1, 64), __shfl_xor(r.s, 1, 64)});
+  r = join(r, MaxSum{__shfl_xor(r.m, 2, 64), __shfl_xor(r.s, 2, 64)});
+  const float lp = live ? target_logp(hit, r) : 0.0f;
+  if (sub == 0 && row < T) {
+    logp[row] = lp;
+    a.stats[row] = live ? make_float2(r.m, r.s) : make_float2(0.0f, 1.0f);
   }
+  return lp;
 }
 
 template <class E>
 __global__ __launch_bounds__(256) void join_kernel(RowPieces<E> a, int64_t T, float* __restrict__ logp) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
-  if (row < T) join_row(a, row, threadIdx.x & 63, logp);
+  join_row(a, (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2), T, threadIdx.x & 3, logp);
 }
 
-// The same in a workgroup of 1024 that goes on with the log probabilities.
+// The same for up to kJoinRows rows in a workgroup of 1024 that goes on with
+// their log probabilities: it finds them in `lds`. Without pieces: in logp.
+constexpr int kJoinRows = 256;
 template <class E>
-__device__ __forceinline__ void join_rows(const RowPieces<E>& a, int64_t T, float* logp) {
-  if (a.part == nullptr) return;
-#pragma unroll 4
-  for (int64_t row = wave_id(); row < T; row += 16) join_row(a, row, threadIdx.x & 63, logp);
+__device__ __forceinline__ const float* join_rows(const RowPieces<E>& a, int64_t T, float* logp, float* lds) {
+  if (a.part == nullptr) return logp;
+  const int row = threadIdx.x >> 2, sub = threadIdx.x & 3;
+  const float lp = join_row(a, row, T, sub, logp);
+  if (sub == 0) lds[row] = lp;
   __syncthreads();
+  return lds;
 }
 
 // ---------------------------------------------------------------------------
@@ -198,13 +216,14 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // difference of long sums. One wave per pair; its two sequences' tokens get
 // the coefficients beta * dz / pairs and minus that.
 template <class E>
-__global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* logp, int64_t T,
+__global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
                                                     const float* __restrict__ ref, float beta, float eps,
                                                     float* __restrict__ loss, float* __restrict__ seq_logp,
                                                     float* __restrict__ coef) {
   __shared__ double lds[16];
-  join_rows(pieces, T, logp);
+  __shared__ float joined[kJoinRows];
+  const float* logp = join_rows(pieces, T, logp_out, joined);
   const int lane = threadIdx.x & 63;
   auto offset = [&](int64_t i) -> int64_t {
     const int64_t o = offsets[i];
@@ -268,11 +287,12 @@ __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, f
 }
 
 template <class E>
-__global__ __launch_bounds__(1024) void policy_kernel(RowPieces<E> pieces, float* logp, int64_t T, int64_t V,
+__global__ __launch_bounds__(1024) void policy_kernel(RowPieces<E> pieces, float* logp_out, int64_t T, int64_t V,
                                                       PolicyArgs a, float* __restrict__ loss,
                                                       float* __restrict__ coef) {
   __shared__ double lds[16];
-  join_rows(pieces, T, logp);
+  __shared__ float joined[kJoinRows];
+  const float* logp = join_rows(pieces, T, logp_out, joined);
   double sum = 0.0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int y = a.targets[t];
@@ -408,20 +428,23 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ ter
 }
 
 // ---------------------------------------------------------------------------
-// gradient: a workgroup takes 256 * U vectors of one row
+// gradient: a workgroup takes one piece of a row, a vector per lane. Memory
+// that many short workgroups write in the order of its addresses goes faster
+// than what fewer, longer ones write: 8192 x 128256 bfloat16 takes 568 us
+// with one vector per lane, 602 with two, 637 with four.
 // ---------------------------------------------------------------------------
-constexpr int kGradVecs = 1024;
+constexpr int kGradVecs = 256;
 
 template <class E>
-__global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t stride,
-                                                         const int32_t* __restrict__ targets,
-                                                         const float2* __restrict__ stats,
-                                                         const float* __restrict__ coef,
-                                                         const float* __restrict__ grad_out, float scale, int V,
-                                                         int pieces, E* dx, int64_t dx_stride) {
-  constexpr int N = Vec<E>::N, U = kGradVecs / 256;
-  const int64_t row = (int64_t)blockIdx.x / pieces;
-  const int lo = (int)((int64_t)blockIdx.x % pieces) * kGradVecs * N;
+__global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(const E* x, int64_t stride,
+                                                               const int32_t* __restrict__ targets,
+                                                               const float2* __restrict__ stats,
+                                                               const float* __restrict__ coef,
+                                                               const float* __restrict__ grad_out, float scale, int V,
+                                                               int pieces, E* dx, int64_t dx_stride) {
+  constexpr int N = Vec<E>::N;
+  const int64_t row = blockIdx.x / (unsigned)pieces;
+  const int lo = (int)(blockIdx.x % (unsigned)pieces) * kGradVecs * N;
   const int n = V - lo < kGradVecs * N ? V - lo : kGradVecs * N;
   const int tid = threadIdx.x;
   const int y = targets[row];
@@ -430,41 +453,32 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t str
   const E* p = x + row * stride + lo;
   E* q = dx + row * dx_stride + lo;
   const int vecs = n / N;
+  const int rest = vecs * N + tid;  // the row's last elements, one per lane
   if (!live) {
     const typename Vec<E>::type zero = {0u, 0u, 0u, 0u};
-    for (int i = tid; i < vecs; i += 256) vstore_nt(q + i * N, zero);
-    if (tid < n - vecs * N) q[vecs * N + tid] = Vec<E>::round(0.0f);
+    if (tid < vecs) vstore_nt(q + tid * N, zero);
+    if (rest < n) q[rest] = Vec<E>::round(0.0f);
     return;
   }
   float c = coef[row] * scale;
   if (grad_out != nullptr) c *= *grad_out;
   const float2 st = stats[row];
-  const float m = at_max(st.x), cs = c / st.y;
+  const float m = at_max(st.x), cs = -c / st.y;
   const int hit = y - lo;
-  auto value = [&](float v) { return -cs * exp2_raw((v - m) * kLog2e); };
-  typename Vec<E>::type w[U];
+  if (tid < vecs) {
+    float f[N];
+    Vec<E>::unpack(vload_nt(p + tid * N), f);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (tid + u * 256 < vecs) w[u] = vload_nt(p + (tid + u * 256) * N);
+    for (int e = 0; e < N; ++e) f[e] = cs * exp2_raw((f[e] - m) * kLog2e);
+    if (static_cast<unsigned>(hit - tid * N) < N) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i = tid + u * 256;
-    if (i < vecs) {
-      float f[N];
-      Vec<E>::unpack(w[u], f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = value(f[e]);
-      if (static_cast<unsigned>(hit - i * N) < N) {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (i * N + e == hit) f[e] += c;
-      }
-      vstore_nt(q + i * N, Vec<E>::pack(f));
+      for (int e = 0; e < N; ++e)
+        if (tid * N + e == hit) f[e] += c;
     }
+    vstore_nt(q + tid * N, Vec<E>::pack(f));
   }
-  const int rest = vecs * N + tid;
   if (rest < n) {
-    const float g = value(Vec<E>::value(p[rest]));
+    const float g = cs * exp2_raw((Vec<E>::value(p[rest]) - m) * kLog2e);
     q[rest] = Vec<E>::round(rest == hit ? g + c : g);
   }
 }
@@ -474,12 +488,13 @@ __global__ __launch_bounds__(256) void logit_grad_kernel(const E* x, int64_t str
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kMaxLogitRows = 0x7FFFFFFF;
-constexpr int kMaxSplits = 64;  // pieces of one row: one per lane of join_kernel
+constexpr int kMaxSplits = 64;  // pieces of one row
 
-// Pieces per row: one while the rows alone give 2048 workgroups (8 per CU),
-// else enough for that, of at least 4096 logits.
+// Pieces per row: about as many as give 2048 workgroups (8 per CU), of at
+// least 4096 logits each.
 static int row_splits(int64_t T, int64_t V) {
-  int64_t s = ceil_div(2048, T < 1 ? 1 : T);
+  const int64_t rows = T < 1 ? 1 : T;
+  int64_t s = (2048 + rows / 2) / rows;
   const int64_t most = ceil_div(V, 4096);
   s = s < most ? s : most;
   return static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
@@ -548,14 +563,14 @@ static void run_join(const lora_mat* x, const int32_t* targets, float* logp, flo
   if (row_splits(x->rows, x->cols) == 1) return;
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(join_kernel<E>, dim3(ceil_div(x->rows, 4)), dim3(256), 0, st, row_pieces<E>(x, targets, stats, l), x->rows,
+    launch(join_kernel<E>, dim3(ceil_div(x->rows, 64)), dim3(256), 0, st, row_pieces<E>(x, targets, stats, l), x->rows,
            logp);
   });
 }
 
 // Few rows are joined by the loss's own workgroup, which saves a launch (about
-// 3 us each); beyond 256 rows the many waves of join_kernel are faster.
-static bool join_in_loss(int64_t T, int64_t V) { return row_splits(T, V) > 1 && T <= 256; }
+// 3 us each); more rows are spread over the card by join_kernel.
+static bool join_in_loss(int64_t T, int64_t V) { return row_splits(T, V) > 1 && T <= kJoinRows; }
 
 static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;

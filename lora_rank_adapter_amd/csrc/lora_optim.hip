@@ -97,11 +97,21 @@ struct StepConst {
   float alpha, inv_root, decay, gs;
 };
 
+// Square roots and reciprocals by the approximate instructions (within one
+// step of the last place, against half a step at ten times the cost). Below
+// 2^-96 the root is taken of v * 2^64, so that a denormal v keeps its root.
+__device__ __forceinline__ float root(float v) {
+  const bool small = v < 0x1p-96f;
+  const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p-32f : r;
+}
+
 __device__ __forceinline__ void adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
   g *= k.gs;
   m = a.b1 * m + a.c1 * g;
   v = a.b2 * v + a.c2 * (g * g);
-  p = p * k.decay - k.alpha * m / (sqrtf(v) * k.inv_root + a.eps);
+  // the divisor is at least eps, or the root of a v above zero: no denormal, whose reciprocal would be lost
+  p = p * k.decay - k.alpha * m * __builtin_amdgcn_rcpf(root(v) * k.inv_root + a.eps);
 }
 
 // four codes of one word as values, and back (rounded to nearest even)
@@ -116,10 +126,18 @@ __device__ __forceinline__ uint32_t fp8_codes(const float* f) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true));
 }
 
+// The largest of the wave's values: rotations within each row of 16 lanes,
+// then the rows' four results.
+template <int D>
+__device__ __forceinline__ float rotate_max(float v) {
+  const int r = __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + D, 0xF, 0xF, false);
+  return fmaxf(v, __int_as_float(r));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+  const int m = __float_as_int(rotate_max<1>(rotate_max<2>(rotate_max<4>(rotate_max<8>(v)))));
+  const float a = fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 0)), __int_as_float(__builtin_amdgcn_readlane(m, 16)));
+  const float b = fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 32)), __int_as_float(__builtin_amdgcn_readlane(m, 48)));
+  return fmaxf(a, b);
 }
 
 // x: 4 values of each lane, one block over the wave. Returns the codes.
@@ -127,8 +145,8 @@ __device__ __forceinline__ uint32_t quantise(float* x, bool positive, float* sca
   const float amax = wave_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
   // a block below 1e-30 is stored as zeros (448 / amax stays finite above it)
   const bool some = amax >= 1e-30f;
-  const float inv = some ? 448.0f / amax : 0.0f;
-  *scale = some ? amax / 448.0f : 0.0f;
+  const float inv = some ? 448.0f * __builtin_amdgcn_rcpf(amax) : 0.0f;
+  *scale = some ? amax * (1.0f / 448.0f) : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float q = x[i] * inv;
@@ -209,7 +227,7 @@ __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64
     if (e.shadow != nullptr) store4(e.shadow, true, i, e.vec, count, p);
     if constexpr (BITS == 8) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = sqrtf(v[j]);
+      for (int j = 0; j < 4; ++j) v[j] = root(v[j]);
       float ms, vs;
       const uint32_t mc = quantise(m, false, &ms), vc = quantise(v, true, &vs);
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = mc;

@@ -8,6 +8,7 @@ calls: when the library cannot be built or loaded, every op raises.
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 
 from . import build as _build
@@ -42,6 +43,11 @@ class LoraMat(ctypes.Structure):
         ("stride_row", ctypes.c_int64),
         ("stride_col", ctypes.c_int64),
     ]
+
+
+# A LoraMat as packed bytes, which a call takes in a fraction of the time of a Structure object. The functions
+# that take them declare c_void_p (byref of a LoraMat does as well).
+pack_mat = struct.Struct("=Qiiqqqq").pack
 
 
 class LoraT3(ctypes.Structure):
@@ -147,26 +153,26 @@ SIGNATURES = {
                                                  ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
     "lora_gather_shrink": (ctypes.c_int, [ctypes.c_void_p, _P(LoraT3), _P(LoraAddressing), ctypes.c_void_p,
                                           ctypes.c_int32, _P(LoraT3), ctypes.c_void_p]),
-    "lora_embed": (ctypes.c_int, [ctypes.c_void_p, _P(LoraMat), ctypes.c_float, _P(LoraMat), ctypes.c_void_p]),
+    "lora_embed": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
     "lora_embed_grad_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
-    "lora_embed_grad": (ctypes.c_int, [ctypes.c_void_p, _P(LoraMat), ctypes.c_float, _P(LoraMat), ctypes.c_int32,
+    "lora_embed_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32,
                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "lora_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
-    "lora_token_logp": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+    "lora_token_logp": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "lora_pref_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                       ctypes.c_void_p, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "lora_policy_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, _P(LoraPolicy),
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "lora_logit_grad": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
-                                       ctypes.c_void_p, ctypes.c_float, _P(LoraMat), ctypes.c_void_p]),
-    "lora_pref_step": (ctypes.c_int, [_P(LoraMat), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+    "lora_logit_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "lora_pref_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                       ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
-                                      ctypes.c_void_p, ctypes.c_void_p, _P(LoraMat), ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_size_t, ctypes.c_void_p]),
-    "lora_policy_step": (ctypes.c_int, [_P(LoraMat), _P(LoraPolicy), ctypes.c_float, ctypes.c_void_p,
-                                        ctypes.c_void_p, _P(LoraMat), ctypes.c_void_p, ctypes.c_size_t,
+    "lora_policy_step": (ctypes.c_int, [ctypes.c_void_p, _P(LoraPolicy), ctypes.c_float, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]),
     "lora_adamw_table_bytes": (ctypes.c_size_t, [_P(LoraAdamwTensor), ctypes.c_int64]),
     "lora_adamw_state_elems": (ctypes.c_int64, [_P(LoraAdamwTensor), ctypes.c_int64]),

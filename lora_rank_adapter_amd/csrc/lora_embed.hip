@@ -6,14 +6,14 @@
 // Both move rows and compute next to nothing: they are bound by HBM.
 //
 // The gradient sums in a fixed order, without float atomics: sort_kernel
-// orders the tokens by id (stable) and gives every id its range of the sorted
+// groups the tokens by id (stable) and gives every id its range of the
 // list; grad_kernel cuts the list into runs of a fixed length, so that an id
 // that fills the batch costs no more than others, and sums each id's tokens
 // inside a run; merge_kernel adds the pieces of the ids that span runs.
 //
 // Kernels:
 //   embed_kernel   rows gathered, scaled and stored
-//   sort_kernel    stable counting sort of the tokens by id, one launch
+//   sort_kernel    the tokens grouped by id, one launch
 //   grad_kernel    sums of each run's ids, zeros of the rows without tokens
 //   merge_kernel   pieces of an id added in the order of their runs
 
@@ -81,12 +81,15 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// sort: workgroup b owns the ids [b * bins, (b + 1) * bins) and reads every
-// token's id. Wave w takes the w-th part of the tokens and counts its own
-// histogram, so that after a scan over (id, wave) each wave knows where its
-// tokens of each id go; then it places them, a token's rank among the equal
-// ids of its 64 found by ballots over the id's bits. The workgroup also
-// counts the tokens below its ids, so nothing passes between workgroups.
+// sort: groups the tokens by id, those of an id in their order. Four ids in a
+// row belong to one workgroup, the next four to the next (frequent ids, often
+// the low ones, spread over the card), and the ids' lists follow each other
+// by workgroup. Every workgroup reads every token's id. Wave w takes the w-th
+// part of the tokens and counts its own histogram, so that after a scan over
+// (id, wave) each wave knows where its tokens of each id go; then it places
+// them, a token's rank among the equal ids of its 64 found by ballots over
+// the id's bits. The workgroup also counts the tokens of the workgroups
+// before it, so nothing passes between workgroups.
 //
 // While counting, a wave lists its workgroup's tokens in shared memory and
 // places them from there, 64 at a step. Reading the ids again instead, a
@@ -94,6 +97,19 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ 
 // 128256 ids then take 19 us, from the list @@ us. A wave with more than
 // kList of its tokens in one workgroup's ids reads again.
 // ---------------------------------------------------------------------------
+// How ids are shared out: blocks_log2 of the workgroups, `bins` ids to each.
+struct IdMap {
+  int blocks_log2, bins;
+  __device__ __forceinline__ int block(int id) const { return (id >> 2) & ((1 << blocks_log2) - 1); }
+  __device__ __forceinline__ int bin(int id) const { return (id >> (blocks_log2 + 2) << 2) | (id & 3); }
+  __device__ __forceinline__ int id(int block, int bin) const {
+    return (bin >> 2 << (blocks_log2 + 2)) | block << 2 | (bin & 3);
+  }
+  // position of an id in the lists' starts; the end of the last list is at total()
+  __device__ __forceinline__ int64_t at(int id) const { return (int64_t)block(id) * bins + bin(id); }
+  __device__ __forceinline__ int64_t total() const { return (int64_t)bins << blocks_log2; }
+};
+
 constexpr int kBinBits = 9, kBins = 1 << kBinBits;
 constexpr int kSortWaves = 16;
 constexpr int kList = 1024;                                // tokens that a wave lists
@@ -117,16 +133,17 @@ struct Ahead {
   }
 };
 
-__global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ ids, int T, int V, int bins,
+__global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ ids, int T, int V, IdMap map,
                                                     int32_t* __restrict__ order, int32_t* __restrict__ keys,
-                                                    int32_t* __restrict__ start) {
+                                                    int32_t* __restrict__ start, int32_t* __restrict__ count) {
   __shared__ int hist[kSortWaves][kBins];
   __shared__ uint32_t list[kSortWaves][kList];
   __shared__ int below[kSortWaves];
   __shared__ int scan[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
-  const int lo = blockIdx.x * bins;
-  const int n = V - lo < bins ? V - lo : bins;  // this workgroup's ids
+  const int block = blockIdx.x;
+  // the workgroup of an id, or one past all of them
+  auto owner = [&](int id) { return id >= 0 && id < V ? map.block(id) : 0x7FFFFFFF; };
   for (int i = tid; i < kSortWaves * kBins; i += 1024) (&hist[0][0])[i] = 0;
   __syncthreads();
   const int part = (int)((((int64_t)T + kSortWaves - 1) / kSortWaves + 63) / 64 * 64);
@@ -138,14 +155,16 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   Ahead a(ids, begin, end, lane);
   for (int64_t t = begin; t < end; t += 64) {
     const int id = a.next(ids, t, end, lane);
-    less += __popcll(__ballot(id >= 0 && id < lo));
-    const bool mine = id >= lo && id - lo < n;
+    const int o = owner(id);
+    less += __popcll(__ballot(o < block));
+    const bool mine = o == block;
     const uint64_t live = __ballot(mine);
     if (live == 0) continue;
     if (mine) {
-      atomicAdd(&hist[wave][id - lo], 1);
+      const int bin = map.bin(id);
+      atomicAdd(&hist[wave][bin], 1);
       const int at = listed + __popcll(live & ((1ull << lane) - 1));
-      if (at < kList) list[wave][at] = (static_cast<uint32_t>(t - begin) + lane) << kBinBits | (id - lo);
+      if (at < kList) list[wave][at] = (static_cast<uint32_t>(t - begin) + lane) << kBinBits | bin;
     }
     listed += __popcll(live);
   }
@@ -179,8 +198,12 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   if (tid < kBins) {
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) hist[w][tid] = at + before[w];
-    if (tid < n) start[lo + tid] = at;
-    if (tid == n - 1 && lo + n == V) start[V] = at + total;
+    if (tid < map.bins) {
+      start[(int64_t)block * map.bins + tid] = at;
+      const int id = map.id(block, tid);
+      if (id < V) count[id] = total;  // in the order of the ids, for the rows without tokens
+    }
+    if (tid == map.bins - 1 && block == (1 << map.blocks_log2) - 1) start[map.total()] = at + total;
   }
   __syncthreads();
 
@@ -198,7 +221,7 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
     pos = __shfl(pos, mine ? head : 0, 64) + rank;
     if (mine) {
       order[pos] = t;
-      keys[pos] = lo + bin;
+      keys[pos] = map.id(block, bin);
     }
   };
   if (listed <= kList && part <= kListedPart) {
@@ -212,8 +235,8 @@ __global__ __launch_bounds__(1024) void sort_kernel(const int32_t* __restrict__ 
   a = Ahead(ids, begin, end, lane);
   for (int64_t t = begin; t < end; t += 64) {
     const int id = a.next(ids, t, end, lane);
-    const bool mine = id >= lo && id - lo < n;
-    if (__ballot(mine) != 0) place(mine, mine ? id - lo : 0, static_cast<int>(t) + lane);
+    const bool mine = owner(id) == block;
+    if (__ballot(mine) != 0) place(mine, mine ? map.bin(id) : 0, static_cast<int>(t) + lane);
   }
 }
 
@@ -247,7 +270,8 @@ __device__ __forceinline__ void put_row(O* p, const float* f, int count, bool ad
 }
 
 struct GradLists {
-  const int32_t *order, *keys, *start;
+  const int32_t *order, *keys, *start, *count;
+  IdMap map;
   int64_t V, D;
 };
 
@@ -274,7 +298,7 @@ __global__ __launch_bounds__(256, 8) void grad_kernel(GradLists l, const E* __re
     const int64_t row = unit / fill.pieces;
     const int64_t c = (((int64_t)(unit % fill.pieces) << fill.lanes_log2) +
                        (threadIdx.x & ((1 << fill.lanes_log2) - 1))) * M;
-    if (row >= l.V || c >= l.D || l.start[row] != l.start[row + 1]) return;
+    if (row >= l.V || c >= l.D || l.count[row] != 0) return;
     O* p = out + row * out_stride + c;
     const typename Vec<O>::type zero = {0u, 0u, 0u, 0u};
     if (c + M <= l.D) {
@@ -284,7 +308,7 @@ __global__ __launch_bounds__(256, 8) void grad_kernel(GradLists l, const E* __re
     }
     return;
   }
-  const int n = l.start[l.V];
+  const int n = l.start[l.map.total()];
   const unsigned group = (blockIdx.x << (8 - lanes_log2)) + (threadIdx.x >> lanes_log2);
   const int64_t run = group / pieces;
   const int64_t c = ((int64_t)(group % pieces) * lanes + (threadIdx.x & (lanes - 1))) * N;
@@ -356,12 +380,11 @@ __global__ __launch_bounds__(256) void merge_kernel(GradLists l, const float* __
                                                     int lanes_log2, unsigned pieces) {
   __shared__ f32x4_t sums[256];
   const int64_t run = blockIdx.x / pieces;
-  const int n = l.start[l.V];
-  const int64_t p1 = (run + 1) * kRun;
-  if (p1 >= n) return;
-  const int key = l.keys[p1 - 1];
-  if (l.keys[p1] != key) return;
-  const int from = l.start[key], to = l.start[key + 1];
+  const int64_t p1 = (run + 1) * kRun;  // below the padded length of the lists: the last run has no workgroup
+  const int n = l.start[l.map.total()], key = l.keys[p1 - 1], next = l.keys[p1];
+  if (p1 >= n || next != key) return;
+  const int64_t s = l.map.at(key);
+  const int from = l.start[s], to = l.start[s + 1];
   if (from < run * kRun) return;
   const int lanes = 1 << lanes_log2, groups = 256 >> lanes_log2;
   const int64_t c = ((int64_t)(blockIdx.x % pieces) * lanes + (threadIdx.x & (lanes - 1))) * 4;
@@ -416,9 +439,9 @@ constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 
 struct GradPlan {
   int64_t runs, part_stride;
-  int bins, sort_blocks;
+  IdMap map;
   size_t bytes;
-  int32_t *order, *keys, *start;
+  int32_t *order, *keys, *start, *count;
   float* part;
 };
 
@@ -427,12 +450,15 @@ static GradPlan plan_grad(int64_t T, int64_t V, int64_t D, void* ws) {
   g.runs = ceil_div(T, kRun);
   g.part_stride = round_up(D, 4);
   // 256 workgroups (one per CU) while their ids fit the histogram, more beyond
-  g.bins = static_cast<int>(V <= 256 * kBins ? ceil_div(V, 256) : kBins);
-  g.sort_blocks = static_cast<int>(ceil_div(V, g.bins));
+  const int64_t quads = ceil_div(V, 4);
+  g.map.blocks_log2 = 8;
+  while (ceil_div(quads, int64_t(1) << g.map.blocks_log2) > kBins / 4) ++g.map.blocks_log2;
+  g.map.bins = static_cast<int>(4 * ceil_div(quads, int64_t(1) << g.map.blocks_log2));
   Carver w(ws);
   g.order = static_cast<int32_t*>(w.take(T * sizeof(int32_t)));
   g.keys = static_cast<int32_t*>(w.take(T * sizeof(int32_t)));
-  g.start = static_cast<int32_t*>(w.take((V + 1) * sizeof(int32_t)));
+  g.start = static_cast<int32_t*>(w.take(((int64_t(g.map.bins) << g.map.blocks_log2) + 1) * sizeof(int32_t)));
+  g.count = static_cast<int32_t*>(w.take(V * sizeof(int32_t)));
   g.part = static_cast<float*>(w.take(2 * g.runs * g.part_stride * sizeof(float)));
   g.bytes = w.used;
   return g;
@@ -463,14 +489,14 @@ static int run_grad(const GradPlan& g, const lora_mat* dy, float scale, const lo
   const int64_t run_blocks = ceil_div(g.runs * pieces, 256 >> ll);
   const int64_t fill_blocks = add ? 0 : ceil_div(V * fill_pieces, 256 >> fl);
   if (run_blocks + fill_blocks > kMaxGrid) return LORA_ERR_LIMIT;
-  const GradLists l = {g.order, g.keys, g.start, V, D};
+  const GradLists l = {g.order, g.keys, g.start, g.count, g.map, V, D};
   auto* o = static_cast<O*>(out->ptr);
   launch(add ? grad_kernel<E, O, true> : grad_kernel<E, O, false>, dim3(run_blocks + fill_blocks), dim3(256), 0, st,
          l, static_cast<const E*>(dy->ptr), dy->stride_row, scale, o, out->stride_row, g.part, g.part_stride, ll,
          static_cast<unsigned>(pieces), static_cast<unsigned>(run_blocks),
          FillShape{fl, static_cast<unsigned>(fill_pieces)});
   if (g.runs > 1)
-    launch(merge_kernel<O>, dim3(g.runs * merge_pieces), dim3(256), 0, st, l, (const float*)g.part, g.part_stride,
+    launch(merge_kernel<O>, dim3((g.runs - 1) * merge_pieces), dim3(256), 0, st, l, (const float*)g.part, g.part_stride,
            scale, o, out->stride_row, add, ml, static_cast<unsigned>(merge_pieces));
   return launch_status();
 }
@@ -533,8 +559,8 @@ extern "C" int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float sca
   const GradPlan g = plan_grad(T, V, D, workspace);
   if (!workspace || workspace_bytes < g.bytes || !aligned(workspace, 256)) return LORA_ERR_WORKSPACE;
   auto st = static_cast<hipStream_t>(stream);
-  launch(sort_kernel, dim3(g.sort_blocks), dim3(1024), 0, st, ids, static_cast<int>(T), static_cast<int>(V), g.bins,
-         g.order, g.keys, g.start);
+  launch(sort_kernel, dim3(1 << g.map.blocks_log2), dim3(1024), 0, st, ids, static_cast<int>(T), static_cast<int>(V),
+         g.map, g.order, g.keys, g.start, g.count);
   const bool add = accumulate != 0;
   if (dy->dtype == LORA_F32) return run_grad<float, float>(g, dy, scale, dtable, add, st);
   if (dtable->dtype == LORA_F32) return run_grad<uint16_t, float>(g, dy, scale, dtable, add, st);

@@ -183,20 +183,19 @@ __global__ __launch_bounds__(256) void join_kernel(RowPieces<E> a, int64_t T, fl
 }
 
 // The same for up to kJoinRows rows in a workgroup of 1024 that goes on with
-// their log probabilities: it finds them in `lds`. Without pieces: in logp.
+// their log probabilities, which it finds in `lds`.
 constexpr int kJoinRows = 256;
 template <class E>
-__device__ __forceinline__ const float* join_rows(const RowPieces<E>& a, int64_t T, float* logp, float* lds) {
-  if (a.part == nullptr) return logp;
+__device__ __forceinline__ void join_rows(const RowPieces<E>& a, int64_t T, float* logp, float* lds) {
   const int row = threadIdx.x >> 2, sub = threadIdx.x & 3;
   const float lp = join_row(a, row, T, sub, logp);
   if (sub == 0) lds[row] = lp;
   __syncthreads();
-  return lds;
 }
 
 // ---------------------------------------------------------------------------
-// losses on the log probabilities (one workgroup: a few values per token)
+// losses on the log probabilities (one workgroup: a few values per token),
+// which with JOIN are joined from their rows' pieces first
 // ---------------------------------------------------------------------------
 
 // The sum of v over the workgroup's 16 waves, in the order of the waves.
@@ -215,15 +214,16 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // eps - sigmoid(-z). Sequence sums and z are float64: z is a small
 // difference of long sums. One wave per pair; its two sequences' tokens get
 // the coefficients beta * dz / pairs and minus that.
-template <class E>
+template <class E, bool JOIN>
 __global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
                                                     const float* __restrict__ ref, float beta, float eps,
                                                     float* __restrict__ loss, float* __restrict__ seq_logp,
                                                     float* __restrict__ coef) {
   __shared__ double lds[16];
-  __shared__ float joined[kJoinRows];
-  const float* logp = join_rows(pieces, T, logp_out, joined);
+  __shared__ float joined[JOIN ? kJoinRows : 1];
+  if constexpr (JOIN) join_rows(pieces, T, logp_out, joined);
+  auto logp = [&](int64_t t) { return JOIN ? joined[t] : logp_out[t]; };
   const int lane = threadIdx.x & 63;
   auto offset = [&](int64_t i) -> int64_t {
     const int64_t o = offsets[i];
@@ -242,7 +242,8 @@ __global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* 
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       double v = 0.0;
-      for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) v += logp[t];
+#pragma unroll 4
+      for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) v += logp(t);
       s[k] = wave_sum(v);
       if (lane == 0 && seq_logp != nullptr) seq_logp[2 * p + k] = static_cast<float>(s[k]);
     }
@@ -286,18 +287,19 @@ __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, f
   return make_float2(w * l, w * d);
 }
 
-template <class E>
+template <class E, bool JOIN>
 __global__ __launch_bounds__(1024) void policy_kernel(RowPieces<E> pieces, float* logp_out, int64_t T, int64_t V,
                                                       PolicyArgs a, float* __restrict__ loss,
                                                       float* __restrict__ coef) {
   __shared__ double lds[16];
-  __shared__ float joined[kJoinRows];
-  const float* logp = join_rows(pieces, T, logp_out, joined);
+  __shared__ float joined[JOIN ? kJoinRows : 1];
+  if constexpr (JOIN) join_rows(pieces, T, logp_out, joined);
+  auto logp = [&](int64_t t) { return JOIN ? joined[t] : logp_out[t]; };
   double sum = 0.0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int y = a.targets[t];
     float2 v = make_float2(0.0f, 0.0f);
-    if (y >= 0 && y < V) v = policy_token(a, t, logp[t]);
+    if (y >= 0 && y < V) v = policy_token(a, t, logp(t));
     sum += v.x;
     if (coef != nullptr) coef[t] = v.y;
   }
@@ -570,7 +572,7 @@ static void run_join(const lora_mat* x, const int32_t* targets, float* logp, flo
 
 // Few rows are joined by the loss's own workgroup, which saves a launch (about
 // 3 us each); more rows are spread over the card by join_kernel.
-static bool join_in_loss(int64_t T, int64_t V) { return row_splits(T, V) > 1 && T <= kJoinRows; }
+static bool join_in_loss(int64_t T, int64_t V) { return T > 0 && T <= kJoinRows && row_splits(T, V) > 1; }
 
 static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;
@@ -665,7 +667,7 @@ extern "C" int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_o
   if (T < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(pref_kernel<float>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
+  launch(pref_kernel<float, false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
          const_cast<float*>(logp), T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss, seq_logp, coef);
   return launch_status();
 }
@@ -676,7 +678,7 @@ extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const l
   if (T < 0 || V < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(policy_kernel<float>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
+  launch(policy_kernel<float, false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
          const_cast<float*>(logp), T, V, policy_args(policy), loss, coef);
   return launch_status();
 }
@@ -712,9 +714,9 @@ extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, co
   if (T > 0 && !join) run_join(logits, targets, logp, l.stats, l, st);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(pref_kernel<E>, dim3(1), dim3(1024), 0, st,
-           join ? row_pieces<E>(logits, targets, l.stats, l) : RowPieces<E>{}, logp, T, seq_offsets, pairs, ref_logp,
-           beta, label_smoothing, loss, seq_logp, l.coef);
+    launch(join ? pref_kernel<E, true> : pref_kernel<E, false>, dim3(1), dim3(1024), 0, st,
+           row_pieces<E>(logits, targets, l.stats, l), logp, T, seq_offsets, pairs, ref_logp, beta, label_smoothing,
+           loss, seq_logp, l.coef);
   });
   if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
@@ -743,7 +745,7 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
   run_logp(logits, a.targets, logp, l.stats, l, st);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(policy_kernel<E>, dim3(1), dim3(1024), 0, st, row_pieces<E>(logits, a.targets, l.stats, l), logp, T, V, a,
+    launch(policy_kernel<E, true>, dim3(1), dim3(1024), 0, st, row_pieces<E>(logits, a.targets, l.stats, l), logp, T, V, a,
            loss, l.coef);
   });
   run_logit_grad(logits, a.targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);

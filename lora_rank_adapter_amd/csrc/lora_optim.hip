@@ -19,6 +19,7 @@
 //   table_kernel   table entries and the chunks' tensors
 //   begin_kernel   the step count and the constants that depend on it
 //   step_kernel    the update, 256 elements per wave at a time
+//   small_step_kernel  constants and update of a few chunks, one workgroup
 
 #include "lora_host.hpp"
 #include "lora_rows.hpp"
@@ -75,16 +76,20 @@ __global__ __launch_bounds__(256) void table_kernel(TableBatch batch, int first,
 }
 
 // The constants need powers in float64; one thread computes them once.
-__global__ void begin_kernel(void* table, int32_t* step, double lr, double beta1, double beta2, double decay,
-                             const float* lr_scale) {
-  const int t = *step + 1;
-  *step = t;
-  if (lr_scale != nullptr) lr *= (double)*lr_scale;
-  auto* h = static_cast<TableHead*>(table);
-  h->alpha = static_cast<float>(lr / (1.0 - pow(beta1, (double)t)));
-  h->inv_root = static_cast<float>(1.0 / sqrt(1.0 - pow(beta2, (double)t)));
-  h->decay = static_cast<float>(1.0 - lr * decay);
+struct BeginArgs {
+  int32_t* step;
+  double lr, beta1, beta2, decay;
+  const float* lr_scale;
+};
+__device__ __forceinline__ void begin(const BeginArgs& a, TableHead* h) {
+  const int t = *a.step + 1;
+  *a.step = t;
+  const double lr = a.lr_scale != nullptr ? a.lr * (double)*a.lr_scale : a.lr;
+  h->alpha = static_cast<float>(lr / (1.0 - pow(a.beta1, (double)t)));
+  h->inv_root = static_cast<float>(1.0 / sqrt(1.0 - pow(a.beta2, (double)t)));
+  h->decay = static_cast<float>(1.0 - lr * a.decay);
 }
+__global__ void begin_kernel(void* table, BeginArgs a) { begin(a, static_cast<TableHead*>(table)); }
 
 struct StepArgs {
   void *m, *v;
@@ -107,11 +112,12 @@ __device__ __forceinline__ float root(float v) {
 }
 
 __device__ __forceinline__ void adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
+  // the fused products are written out: a tensor's steps are the same bits in either kernel
   g *= k.gs;
-  m = a.b1 * m + a.c1 * g;
-  v = a.b2 * v + a.c2 * (g * g);
+  m = fmaf(a.b1, m, a.c1 * g);
+  v = fmaf(a.b2, v, a.c2 * (g * g));
   // the divisor is at least eps, or the root of a v above zero: no denormal, whose reciprocal would be lost
-  p = p * k.decay - k.alpha * m * __builtin_amdgcn_rcpf(root(v) * k.inv_root + a.eps);
+  p = fmaf(-(k.alpha * m), __builtin_amdgcn_rcpf(fmaf(root(v), k.inv_root, a.eps)), p * k.decay);
 }
 
 // four codes of one word as values, and back (rounded to nearest even)
@@ -188,34 +194,39 @@ __device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, bool vec, 
   }
 }
 
+// One wave updates a block of 256 elements of a tensor, 4 per lane: what it
+// loads, and the update from there.
 template <int BITS>
-__global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
-  const auto* h = static_cast<const TableHead*>(table);
-  // a table of other tensors than the states: leave everything as it is
-  if (h->magic != kTableMagic || h->tensors != n || h->elems != elems || blockIdx.x >= h->chunks) return;
-  const auto* map = reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
-  const TableEntry e = table_entries(table)[map[blockIdx.x]];
-  const StepConst k = {h->alpha, h->inv_root, h->decay, a.grad_scale != nullptr ? *a.grad_scale : 1.0f};
-  const int lane = threadIdx.x & 63;
-  const int64_t chunk = (int64_t)(blockIdx.x - e.first_chunk) * kChunk;
-#pragma unroll
-  for (int it = 0; it < kChunk / (4 * kStateBlock); ++it) {
-    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
-    if (block >= e.numel) break;
-    const int64_t i = block + lane * 4;  // in the tensor
-    const int64_t s = e.state + i;       // in the states
-    const int count = e.numel - i < 4 ? (e.numel - i < 0 ? 0 : (int)(e.numel - i)) : 4;
-    float p[4], g[4], m[4], v[4];
+struct Block {
+  int64_t i, s;  // the lane's first element, in the tensor and in the states
+  int count;     // its elements inside the tensor
+  float p[4], g[4], m[4], v[4];
+  uint32_t m_code, v_code;
+  float m_scale, v_scale;
+
+  __device__ __forceinline__ void load(const TableEntry& e, const StepArgs& a, int64_t block, int lane) {
+    i = block + lane * 4;
+    s = e.state + i;
+    count = e.numel - i < 4 ? (e.numel - i < 0 ? 0 : (int)(e.numel - i)) : 4;
     load4(e.param, e.param_bf16, i, e.vec, count, p);
     load4(e.grad, e.grad_bf16, i, e.vec, count, g);
     if constexpr (BITS == 8) {
-      fp8_values(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s), a.m_scale[s / kStateBlock], m);
-      fp8_values(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s), a.v_scale[s / kStateBlock], v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= v[j];
+      m_code = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
+      v_code = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
+      m_scale = a.m_scale[s / kStateBlock];
+      v_scale = a.v_scale[s / kStateBlock];
     } else {
       load4(a.m, false, s, true, 4, m);
       load4(a.v, false, s, true, 4, v);
+    }
+  }
+
+  __device__ __forceinline__ void update(const TableEntry& e, const StepConst& k, const StepArgs& a, int lane) {
+    if constexpr (BITS == 8) {
+      fp8_values(m_code, m_scale, m);
+      fp8_values(v_code, v_scale, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= v[j];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -228,18 +239,75 @@ __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64
     if constexpr (BITS == 8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = root(v[j]);
-      float ms, vs;
-      const uint32_t mc = quantise(m, false, &ms), vc = quantise(v, true, &vs);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = mc;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = vc;
+      m_code = quantise(m, false, &m_scale);
+      v_code = quantise(v, true, &v_scale);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = m_code;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = v_code;
       if (lane == 0) {
-        a.m_scale[s / kStateBlock] = ms;
-        a.v_scale[s / kStateBlock] = vs;
+        a.m_scale[s / kStateBlock] = m_scale;
+        a.v_scale[s / kStateBlock] = v_scale;
       }
     } else {
       store4(a.m, false, s, true, 4, m);
       store4(a.v, false, s, true, 4, v);
     }
+  }
+};
+
+// A table of other tensors than the states: leave everything as it is.
+__device__ __forceinline__ bool foreign(const TableHead* h, int64_t n, int64_t elems) {
+  return h->magic != kTableMagic || h->tensors != n || h->elems != elems;
+}
+__device__ __forceinline__ const int32_t* chunk_map(const void* table, int64_t n) {
+  return reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
+  const auto* h = static_cast<const TableHead*>(table);
+  if (foreign(h, n, elems) || blockIdx.x >= h->chunks) return;
+  const TableEntry e = table_entries(table)[chunk_map(table, n)[blockIdx.x]];
+  const StepConst k = {h->alpha, h->inv_root, h->decay, a.grad_scale != nullptr ? *a.grad_scale : 1.0f};
+  const int64_t chunk = (int64_t)(blockIdx.x - e.first_chunk) * kChunk;
+  const int lane = threadIdx.x & 63;
+  // all of a wave's loads go out before its first store
+  constexpr int kTimes = kChunk / (4 * kStateBlock);
+  Block<BITS> b[kTimes];
+#pragma unroll
+  for (int it = 0; it < kTimes; ++it) {
+    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
+    if (block < e.numel) b[it].load(e, a, block, lane);
+  }
+#pragma unroll
+  for (int it = 0; it < kTimes; ++it) {
+    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
+    if (block < e.numel) b[it].update(e, k, a, lane);
+  }
+}
+
+// A few chunks in one workgroup, which computes the constants itself: one
+// launch instead of two. Two adapter weights of 4096 elements: @@ us a step
+// against @@; beyond kSmall chunks one CU is too slow for the data.
+constexpr int kSmall = 8;
+
+template <int BITS>
+__global__ __launch_bounds__(1024) void small_step_kernel(void* table, int64_t n, int64_t elems, BeginArgs b,
+                                                          StepArgs a) {
+  __shared__ TableHead now;
+  if (threadIdx.x == 0) begin(b, &now);
+  __syncthreads();
+  const auto* h = static_cast<const TableHead*>(table);
+  if (foreign(h, n, elems)) return;
+  const StepConst k = {now.alpha, now.inv_root, now.decay, a.grad_scale != nullptr ? *a.grad_scale : 1.0f};
+  constexpr int kBlocks = kChunk / kStateBlock;  // of a chunk
+  for (int64_t u = wave_id(); u < h->chunks * kBlocks; u += 16) {
+    const int64_t c = u / kBlocks;
+    const TableEntry e = table_entries(table)[chunk_map(table, n)[c]];
+    const int64_t block = (c - e.first_chunk) * kChunk + (u % kBlocks) * kStateBlock;
+    if (block >= e.numel) continue;
+    Block<BITS> x;
+    x.load(e, a, block, threadIdx.x & 63);
+    x.update(e, k, a, threadIdx.x & 63);
   }
 }
 
@@ -336,11 +404,14 @@ extern "C" int lora_adamw_step(const lora_adamw_tensor* tensors, int64_t n, void
                       static_cast<float>(hyper->beta2), static_cast<float>(1.0 - hyper->beta2),
                       static_cast<float>(hyper->eps)};
   auto st = static_cast<hipStream_t>(stream);
-  launch(begin_kernel, dim3(1), dim3(1), 0, st, table, state->step, hyper->lr, hyper->beta1, hyper->beta2,
-         hyper->weight_decay, hyper->lr_scale);
-  if (state->bits == 8)
-    launch(step_kernel<8>, dim3(size.chunks), dim3(256), 0, st, table, n, size.elems, a);
-  else
-    launch(step_kernel<32>, dim3(size.chunks), dim3(256), 0, st, table, n, size.elems, a);
+  const BeginArgs b = {state->step, hyper->lr, hyper->beta1, hyper->beta2, hyper->weight_decay, hyper->lr_scale};
+  if (size.chunks <= kSmall) {
+    launch(state->bits == 8 ? small_step_kernel<8> : small_step_kernel<32>, dim3(1), dim3(1024), 0, st, table, n,
+           size.elems, b, a);
+    return launch_status();
+  }
+  launch(begin_kernel, dim3(1), dim3(1), 0, st, table, b);
+  launch(state->bits == 8 ? step_kernel<8> : step_kernel<32>, dim3(size.chunks), dim3(256), 0, st, table, n, size.elems,
+         a);
   return launch_status();
 }

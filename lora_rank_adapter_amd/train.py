@@ -12,10 +12,11 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import LoraAdamwHyper, LoraAdamwState, LoraAdamwTensor, LoraPolicy, check
-from .ops import _dtype_code, _ptr, _stream, mat
+from ._lib import LoraAdamwHyper, LoraAdamwState, LoraAdamwTensor, LoraPolicy, check, pack_mat
+from .ops import _DT, _dtype_code, _stream
 
 _I32, _F32 = torch.int32, torch.float32
+_data_ptr = torch.Tensor.data_ptr
 
 
 def _vector(name: str, t: torch.Tensor, n: int, dtype: torch.dtype, device: torch.device) -> int:
@@ -35,10 +36,14 @@ def _queue(device: torch.device):
     return _stream(device)
 
 
-def _matrix(name: str, t: torch.Tensor, device: torch.device):
+def _matrix(name: str, t: torch.Tensor, device: torch.device) -> bytes:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return ctypes.byref(mat(t))
+    row, col = t.stride()
+    return pack_mat(t.data_ptr(), _DT.get(t.dtype, -1), 0, shape[0], shape[1], row, col)
 
 
 def _given(workspace, need, device):
@@ -88,7 +93,7 @@ def lora_embed_grad(ids: torch.Tensor, dy: torch.Tensor, num_rows: int, scale: f
         raise ValueError(f"dtable has {dtable.shape[0]} rows, expected {num_rows}")
     ws, nbytes = _given(workspace, lib.lora_embed_grad_workspace_bytes(T, num_rows, D), dev)
     check("lora_embed_grad", lib.lora_embed_grad(p, _matrix("dy", dy, dev), float(scale),
-                                                 _matrix("dtable", dtable, dev), int(bool(accumulate)), _ptr(ws),
+                                                 _matrix("dtable", dtable, dev), int(bool(accumulate)), ws.data_ptr(),
                                                  nbytes, _queue(dev)))
     return dtable
 
@@ -109,7 +114,7 @@ def lora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
     logp = torch.empty(T, dtype=_F32, device=dev)
     stats = torch.empty((T, 2), dtype=_F32, device=dev)
     ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
-    check("lora_token_logp", lib.lora_token_logp(_matrix("logits", logits, dev), y, _ptr(logp), _ptr(stats), _ptr(ws),
+    check("lora_token_logp", lib.lora_token_logp(_matrix("logits", logits, dev), y, logp.data_ptr(), stats.data_ptr(), ws.data_ptr(),
                                                  nbytes, _queue(dev)))
     return logp, stats
 
@@ -133,8 +138,8 @@ def lora_pref_loss(logp: torch.Tensor, seq_offsets: torch.Tensor, ref_logp: torc
     coef = torch.empty(T, dtype=_F32, device=dev)
     check("lora_pref_loss", lib.lora_pref_loss(
         _vector("logp", logp, T, _F32, dev), T, _vector("seq_offsets", seq_offsets, 2 * pairs + 1, _I32, dev), pairs,
-        _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), _ptr(loss),
-        _ptr(seq), _ptr(coef), _queue(dev)))
+        _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), loss.data_ptr(),
+        seq.data_ptr(), coef.data_ptr(), _queue(dev)))
     return loss, seq, coef
 
 
@@ -159,7 +164,7 @@ def lora_policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_
     loss = torch.empty((), dtype=_F32, device=dev)
     coef = torch.empty(T, dtype=_F32, device=dev)
     check("lora_policy_loss", lib.lora_policy_loss(_vector("logp", logp, T, _F32, dev), T, int(vocab),
-                                                   ctypes.byref(args), _ptr(loss), _ptr(coef), _queue(dev)))
+                                                   ctypes.byref(args), loss.data_ptr(), coef.data_ptr(), _queue(dev)))
     return loss, coef
 
 
@@ -200,7 +205,7 @@ def lora_pref_step(logits: torch.Tensor, targets: torch.Tensor, seq_offsets: tor
         _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
         _vector("seq_offsets", seq_offsets, 2 * pairs + 1, _I32, dev), pairs,
         _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), float(grad_scale),
-        _ptr(loss), _ptr(seq), _ptr(logp), _matrix("dlogits", dlogits, dev), _ptr(ws), nbytes, _queue(dev)))
+        loss.data_ptr(), seq.data_ptr(), logp.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
     return loss, seq, logp, dlogits
 
 
@@ -220,8 +225,8 @@ def lora_policy_step(logits: torch.Tensor, targets: torch.Tensor, old_logp: torc
     logp = torch.empty(T, dtype=_F32, device=dev)
     ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
     check("lora_policy_step", lib.lora_policy_step(
-        _matrix("logits", logits, dev), ctypes.byref(args), float(grad_scale), _ptr(loss), _ptr(logp),
-        _matrix("dlogits", dlogits, dev), _ptr(ws), nbytes, _queue(dev)))
+        _matrix("logits", logits, dev), ctypes.byref(args), float(grad_scale), loss.data_ptr(), logp.data_ptr(),
+        _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
     return loss, logp, dlogits
 
 
@@ -292,16 +297,16 @@ class AdamW:
                                          _dtype_code(g))
         need = self._lib.lora_adamw_table_bytes(tensors, len(grads))
         table = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
-        check("lora_adamw_table", self._lib.lora_adamw_table(tensors, len(grads), _ptr(table), need,
+        check("lora_adamw_table", self._lib.lora_adamw_table(tensors, len(grads), table.data_ptr(), need,
                                                              _queue(self.device)))
         self.grads, self._tensors, self._table, self._table_bytes = grads, tensors, table, need
         self._held = self.params + grads + [s for s in self.shadows if s is not None]
-        self._addresses = [t.data_ptr() for t in self._held]
+        self._addresses = list(map(_data_ptr, self._held))
 
     def step(self, lr_scale: torch.Tensor | None = None, grad_scale: torch.Tensor | None = None) -> None:
         """One step on the current stream. lr_scale, grad_scale: None or float32 [] tensors on the device that
         multiply lr and every gradient (a schedule, a clipping factor; read when the step runs)."""
-        if [t.data_ptr() for t in self._held] != self._addresses:
+        if list(map(_data_ptr, self._held)) != self._addresses:
             raise ValueError("a bound tensor's memory moved: bind the gradients again")
         if any(self.state[k].data_ptr() != a for k, a in self._addresses_of_state.items()):
             raise ValueError("a state tensor was replaced: copy into it instead")
@@ -309,6 +314,6 @@ class AdamW:
         hyper = LoraAdamwHyper(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                                None if lr_scale is None else _vector("lr_scale", lr_scale, 1, _F32, dev),
                                None if grad_scale is None else _vector("grad_scale", grad_scale, 1, _F32, dev))
-        check("lora_adamw_step", self._lib.lora_adamw_step(self._tensors, len(self.params), _ptr(self._table),
+        check("lora_adamw_step", self._lib.lora_adamw_step(self._tensors, len(self.params), self._table.data_ptr(),
                                                            self._table_bytes, ctypes.byref(self._state),
                                                            ctypes.byref(hyper), _queue(dev)))

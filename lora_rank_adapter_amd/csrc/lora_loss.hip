@@ -21,6 +21,7 @@
 //   policy_row_kernel a row from its statistics to its gradient (policy loss)
 //   sum_kernel        the sum of the tokens' losses
 //   logit_grad_kernel the gradient's rows from the statistics and coefficients
+//   policy_grad_kernel  the same from the pieces of few long rows, and the policy loss
 
 #include <type_traits>
 
@@ -72,7 +73,7 @@ template <class E>
 __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
                                                    const int32_t* __restrict__ targets, int V, int splits, int piece,
                                                    float* __restrict__ logp, float2* __restrict__ stats,
-                                                   float2* __restrict__ part) {
+                                                   float2* __restrict__ part, float* __restrict__ hit) {
   constexpr int N = Vec<E>::N, U = 4;
   __shared__ MaxSum waves[4];
   const int64_t row = blockIdx.x / (unsigned)splits;
@@ -127,6 +128,8 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   for (int w = 1; w < 4; ++w) r = join(r, waves[w]);
   if (splits > 1) {
     part[row * splits + sp] = make_float2(r.m, r.s);
+    // kept beside the pieces: the logits may be overwritten while they are joined
+    if (y >= lo && y - lo < n) hit[row] = Vec<E>::value(src[y]);
   } else {
     logp[row] = target_logp(Vec<E>::value(src[y]), r);
     stats[row] = make_float2(r.m, r.s);
@@ -135,23 +138,27 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
 
 // What remains of the softmax once logp_kernel has written `splits` pieces of
 // each row: four lanes join a row's.
-template <class E>
 struct RowPieces {
-  const E* x;
-  int64_t stride;
   const int32_t* targets;
-  int V, splits;
+  int64_t V;
+  int splits;
   const float2* part;
+  const float* hit;  // the rows' target logits
   float2* stats;
 };
 
-// The log probability of `row` for the lane of its four whose `sub` is 0.
-template <class E>
-__device__ __forceinline__ float join_row(const RowPieces<E>& a, int64_t row, int64_t T, int sub, float* logp) {
+struct Joined {
+  bool live;  // the row is there and not masked
+  MaxSum r;
+  float logp;
+};
+
+// Row `row` for lane `sub` of its four (all of them get the result).
+__device__ __forceinline__ Joined join_row(const RowPieces& a, int64_t row, int64_t T, int sub) {
   constexpr int U = 8;
   const int y = row < T ? a.targets[row] : -1;
   const bool live = y >= 0 && y < a.V;
-  const float hit = live ? Vec<E>::value(a.x[row * a.stride + y]) : 0.0f;
+  const float hit = live ? a.hit[row] : 0.0f;
   MaxSum r{-INFINITY, 0.0f};
   for (int sp = sub; sp < a.splits; sp += 4 * U) {
     float2 v[U];
@@ -169,42 +176,46 @@ __device__ __forceinline__ float join_row(const RowPieces<E>& a, int64_t row, in
   }
   r = join(r, MaxSum{__shfl_xor(r.m, 1, 64), __shfl_xor(r.s, 1, 64)});
   r = join(r, MaxSum{__shfl_xor(r.m, 2, 64), __shfl_xor(r.s, 2, 64)});
-  const float lp = live ? target_logp(hit, r) : 0.0f;
-  if (sub == 0 && row < T) {
-    logp[row] = lp;
-    a.stats[row] = live ? make_float2(r.m, r.s) : make_float2(0.0f, 1.0f);
-  }
-  return lp;
+  return {live, r, live ? target_logp(hit, r) : 0.0f};
 }
 
-template <class E>
-__global__ __launch_bounds__(256) void join_kernel(RowPieces<E> a, int64_t T, float* __restrict__ logp) {
-  join_row(a, (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2), T, threadIdx.x & 3, logp);
+__device__ __forceinline__ void put_joined(const RowPieces& a, int64_t row, int64_t T, const Joined& v, float* logp) {
+  if (row >= T) return;
+  logp[row] = v.logp;
+  a.stats[row] = v.live ? make_float2(v.r.m, v.r.s) : make_float2(0.0f, 1.0f);
+}
+
+__global__ __launch_bounds__(256) void join_kernel(RowPieces a, int64_t T, float* __restrict__ logp) {
+  const int64_t row = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
+  const Joined v = join_row(a, row, T, threadIdx.x & 3);
+  if ((threadIdx.x & 3) == 0) put_joined(a, row, T, v, logp);
 }
 
 // The same for up to kJoinRows rows in a workgroup of 1024 that goes on with
 // their log probabilities, which it finds in `lds`.
 constexpr int kJoinRows = 256;
-template <class E>
-__device__ __forceinline__ void join_rows(const RowPieces<E>& a, int64_t T, float* logp, float* lds) {
-  const int row = threadIdx.x >> 2, sub = threadIdx.x & 3;
-  const float lp = join_row(a, row, T, sub, logp);
-  if (sub == 0) lds[row] = lp;
+__device__ __forceinline__ void join_rows(const RowPieces& a, int64_t T, float* logp, float* lds) {
+  const int row = threadIdx.x >> 2;
+  const Joined v = join_row(a, row, T, threadIdx.x & 3);
+  if ((threadIdx.x & 3) == 0) {
+    put_joined(a, row, T, v, logp);
+    lds[row] = v.logp;
+  }
   __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// losses on the log probabilities (one workgroup: a few values per token),
-// which with JOIN are joined from their rows' pieces first
+// losses on the log probabilities (one workgroup: a few values per token)
 // ---------------------------------------------------------------------------
 
-// The sum of v over the workgroup's 16 waves, in the order of the waves.
+// The sum of v over the workgroup's waves, in their order.
+template <int WAVES = 16>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
   v = wave_sum(v);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
   double total = 0.0;
-  for (int w = 0; w < 16; ++w) total += lds[w];
+  for (int w = 0; w < WAVES; ++w) total += lds[w];
   __syncthreads();
   return total;
 }
@@ -213,9 +224,10 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // -(1 - eps) log sigmoid(z) - eps log sigmoid(-z), whose derivative by z is
 // eps - sigmoid(-z). Sequence sums and z are float64: z is a small
 // difference of long sums. One wave per pair; its two sequences' tokens get
-// the coefficients beta * dz / pairs and minus that.
-template <class E, bool JOIN>
-__global__ __launch_bounds__(1024) void pref_kernel(RowPieces<E> pieces, float* logp_out, int64_t T,
+// the coefficients beta * dz / pairs and minus that. With JOIN the log
+// probabilities are joined from their rows' pieces first.
+template <bool JOIN>
+__global__ __launch_bounds__(1024) void pref_kernel(RowPieces pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
                                                     const float* __restrict__ ref, float beta, float eps,
                                                     float* __restrict__ loss, float* __restrict__ seq_logp,
@@ -287,19 +299,15 @@ __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, f
   return make_float2(w * l, w * d);
 }
 
-template <class E, bool JOIN>
-__global__ __launch_bounds__(1024) void policy_kernel(RowPieces<E> pieces, float* logp_out, int64_t T, int64_t V,
+__global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ logp, int64_t T, int64_t V,
                                                       PolicyArgs a, float* __restrict__ loss,
                                                       float* __restrict__ coef) {
   __shared__ double lds[16];
-  __shared__ float joined[JOIN ? kJoinRows : 1];
-  if constexpr (JOIN) join_rows(pieces, T, logp_out, joined);
-  auto logp = [&](int64_t t) { return JOIN ? joined[t] : logp_out[t]; };
   double sum = 0.0;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int y = a.targets[t];
     float2 v = make_float2(0.0f, 0.0f);
-    if (y >= 0 && y < V) v = policy_token(a, t, logp(t));
+    if (y >= 0 && y < V) v = policy_token(a, t, logp[t]);
     sum += v.x;
     if (coef != nullptr) coef[t] = v.y;
   }
@@ -438,33 +446,31 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ ter
 constexpr int kGradVecs = 256;
 
 template <class E>
-__global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(const E* x, int64_t stride,
-                                                               const int32_t* __restrict__ targets,
-                                                               const float2* __restrict__ stats,
-                                                               const float* __restrict__ coef,
-                                                               const float* __restrict__ grad_out, float scale, int V,
-                                                               int pieces, E* dx, int64_t dx_stride) {
+struct GradArgs {
+  const E* x;
+  int64_t stride;
+  E* dx;  // may be x: a vector is stored by the lane that loaded it
+  int64_t dx_stride;
+  int V, pieces;
+};
+
+// One piece of row `row`: coefficient c, statistics st; zeros for a masked row.
+template <class E>
+__device__ __forceinline__ void grad_piece(const GradArgs<E>& a, int64_t row, int piece, int y, float c, float2 st) {
   constexpr int N = Vec<E>::N;
-  const int64_t row = blockIdx.x / (unsigned)pieces;
-  const int lo = (int)(blockIdx.x % (unsigned)pieces) * kGradVecs * N;
-  const int n = V - lo < kGradVecs * N ? V - lo : kGradVecs * N;
+  const int lo = piece * kGradVecs * N;
+  const int n = a.V - lo < kGradVecs * N ? a.V - lo : kGradVecs * N;
   const int tid = threadIdx.x;
-  const int y = targets[row];
-  const bool live = y >= 0 && y < V;
-  // dx may be x: no restrict on it, and a vector is stored by the lane that loaded it
-  const E* p = x + row * stride + lo;
-  E* q = dx + row * dx_stride + lo;
+  const E* p = a.x + row * a.stride + lo;
+  E* q = a.dx + row * a.dx_stride + lo;
   const int vecs = n / N;
   const int rest = vecs * N + tid;  // the row's last elements, one per lane
-  if (!live) {
+  if (y < 0 || y >= a.V) {
     const typename Vec<E>::type zero = {0u, 0u, 0u, 0u};
     if (tid < vecs) vstore_nt(q + tid * N, zero);
     if (rest < n) q[rest] = Vec<E>::round(0.0f);
     return;
   }
-  float c = coef[row] * scale;
-  if (grad_out != nullptr) c *= *grad_out;
-  const float2 st = stats[row];
   const float m = at_max(st.x), cs = -c / st.y;
   const int hit = y - lo;
   if (tid < vecs) {
@@ -483,6 +489,46 @@ __global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(const E* x, int64
     const float g = cs * exp2_raw((Vec<E>::value(p[rest]) - m) * kLog2e);
     q[rest] = Vec<E>::round(rest == hit ? g + c : g);
   }
+}
+
+template <class E>
+__global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(GradArgs<E> a, const int32_t* __restrict__ targets,
+                                                               const float2* __restrict__ stats,
+                                                               const float* __restrict__ coef,
+                                                               const float* __restrict__ grad_out, float scale) {
+  const int64_t row = blockIdx.x / (unsigned)a.pieces;
+  float c = coef[row] * scale;
+  if (grad_out != nullptr) c *= *grad_out;
+  grad_piece(a, row, blockIdx.x % (unsigned)a.pieces, targets[row], c, stats[row]);
+}
+
+// The second half of a policy step by pieces: every workgroup joins the
+// pieces of its row and finds its coefficient itself, and one more at the end
+// of the grid sums the rows' losses, so that nothing stands between the two
+// launches (40 rows of 128256: 23 us a call, with a kernel between them 25).
+template <class E>
+__global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, RowPieces pieces, int64_t T,
+                                                                PolicyArgs policy, float scale,
+                                                                float* __restrict__ loss, float* __restrict__ logp) {
+  const int sub = threadIdx.x & 3;
+  const int64_t row = blockIdx.x / (unsigned)a.pieces;
+  if (row == T) {
+    __shared__ double lds[kGradVecs / 64];
+    double sum = 0.0;
+    for (int64_t t = threadIdx.x >> 2; t - (threadIdx.x >> 2) < T; t += kGradVecs / 4) {
+      const Joined v = join_row(pieces, t, T, sub);
+      if (!v.live || sub != 0) continue;
+      sum += policy_token(policy, t, v.logp).x;
+    }
+    sum = block_sum<kGradVecs / 64>(sum, lds);
+    if (threadIdx.x == 0) *loss = static_cast<float>(sum);
+    return;
+  }
+  const int piece = blockIdx.x % (unsigned)a.pieces;
+  const Joined v = join_row(pieces, row, T, sub);
+  if (piece == 0 && threadIdx.x == 0) logp[row] = v.logp;
+  const float c = v.live ? policy_token(policy, row, v.logp).y * scale : 0.0f;
+  grad_piece(a, row, piece, policy.targets[row], c, make_float2(v.r.m, v.r.s));
 }
 
 // ---------------------------------------------------------------------------
@@ -504,7 +550,7 @@ static int row_splits(int64_t T, int64_t V) {
 
 struct LossPlan {
   float2 *stats, *part;
-  float* coef;
+  float *hit, *coef;
   size_t bytes;
 };
 
@@ -512,6 +558,7 @@ static LossPlan plan_loss(int64_t T, int64_t V, void* ws) {
   LossPlan l{};
   Carver w(ws);
   l.part = static_cast<float2*>(w.take(row_splits(T, V) > 1 ? T * row_splits(T, V) * sizeof(float2) : 0));
+  l.hit = static_cast<float*>(w.take(row_splits(T, V) > 1 ? T * sizeof(float) : 0));
   l.stats = static_cast<float2*>(w.take(T * sizeof(float2)));
   l.coef = static_cast<float*>(w.take(T * sizeof(float)));
   l.bytes = w.used;
@@ -541,10 +588,8 @@ static void by_type(const lora_mat* x, F f) {
     f(static_cast<uint16_t*>(nullptr));
 }
 
-template <class E>
-static RowPieces<E> row_pieces(const lora_mat* x, const int32_t* targets, float2* stats, const LossPlan& l) {
-  return {static_cast<const E*>(x->ptr), x->stride_row, targets, static_cast<int>(x->cols), row_splits(x->rows, x->cols),
-          l.part, stats};
+static RowPieces row_pieces(const lora_mat* x, const int32_t* targets, float2* stats, const LossPlan& l) {
+  return {targets, x->cols, row_splits(x->rows, x->cols), l.part, l.hit, stats};
 }
 
 // Statistics of the rows, or of their pieces.
@@ -556,18 +601,14 @@ static void run_logp(const lora_mat* x, const int32_t* targets, float* logp, flo
     using E = std::remove_pointer_t<decltype(e)>;
     const int piece = static_cast<int>(round_up(ceil_div(V, splits), Vec<E>::N));
     launch(logp_kernel<E>, dim3(x->rows * splits), dim3(256), 0, st, (const E*)x->ptr, x->stride_row, targets, V,
-           splits, piece, logp, stats, l.part);
+           splits, piece, logp, stats, l.part, l.hit);
   });
 }
 
 static void run_join(const lora_mat* x, const int32_t* targets, float* logp, float2* stats, const LossPlan& l,
                      hipStream_t st) {
   if (row_splits(x->rows, x->cols) == 1) return;
-  by_type(x, [&](auto* e) {
-    using E = std::remove_pointer_t<decltype(e)>;
-    launch(join_kernel<E>, dim3(ceil_div(x->rows, 64)), dim3(256), 0, st, row_pieces<E>(x, targets, stats, l), x->rows,
-           logp);
-  });
+  launch(join_kernel, dim3(ceil_div(x->rows, 64)), dim3(256), 0, st, row_pieces(x, targets, stats, l), x->rows, logp);
 }
 
 // Few rows are joined by the loss's own workgroup, which saves a launch (about
@@ -579,17 +620,23 @@ static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->dtype != x->dtype) return LORA_ERR_DTYPE;
   if (int e = check_logits(dx)) return e;
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  return x->rows * pieces > 0x7FFFFFFF ? LORA_ERR_LIMIT : LORA_OK;
+  return x->rows * pieces >= 0x7FFFFFFF ? LORA_ERR_LIMIT : LORA_OK;
+}
+
+template <class E>
+static GradArgs<E> grad_args(const lora_mat* x, const lora_mat* dx) {
+  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * Vec<E>::N);
+  return {static_cast<const E*>(x->ptr), x->stride_row,          static_cast<E*>(dx->ptr),
+          dx->stride_row,                static_cast<int>(x->cols), static_cast<int>(pieces)};
 }
 
 static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* coef,
                            const float* grad_out, float scale, const lora_mat* dx, hipStream_t st) {
-  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(logit_grad_kernel<E>, dim3(x->rows * pieces), dim3(256), 0, st, (const E*)x->ptr, x->stride_row, targets,
-           stats, coef, grad_out, scale, static_cast<int>(x->cols), static_cast<int>(pieces),
-           static_cast<E*>(dx->ptr), dx->stride_row);
+    const GradArgs<E> a = grad_args<E>(x, dx);
+    launch(logit_grad_kernel<E>, dim3(x->rows * a.pieces), dim3(kGradVecs), 0, st, a, targets, stats, coef, grad_out,
+           scale);
   });
 }
 
@@ -667,7 +714,7 @@ extern "C" int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_o
   if (T < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(pref_kernel<float, false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
+  launch(pref_kernel<false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces{},
          const_cast<float*>(logp), T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss, seq_logp, coef);
   return launch_status();
 }
@@ -678,8 +725,8 @@ extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const l
   if (T < 0 || V < 0) return LORA_ERR_SHAPE;
   if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
-  launch(policy_kernel<float, false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces<float>{},
-         const_cast<float*>(logp), T, V, policy_args(policy), loss, coef);
+  launch(policy_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, V, policy_args(policy),
+         loss, coef);
   return launch_status();
 }
 
@@ -712,12 +759,9 @@ extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, co
   if (T > 0) run_logp(logits, targets, logp, l.stats, l, st);
   const bool join = join_in_loss(T, V);
   if (T > 0 && !join) run_join(logits, targets, logp, l.stats, l, st);
-  by_type(logits, [&](auto* e) {
-    using E = std::remove_pointer_t<decltype(e)>;
-    launch(join ? pref_kernel<E, true> : pref_kernel<E, false>, dim3(1), dim3(1024), 0, st,
-           row_pieces<E>(logits, targets, l.stats, l), logp, T, seq_offsets, pairs, ref_logp, beta, label_smoothing,
-           loss, seq_logp, l.coef);
-  });
+  launch(join ? pref_kernel<true> : pref_kernel<false>, dim3(1), dim3(1024), 0, st,
+         row_pieces(logits, targets, l.stats, l), logp, T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss,
+         seq_logp, l.coef);
   if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
 }
@@ -745,9 +789,9 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
   run_logp(logits, a.targets, logp, l.stats, l, st);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(policy_kernel<E, true>, dim3(1), dim3(1024), 0, st, row_pieces<E>(logits, a.targets, l.stats, l), logp, T, V, a,
-           loss, l.coef);
+    const GradArgs<E> g = grad_args<E>(logits, dlogits);
+    launch(policy_grad_kernel<E>, dim3(T * g.pieces + 1), dim3(kGradVecs), 0, st, g,
+           row_pieces(logits, a.targets, nullptr, l), T, a, grad_scale, loss, logp);
   });
-  run_logit_grad(logits, a.targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
 }

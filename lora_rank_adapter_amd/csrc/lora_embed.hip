@@ -51,16 +51,17 @@ template <class E, class O, int U>
 __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ ids, int64_t T,
                                                     const E* __restrict__ table, int64_t table_stride, int64_t V,
                                                     int64_t D, float scale, O* __restrict__ out, int64_t out_stride,
-                                                    int lanes_log2) {
+                                                    int lanes_log2, unsigned pieces) {
   constexpr int N = Vec<O>::N;
   const int lanes = 1 << lanes_log2;
-  const int64_t t = (int64_t)blockIdx.x * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
+  // a row's pieces follow each other: the grid writes in the order of the addresses
+  const int64_t t = (int64_t)(blockIdx.x / pieces) * (256 >> lanes_log2) + (threadIdx.x >> lanes_log2);
   if (t >= T) return;
   const int64_t id = ids[t];
   const bool live = id >= 0 && id < V;
   const E* src = table + (live ? id : 0) * table_stride;
   O* dst = out + t * out_stride;
-  const int64_t c0 = ((int64_t)blockIdx.y * U * lanes + (threadIdx.x & (lanes - 1))) * N;
+  const int64_t c0 = ((int64_t)(blockIdx.x % pieces) * U * lanes + (threadIdx.x & (lanes - 1))) * N;
   float f[U][N];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t* __restrict__ 
 // While counting, a wave lists its workgroup's tokens in shared memory and
 // places them from there, 64 at a step. Reading the ids again instead, a
 // load would wait for the stores of the steps before it: 16384 tokens over
-// 128256 ids then take 19 us, from the list @@ us. A wave with more than
+// 128256 ids take 19 us that way, 9 from the list. A wave with more than
 // kList of its tokens in one workgroup's ids reads again.
 // ---------------------------------------------------------------------------
 // How ids are shared out: blocks_log2 of the workgroups, `bins` ids to each.
@@ -521,14 +522,15 @@ extern "C" int lora_embed(const int32_t* ids, const lora_mat* table, float scale
   const int64_t steps = ceil_div(D, int64_t(item) << ll);
   // U vectors of a row per lane where the row has them and the workgroups still fill the card
   const int u = steps >= 4 && blocks >= 512 ? 4 : steps >= 2 && blocks >= 512 ? 2 : 1;
-  if (blocks > kMaxGrid || ceil_div(steps, u) > 65535) return LORA_ERR_LIMIT;
-  const dim3 grid(blocks, ceil_div(steps, u));
+  const int64_t pieces = ceil_div(steps, u);
+  if (blocks > kMaxGrid || pieces > kMaxGrid || blocks * pieces > kMaxGrid) return LORA_ERR_LIMIT;
   auto st = static_cast<hipStream_t>(stream);
   auto go = [&](auto* e, auto* o) {
     using E = std::remove_pointer_t<decltype(e)>;
     using O = std::remove_pointer_t<decltype(o)>;
-    launch(u == 4 ? embed_kernel<E, O, 4> : u == 2 ? embed_kernel<E, O, 2> : embed_kernel<E, O, 1>, grid, dim3(256),
-           0, st, ids, T, (const E*)e, table->stride_row, V, D, scale, o, out->stride_row, ll);
+    launch(u == 4 ? embed_kernel<E, O, 4> : u == 2 ? embed_kernel<E, O, 2> : embed_kernel<E, O, 1>, dim3(blocks * pieces), dim3(256),
+           0, st, ids, T, (const E*)e, table->stride_row, V, D, scale, o, out->stride_row, ll,
+           static_cast<unsigned>(pieces));
   };
   if (table->dtype == LORA_F32)
     go(static_cast<float*>(table->ptr), static_cast<float*>(out->ptr));

@@ -21,6 +21,13 @@ Ops (the addressing arrays are passed as the tensors of lora_addressing):
   lora_bwd_dx_da_accumulate_(xt, dy, lora_B, lora_A, scale, dx) -> dA  [dx += scale * (dy @ lora_B) @ lora_A]
   lora_bwd_db(lora_A, xt, dy, scale) -> dB
   lora_delta(x, A_w, B_w, scale) -> scale * (x @ A_w^T) @ B_w^T  (float32, differentiable)
+  embed(ids, table, scale, dtype) -> scale * table[ids]     (differentiable in table)
+  embed_grad(ids, dy, num_rows, scale, dtype) -> dtable
+  token_logp(logits, targets) -> (logp, stats)              (logp differentiable in logits)
+  logit_grad(logits, targets, stats, coef) -> dlogits
+  pref_loss(logp, seq_offsets, ref_logp, beta, label_smoothing) -> (loss, seq_logp, coef)
+  policy_loss(logp, targets, vocab, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef)
+    -> (loss, coef)                                         (both losses differentiable in logp)
 
 h from shrink and gather_shrink is zero where the op leaves it unspecified
 (inactive tokens, columns past a slot's rank), and sorted_tokens from
@@ -28,13 +35,14 @@ addressing is -1 past the active tokens, so every output is fully defined. lora_
 weights in nn.Linear layout (A_w r x K, B_w L x r); its backward casts the
 incoming float32 gradient to x's dtype for the backward kernels (which take dy
 in the input dtype) and returns gradients in the dtypes and layouts of x, A_w
-and B_w.
+and B_w. The losses' other outputs (stats, seq_logp, coef) have no gradient: asking
+for one raises.
 """
 from __future__ import annotations
 
 import torch
 
-from . import ops
+from . import ops, train
 
 _NS = "lora_amd"
 
@@ -198,3 +206,129 @@ def _delta_backward(ctx, grad):
 
 
 torch.library.register_autograd(f"{_NS}::lora_delta", _delta_backward, setup_context=_delta_setup)
+
+
+# ---------------------------------------------------------------------------
+# the operators of a training step
+# ---------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t in a layout that the library's matrices take (gradients of sums and broadcasts come expanded)."""
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
+def _no_grad(name: str, *grads) -> None:
+    if any(g is not None for g in grads):
+        raise RuntimeError(f"{name} has no gradient: detach it")
+
+
+@torch.library.custom_op(f"{_NS}::embed", mutates_args=(), device_types="cuda")
+def embed(ids: torch.Tensor, table: torch.Tensor, scale: float, dtype: torch.dtype) -> torch.Tensor:
+    return train.lora_embed(ids, table, scale, dtype=dtype)
+
+
+@embed.register_fake
+def _(ids, table, scale, dtype):
+    return table.new_empty((ids.shape[0], table.shape[1]), dtype=dtype)
+
+
+@torch.library.custom_op(f"{_NS}::embed_grad", mutates_args=(), device_types="cuda")
+def embed_grad(ids: torch.Tensor, dy: torch.Tensor, num_rows: int, scale: float, dtype: torch.dtype) -> torch.Tensor:
+    return train.lora_embed_grad(ids, dy, num_rows, scale, dtype=dtype)
+
+
+@embed_grad.register_fake
+def _(ids, dy, num_rows, scale, dtype):
+    return dy.new_empty((num_rows, dy.shape[1]), dtype=dtype)
+
+
+def _embed_setup(ctx, inputs, output):
+    ids, table, scale, _ = inputs
+    ctx.save_for_backward(ids)
+    ctx.rows, ctx.dtype, ctx.scale = table.shape[0], table.dtype, scale
+
+
+def _embed_backward(ctx, grad):
+    ids, = ctx.saved_tensors
+    dtype = ctx.dtype if grad.dtype is ctx.dtype else torch.float32
+    return None, torch.ops.lora_amd.embed_grad(ids, _rows(grad), ctx.rows, ctx.scale, dtype).to(ctx.dtype), None, None
+
+
+torch.library.register_autograd(f"{_NS}::embed", _embed_backward, setup_context=_embed_setup)
+
+
+@torch.library.custom_op(f"{_NS}::token_logp", mutates_args=(), device_types="cuda")
+def token_logp(logits: torch.Tensor, targets: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    return train.lora_token_logp(logits, targets)
+
+
+@token_logp.register_fake
+def _(logits, targets):
+    T = logits.shape[0]
+    return logits.new_empty(T, dtype=torch.float32), logits.new_empty((T, 2), dtype=torch.float32)
+
+
+@torch.library.custom_op(f"{_NS}::logit_grad", mutates_args=(), device_types="cuda")
+def logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, coef: torch.Tensor) -> torch.Tensor:
+    return train.lora_logit_grad(logits, targets, stats, coef)
+
+
+@logit_grad.register_fake
+def _(logits, targets, stats, coef):
+    return logits.new_empty(logits.shape)
+
+
+def _logp_setup(ctx, inputs, output):
+    ctx.save_for_backward(*inputs, output[1])
+    ctx.set_materialize_grads(False)
+
+
+def _logp_backward(ctx, grad, grad_stats):
+    _no_grad("stats", grad_stats)
+    if grad is None:
+        return None, None
+    logits, targets, stats = ctx.saved_tensors
+    return torch.ops.lora_amd.logit_grad(logits, targets, stats, grad.contiguous()), None
+
+
+torch.library.register_autograd(f"{_NS}::token_logp", _logp_backward, setup_context=_logp_setup)
+
+
+@torch.library.custom_op(f"{_NS}::pref_loss", mutates_args=(), device_types="cuda")
+def pref_loss(logp: torch.Tensor, seq_offsets: torch.Tensor, ref_logp: torch.Tensor, beta: float,
+              label_smoothing: float) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return train.lora_pref_loss(logp, seq_offsets, ref_logp, beta, label_smoothing)
+
+
+@pref_loss.register_fake
+def _(logp, seq_offsets, ref_logp, beta, label_smoothing):
+    return logp.new_empty(()), logp.new_empty(ref_logp.shape[0]), logp.new_empty(logp.shape[0])
+
+
+@torch.library.custom_op(f"{_NS}::policy_loss", mutates_args=(), device_types="cuda")
+def policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_logp: torch.Tensor,
+                advantages: torch.Tensor, weights: torch.Tensor, clip_low: float, clip_high: float,
+                ref_logp: torch.Tensor | None, kl_coef: float) -> tuple[torch.Tensor, torch.Tensor]:
+    return train.lora_policy_loss(logp, targets, vocab, old_logp, advantages, weights, clip_low, clip_high, ref_logp,
+                                  kl_coef)
+
+
+@policy_loss.register_fake
+def _(logp, targets, vocab, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef):
+    return logp.new_empty(()), logp.new_empty(logp.shape[0])
+
+
+def _loss_setup(ctx, inputs, output):
+    ctx.save_for_backward(output[-1])
+    ctx.inputs = len(inputs)
+    ctx.set_materialize_grads(False)
+
+
+def _loss_backward(ctx, grad, *others):
+    _no_grad("what a loss returns beside the loss", *others)
+    coef, = ctx.saved_tensors
+    return (None if grad is None else grad * coef,) + (None,) * (ctx.inputs - 1)
+
+
+torch.library.register_autograd(f"{_NS}::pref_loss", _loss_backward, setup_context=_loss_setup)
+torch.library.register_autograd(f"{_NS}::policy_loss", _loss_backward, setup_context=_loss_setup)

@@ -223,56 +223,93 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // z = beta * ((S_c - ref_c) - (S_r - ref_r)); loss = mean of
 // -(1 - eps) log sigmoid(z) - eps log sigmoid(-z), whose derivative by z is
 // eps - sigmoid(-z). Sequence sums and z are float64: z is a small
-// difference of long sums. One wave per pair; its two sequences' tokens get
-// the coefficients beta * dz / pairs and minus that. With JOIN the log
-// probabilities are joined from their rows' pieces first.
+// difference of long sums. 64 pairs at a time: each wave sums sequences (or,
+// with fewer than 8 pairs, a part of one), 64 lanes take a pair each, and the
+// waves give their tokens the coefficients beta * dz / pairs and minus that.
+// With JOIN the log probabilities are joined from their rows' pieces first.
 template <bool JOIN>
 __global__ __launch_bounds__(1024) void pref_kernel(RowPieces pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
                                                     const float* __restrict__ ref, float beta, float eps,
                                                     float* __restrict__ loss, float* __restrict__ seq_logp,
                                                     float* __restrict__ coef) {
+  constexpr int kBatch = 64;
   __shared__ double lds[16];
+  __shared__ double sums[2 * kBatch];  // of sequences, or of the parts of each
+  __shared__ float slope[kBatch];
   __shared__ float joined[JOIN ? kJoinRows : 1];
   if constexpr (JOIN) join_rows(pieces, T, logp_out, joined);
   auto logp = [&](int64_t t) { return JOIN ? joined[t] : logp_out[t]; };
   const int lane = threadIdx.x & 63;
-  auto offset = [&](int64_t i) -> int64_t {
-    const int64_t o = offsets[i];
-    return o < 0 ? 0 : (o > T ? T : o);
+  const int last = (int)T;  // below 2^25
+  auto offset = [&](int64_t i) {
+    const int o = offsets[i];
+    return o < 0 ? 0 : (o > last ? last : o);
   };
   if (coef != nullptr) {
     // tokens before the first sequence and after the last
-    const int64_t a = offset(0), b = offset(2 * pairs);
-    for (int64_t t = threadIdx.x; t < a; t += 1024) coef[t] = 0.0f;
-    for (int64_t t = b + threadIdx.x; t < T; t += 1024) coef[t] = 0.0f;
+    const int a = offset(0), b = offset(2 * pairs);
+    for (int t = threadIdx.x; t < a; t += 1024) coef[t] = 0.0f;
+    for (int t = b + threadIdx.x; t < last; t += 1024) coef[t] = 0.0f;
   }
+  // 2^split parts of a sequence, a wave for each
+  const int split = pairs >= 8 ? 0 : pairs >= 4 ? 1 : pairs >= 2 ? 2 : 3;
   double total = 0.0;
-  for (int64_t p = wave_id(); p < pairs; p += 16) {
-    const int64_t o[3] = {offset(2 * p), offset(2 * p + 1), offset(2 * p + 2)};
-    double s[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      double v = 0.0;
-#pragma unroll 4
-      for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) v += logp(t);
-      s[k] = wave_sum(v);
-      if (lane == 0 && seq_logp != nullptr) seq_logp[2 * p + k] = static_cast<float>(s[k]);
+  for (int64_t p0 = 0; p0 < pairs; p0 += kBatch) {
+    const int batch = pairs - p0 < kBatch ? (int)(pairs - p0) : kBatch, units = 2 * batch << split;
+    // read before the sums, used after them
+    const int p = threadIdx.x;
+    float r[2] = {};
+    if (p < batch) {
+      r[0] = ref[2 * (p0 + p)];
+      r[1] = ref[2 * (p0 + p) + 1];
     }
-    const double z = (double)beta * ((s[0] - ref[2 * p]) - (s[1] - ref[2 * p + 1]));
-    const double e = exp(-fabs(z)), l = log1p(e);
-    // a weight of zero drops its term, also where that is infinite
-    if (eps != 1.0f) total += (1.0 - (double)eps) * (l + fmax(-z, 0.0));
-    if (eps != 0.0f) total += (double)eps * (l + fmax(z, 0.0));
-    if (coef != nullptr) {
+    int lo = 0, hi = 0;  // the tokens of a unit
+    auto range = [&](int u) {
+      const int64_t s = 2 * p0 + (u >> split);
+      const int a = offset(s), n = offset(s + 1) - a;
+      const int step = n > 0 ? (n + (1 << split) - 1) >> split : 0;
+      lo = a + (u & ((1 << split) - 1)) * step;
+      hi = lo + step < a + n ? lo + step : a + n;
+    };
+    for (int u = wave_id(); u < units; u += 16) {
+      range(u);
+      double v = 0.0;
+#pragma unroll 8
+      for (int t = lo + lane; t < hi; t += 64) v += logp(t);
+      v = wave_sum(v);
+      if (lane == 0) sums[u] = v;
+    }
+    __syncthreads();
+    if (p < batch) {
+      double s[2] = {};
+      for (int u = 0; u < 1 << split; ++u) {
+        s[0] += sums[(2 * p << split) + u];
+        s[1] += sums[(2 * p + 1 << split) + u];
+      }
+      const double z = (double)beta * ((s[0] - r[0]) - (s[1] - r[1]));
+      const double e = exp(-fabs(z));
       const double down = (z >= 0.0 ? e : 1.0) / (1.0 + e);  // sigmoid(-z)
-      const double d = ((double)eps - down) * (double)beta / (double)pairs;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        for (int64_t t = o[k] + lane; t < o[k + 1]; t += 64) coef[t] = static_cast<float>(k == 0 ? d : -d);
+      slope[p] = static_cast<float>(((double)eps - down) * (double)beta / (double)pairs);
+      const double l = log1p(e);
+      // a weight of zero drops its term, also where that is infinite
+      if (eps != 1.0f) total += (1.0 - (double)eps) * (l + fmax(-z, 0.0));
+      if (eps != 0.0f) total += (double)eps * (l + fmax(z, 0.0));
+      if (seq_logp != nullptr) {
+        seq_logp[2 * (p0 + p)] = static_cast<float>(s[0]);
+        seq_logp[2 * (p0 + p) + 1] = static_cast<float>(s[1]);
+      }
+    }
+    __syncthreads();
+    if (coef == nullptr) continue;
+    for (int u = wave_id(); u < units; u += 16) {
+      if (units > 16) range(u);
+      const int s = u >> split;
+      const float d = s & 1 ? -slope[s >> 1] : slope[s >> 1];
+      for (int t = lo + lane; t < hi; t += 64) coef[t] = d;
     }
   }
-  total = block_sum(lane == 0 ? total : 0.0, lds);
+  total = block_sum(total, lds);
   if (threadIdx.x == 0) *loss = static_cast<float>(total / (double)pairs);
 }
 

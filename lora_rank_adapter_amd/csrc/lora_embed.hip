@@ -371,15 +371,18 @@ __global__ __launch_bounds__(256, 8) void grad_kernel(GradLists l, const E* __re
   }
 }
 
-// One workgroup per run whose last id began in it and goes on, and 4 columns
+// One workgroup per run whose last id began in it and goes on, and 8 columns
 // for each of `lanes` lanes: the id's pieces are part[run][1] and part[r][0]
 // of the runs r that follow. The workgroup's 256 / lanes groups take every
-// so many-th of them, and the groups' sums are added in order.
+// so many-th of them, and the groups' sums are added in order. Most runs have
+// nothing to merge: their workgroups only look.
+constexpr int kMergeCols = 8;
+
 template <class O>
 __global__ __launch_bounds__(256) void merge_kernel(GradLists l, const float* __restrict__ part, int64_t part_stride,
                                                     float scale, O* __restrict__ out, int64_t out_stride, bool add,
                                                     int lanes_log2, unsigned pieces) {
-  __shared__ f32x4_t sums[256];
+  __shared__ f32x4_t sums[2][256];
   const int64_t run = blockIdx.x / pieces;
   const int64_t p1 = (run + 1) * kRun;  // below the padded length of the lists: the last run has no workgroup
   const int n = l.start[l.map.total()], key = l.keys[p1 - 1], next = l.keys[p1];
@@ -388,31 +391,37 @@ __global__ __launch_bounds__(256) void merge_kernel(GradLists l, const float* __
   const int from = l.start[s], to = l.start[s + 1];
   if (from < run * kRun) return;
   const int lanes = 1 << lanes_log2, groups = 256 >> lanes_log2;
-  const int64_t c = ((int64_t)(blockIdx.x % pieces) * lanes + (threadIdx.x & (lanes - 1))) * 4;
-  const int count = l.D - c < 4 ? (int)(l.D - c) : 4;
+  const int64_t c = ((int64_t)(blockIdx.x % pieces) * lanes + (threadIdx.x & (lanes - 1))) * kMergeCols;
   const int64_t last = (to - 1) / kRun;  // the id's last run
-  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4_t sum[2] = {};
   if (c < l.D) {
-    int64_t r = run + (threadIdx.x >> lanes_log2);
-    for (; r <= last; r += 4 * groups) {
-      f32x4_t v[4];
+    for (int64_t r = run + (threadIdx.x >> lanes_log2); r <= last; r += 4 * groups) {
+      f32x4_t v[4][2];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t k = r + u * groups;
-        v[u] = k <= last ? ld16f(part + (2 * k + (k == run ? 1 : 0)) * part_stride + c) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        const float* p = part + (2 * k + (k == run ? 1 : 0)) * part_stride + c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[u][h] = k <= last ? ld16f(p + 4 * h) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sum += v[u];
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) sum[h] += v[u][h];
     }
   }
-  sums[threadIdx.x] = sum;
+  sums[0][threadIdx.x] = sum[0];
+  sums[1][threadIdx.x] = sum[1];
   __syncthreads();
   if ((int)threadIdx.x >= lanes || c >= l.D) return;
-  for (int g = 1; g < groups; ++g) sum += sums[(g << lanes_log2) + threadIdx.x];
-  O* p = out + (int64_t)key * out_stride + c;
+  for (int g = 1; g < groups; ++g) {
+    sum[0] += sums[0][(g << lanes_log2) + threadIdx.x];
+    sum[1] += sums[1][(g << lanes_log2) + threadIdx.x];
+  }
+  float f[kMergeCols];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < count) p[e] = Vec<O>::round(add ? Vec<O>::value(p[e]) + sum[e] * scale : sum[e] * scale);
+  for (int e = 0; e < kMergeCols; ++e) f[e] = sum[e >> 2][e & 3] * scale;
+  put_row<kMergeCols>(out + (int64_t)key * out_stride + c, f, l.D - c < kMergeCols ? (int)(l.D - c) : kMergeCols, add);
 }
 
 // ---------------------------------------------------------------------------
@@ -449,7 +458,7 @@ struct GradPlan {
 static GradPlan plan_grad(int64_t T, int64_t V, int64_t D, void* ws) {
   GradPlan g{};
   g.runs = ceil_div(T, kRun);
-  g.part_stride = round_up(D, 4);
+  g.part_stride = round_up(D, kMergeCols);
   // 256 workgroups (one per CU) while their ids fit the histogram, more beyond
   const int64_t quads = ceil_div(V, 4);
   g.map.blocks_log2 = 8;
@@ -468,7 +477,7 @@ static GradPlan plan_grad(int64_t T, int64_t V, int64_t D, void* ws) {
 static bool grad_sizes_ok(int64_t T, int64_t V, int64_t D) {
   // partial sums: 8 bytes per run and column, within what one operand may span
   return T >= 0 && V >= 0 && D >= 0 && T <= kMaxTokens && V <= kMaxTokens && D <= kMaxOperand &&
-         (T == 0 || D == 0 || ceil_div(T, kRun) <= kMaxOperand / (8 * (D + 4)));
+         (T == 0 || D == 0 || ceil_div(T, kRun) <= kMaxOperand / (8 * (D + kMergeCols)));
 }
 
 template <class E, class O>
@@ -479,9 +488,9 @@ static int run_grad(const GradPlan& g, const lora_mat* dy, float scale, const lo
   const int64_t pieces = ceil_div(D, int64_t(Vec<E>::N) << ll);
   const int fl = row_lanes_log2(D, Vec<O>::N);
   const int64_t fill_pieces = ceil_div(D, int64_t(Vec<O>::N) << fl);
-  int ml = row_lanes_log2(D, 4);
-  ml = ml < 6 ? ml : 6;
-  const int64_t merge_pieces = ceil_div(D, int64_t(4) << ml);
+  int ml = row_lanes_log2(D, kMergeCols);
+  ml = ml < 4 ? 4 : ml < 6 ? ml : 6;  // 4 to 16 groups
+  const int64_t merge_pieces = ceil_div(D, int64_t(kMergeCols) << ml);
   // runs, rows and their pieces are counted in 32 bits, rounded up to a workgroup's 256
   constexpr int64_t kMost = kMaxGrid - 256;
   if (pieces > kMost || fill_pieces > kMost || g.runs * pieces > kMost || V * fill_pieces > kMost ||

@@ -319,8 +319,11 @@ struct PolicyArgs {
   float clip_low, clip_high, kl;
 };
 
-// One token of the policy loss: its weighted loss and d loss / d logp.
+// One token of the policy loss: its weighted loss and d loss / d logp. The
+// derivative is a difference of two terms that may nearly cancel, so every
+// kernel has to round them alike: no products fused with sums here.
 __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, float lp) {
+#pragma clang fp contract(off)
   const float ratio = expf(lp - a.old_logp[t]);
   const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
   const float adv = a.advantages[t], w = a.weights[t];

@@ -24,6 +24,7 @@ pytestmark = pytest.mark.gpu
                                        (F, 9, 24581), (F, 127, 49153), (BF, 130, 60001), (BF, 3, 300007)])
 def test_policy_step_changes_over(dtype, T, V):
     note(f"policy changes over {dtype} {T} {V}")
+    torch.manual_seed(T + V)
     x, y = make(T, V, dtype, T + V, pad=1, shift=1)
     masked = torch.from_numpy(O.masked(y.cpu().numpy(), V)).to(DEV)
     lp, _ = L.lora_token_logp(x, y)
@@ -35,6 +36,7 @@ def test_policy_step_changes_over(dtype, T, V):
     loss, logp, dx = L.lora_policy_step(x, y, *args, grad_scale=0.5)
     x64, yn = f64(x), y.cpu().numpy()
     close(f64(logp), O.token_logp(x64, yn), row_bounds(x64, yn)[1], "logp")
+    # the coefficient of a log probability is the same bits in every kernel
     loss2, coef = L.lora_policy_loss(logp, y, V, *args)
     # each token's loss is rounded a few times in either kernel, their sum is float64
     terms = np.abs(f64(w)) * (3 * np.abs(f64(adv)) + 1)

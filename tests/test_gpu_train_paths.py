@@ -160,6 +160,25 @@ def test_gradient_lists(T, V, kind):
         check_grad(L.lora_embed_grad(ids, real, V, 0.7), ids, real, V, 0.7)
 
 
+@pytest.mark.parametrize("types", [(F, F), (BF, F), (BF, BF)])
+@pytest.mark.parametrize("T", [1, 8, 63, 64, 65, 257])
+@pytest.mark.parametrize("V,D,kind", [(700, 37, "zipf"), (3, 2100, "zipf"), (5000, 64, "same"), (90, 9, "outside")])
+def test_gradient_of_few_tokens(types, T, V, D, kind):
+    note(f"embed_grad few {types} {T} {V} {D} {kind}")
+    torch.manual_seed(T + V)
+    ids = make_ids(T, V, kind, np.random.default_rng(T + V))
+    dy = torch.randn(T, D + 3, device=DEV).to(types[0])[:, :D]
+    out = torch.full((V, D + 1), 7.0, device=DEV, dtype=types[1])[:, :D]
+    got = L.lora_embed_grad(ids, dy, V, 0.7, dtable=out)
+    check_grad(got, ids, dy, V, 0.7)
+    assert bool((out._base[:, D] == 7.0).all())
+    assert torch.equal(got, L.lora_embed_grad(ids, dy, V, 0.7, dtype=types[1]))
+    old = torch.randn(V, D, device=DEV).to(types[1])
+    base = old.clone()
+    L.lora_embed_grad(ids, dy, V, 0.7, dtable=old, accumulate=True)
+    check_grad(old, ids, dy, V, 0.7, f64(base))
+
+
 # ---------------------------------------------------------------------------
 # AdamW: few chunks in one workgroup, more in the grid; tiny moments
 # ---------------------------------------------------------------------------

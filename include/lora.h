@@ -365,6 +365,8 @@ int lora_gather_shrink(const int32_t* ids, const lora_t3* a, const lora_addressi
                        int32_t r_max, const lora_t3* h, void* stream);
 
 /*
+ * The operators of a training step.
+ *
  * Embedding lookup with scaling:
  *     out[t] = scale * table[ids[t]], zeros for an id outside [0, V)
  *   ids    int32[T] device.
@@ -384,9 +386,11 @@ int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lor
  *   accumulate 0: every row is written, zeros where no token names it;
  *           otherwise the rows that tokens name are added to and the others
  *           left alone.
- *   Ids outside [0, V) add no term. The tokens are sorted by id on the device
- *   and each id's terms added in an order that depends on the ids alone (no
- *   float atomics). T, V below 2^31 - 4096.
+ *   Ids outside [0, V) add no term. The tokens are grouped by id on the device
+ *   and each id's terms added in an order that depends on the ids and the
+ *   sizes alone (no float atomics): the same call gives the same bits. T, V
+ *   below 2^31 - 4096, and T and V times the pieces of a row (one for every
+ *   256 vectors of 16 bytes) below 2^31 - 256; LORA_ERR_LIMIT above.
  *   workspace: lora_embed_grad_workspace_bytes(T, V, D), 256-byte aligned.
  */
 size_t lora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);
@@ -404,7 +408,8 @@ int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float scale, const l
  *   dlogits  T x V of the logits' dtype, layout rules as for logits; it may
  *            be the logits themselves (same pointer and strides), otherwise
  *            it must not overlap them. Every element is written.
- *   workspace: lora_loss_workspace_bytes(T, V), 256-byte aligned.
+ *   workspace: lora_loss_workspace_bytes(T, V), 256-byte aligned. Its contents
+ *            do not matter before a call and have no meaning after it.
  * A row whose logits are all -inf, or that holds +inf or NaN, gives NaN.
  *
  * Workspace of the calls below; 0 for sizes beyond the limits.
@@ -472,9 +477,11 @@ int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float*
                     const float* grad_out, float scale, const lora_mat* dlogits, void* stream);
 
 /*
- * Loss and gradient in one call: lora_token_logp, then the loss, then
- * lora_logit_grad with the loss's coefficients and scale = grad_scale.
- * Outputs as for these calls (loss, seq_logp or NULL, logp, dlogits).
+ * Loss and gradient in one call: what lora_token_logp, the loss and
+ * lora_logit_grad with the loss's coefficients and scale = grad_scale give.
+ * Outputs as for these calls (loss, seq_logp or NULL, logp, dlogits). The
+ * preference step's are the same bits as theirs; the policy step may take a
+ * row's statistics in another order (and reads a long row from memory once).
  */
 int lora_pref_step(const lora_mat* logits, const int32_t* targets, const int32_t* seq_offsets, int64_t pairs,
                    const float* ref_logp, float beta, float label_smoothing, float grad_scale, float* loss,
@@ -514,7 +521,9 @@ typedef struct {
  *            block (of m, of sqrt(v)) over 448, codes are rounded to nearest
  *            even; a v above zero keeps at least the smallest code; a block
  *            whose largest magnitude is below 1e-30 is stored as zeros. The
- *            update of a step uses m and v before they are rounded.
+ *            update of a step uses m and v before they are rounded. Scales,
+ *            roots and the update's quotient are within a few float32
+ *            roundings of these formulas.
  *   m and v 16-byte aligned. step: one int32, the number of steps taken.
  */
 typedef struct {

@@ -110,8 +110,8 @@ def test_policy_rows_beyond_32_bit_offsets():
 # preference step: rows whole or in pieces, joined with the loss or before it
 # ---------------------------------------------------------------------------
 
-@pytest.mark.parametrize("T,V,pairs", [(255, 9000, 3), (256, 9000, 1), (257, 9000, 2), (1365, 8200, 4),
-                                       (1366, 8200, 4), (1, 128256, 1), (12, 270000, 2)])
+@pytest.mark.parametrize("T,V,pairs", [(255, 9000, 3), (256, 9000, 1), (257, 9000, 2), (682, 8200, 4),
+                                       (683, 8200, 4), (1365, 8200, 4), (1, 128256, 1), (12, 270000, 2)])
 def test_pref_step_changes_over(T, V, pairs):
     note(f"pref changes over {T} {V} {pairs}")
     rng = np.random.default_rng(T + V)

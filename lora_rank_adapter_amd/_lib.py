@@ -45,9 +45,11 @@ class LoraMat(ctypes.Structure):
     ]
 
 
-# A LoraMat as packed bytes, which a call takes in a fraction of the time of a Structure object. The functions
-# that take them declare c_void_p (byref of a LoraMat does as well).
-pack_mat = struct.Struct("=Qiiqqqq").pack
+# Descriptors as packed bytes, which a call takes in a fraction of the time of a Structure object. The functions
+# that take them declare c_void_p (byref of the Structure does as well).
+pack_mat = struct.Struct("=Qiiqqqq").pack        # LoraMat
+pack_policy = struct.Struct("=QQQQQfff4x").pack  # LoraPolicy
+pack_hyper = struct.Struct("=dddddQQ").pack      # LoraAdamwHyper
 
 
 class LoraT3(ctypes.Structure):
@@ -163,7 +165,7 @@ SIGNATURES = {
     "lora_pref_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                       ctypes.c_void_p, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "lora_policy_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, _P(LoraPolicy),
+    "lora_policy_loss": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "lora_logit_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
@@ -171,7 +173,7 @@ SIGNATURES = {
                                       ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_size_t, ctypes.c_void_p]),
-    "lora_policy_step": (ctypes.c_int, [ctypes.c_void_p, _P(LoraPolicy), ctypes.c_float, ctypes.c_void_p,
+    "lora_policy_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]),
     "lora_adamw_table_bytes": (ctypes.c_size_t, [_P(LoraAdamwTensor), ctypes.c_int64]),
@@ -179,7 +181,7 @@ SIGNATURES = {
     "lora_adamw_table": (ctypes.c_int, [_P(LoraAdamwTensor), ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]),
     "lora_adamw_step": (ctypes.c_int, [_P(LoraAdamwTensor), ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
-                                       _P(LoraAdamwState), _P(LoraAdamwHyper), ctypes.c_void_p]),
+                                       _P(LoraAdamwState), ctypes.c_void_p, ctypes.c_void_p]),
     "lora_timing_begin": (ctypes.c_int, []),
     "lora_timing_pause": (ctypes.c_int, []),
     "lora_timing_resume": (ctypes.c_int, []),

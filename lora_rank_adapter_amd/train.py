@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import LoraAdamwHyper, LoraAdamwState, LoraAdamwTensor, LoraPolicy, check, pack_mat
+from ._lib import LoraAdamwState, LoraAdamwTensor, check, pack_hyper, pack_mat, pack_policy
 from .ops import _DT, _dtype_code, _stream
 
 _I32, _F32 = torch.int32, torch.float32
@@ -114,8 +114,8 @@ def lora_token_logp(logits: torch.Tensor, targets: torch.Tensor,
     logp = torch.empty(T, dtype=_F32, device=dev)
     stats = torch.empty((T, 2), dtype=_F32, device=dev)
     ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
-    check("lora_token_logp", lib.lora_token_logp(_matrix("logits", logits, dev), y, logp.data_ptr(), stats.data_ptr(), ws.data_ptr(),
-                                                 nbytes, _queue(dev)))
+    check("lora_token_logp", lib.lora_token_logp(_matrix("logits", logits, dev), y, logp.data_ptr(), stats.data_ptr(),
+                                                 ws.data_ptr(), nbytes, _queue(dev)))
     return logp, stats
 
 
@@ -143,13 +143,13 @@ def lora_pref_loss(logp: torch.Tensor, seq_offsets: torch.Tensor, ref_logp: torc
     return loss, seq, coef
 
 
-def _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev) -> LoraPolicy:
+def _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev) -> bytes:
     if kl_coef != 0.0 and ref_logp is None:
         raise ValueError("kl_coef needs ref_logp")
-    return LoraPolicy(_vector("targets", targets, T, _I32, dev), _vector("old_logp", old_logp, T, _F32, dev),
-                      None if ref_logp is None else _vector("ref_logp", ref_logp, T, _F32, dev),
-                      _vector("advantages", advantages, T, _F32, dev), _vector("weights", weights, T, _F32, dev),
-                      float(clip_low), float(clip_high), float(kl_coef))
+    return pack_policy(_vector("targets", targets, T, _I32, dev), _vector("old_logp", old_logp, T, _F32, dev),
+                       0 if ref_logp is None else _vector("ref_logp", ref_logp, T, _F32, dev),
+                       _vector("advantages", advantages, T, _F32, dev), _vector("weights", weights, T, _F32, dev),
+                       clip_low, clip_high, kl_coef)
 
 
 def lora_policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_logp: torch.Tensor,
@@ -164,7 +164,7 @@ def lora_policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_
     loss = torch.empty((), dtype=_F32, device=dev)
     coef = torch.empty(T, dtype=_F32, device=dev)
     check("lora_policy_loss", lib.lora_policy_loss(_vector("logp", logp, T, _F32, dev), T, int(vocab),
-                                                   ctypes.byref(args), loss.data_ptr(), coef.data_ptr(), _queue(dev)))
+                                                   args, loss.data_ptr(), coef.data_ptr(), _queue(dev)))
     return loss, coef
 
 
@@ -178,7 +178,7 @@ def lora_logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Te
     T = logits.shape[0]
     dev = logits.device
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        dlogits = torch.empty_like(logits)
     check("lora_logit_grad", lib.lora_logit_grad(
         _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
         _vector("stats", stats, 2 * T, _F32, dev), _vector("coef", coef, T, _F32, dev),
@@ -196,16 +196,17 @@ def lora_pref_step(logits: torch.Tensor, targets: torch.Tensor, seq_offsets: tor
     T, V = logits.shape
     dev, pairs = logits.device, _pairs(seq_offsets)
     if dlogits is None:
-        dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
-    loss = torch.empty((), dtype=_F32, device=dev)
-    seq = torch.empty(2 * pairs, dtype=_F32, device=dev)
+        dlogits = torch.empty_like(logits)
     logp = torch.empty(T, dtype=_F32, device=dev)
+    seq = logp.new_empty(2 * pairs)
+    loss = logp.new_empty(())
     ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
     check("lora_pref_step", lib.lora_pref_step(
         _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
         _vector("seq_offsets", seq_offsets, 2 * pairs + 1, _I32, dev), pairs,
         _vector("ref_logp", ref_logp, 2 * pairs, _F32, dev), float(beta), float(label_smoothing), float(grad_scale),
-        loss.data_ptr(), seq.data_ptr(), logp.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
+        loss.data_ptr(), seq.data_ptr(), logp.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes,
+        _queue(dev)))
     return loss, seq, logp, dlogits
 
 
@@ -220,12 +221,12 @@ def lora_policy_step(logits: torch.Tensor, targets: torch.Tensor, old_logp: torc
     dev = logits.device
     args = _policy(targets, T, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef, dev)
     if dlogits is None:
-        dlogits = torch.empty((T, V), dtype=logits.dtype, device=dev)
-    loss = torch.empty((), dtype=_F32, device=dev)
+        dlogits = torch.empty_like(logits)
     logp = torch.empty(T, dtype=_F32, device=dev)
+    loss = logp.new_empty(())
     ws, nbytes = _given(workspace, lib.lora_loss_workspace_bytes(T, V), dev)
     check("lora_policy_step", lib.lora_policy_step(
-        _matrix("logits", logits, dev), ctypes.byref(args), float(grad_scale), loss.data_ptr(), logp.data_ptr(),
+        _matrix("logits", logits, dev), args, float(grad_scale), loss.data_ptr(), logp.data_ptr(),
         _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
     return loss, logp, dlogits
 
@@ -311,9 +312,9 @@ class AdamW:
         if any(self.state[k].data_ptr() != a for k, a in self._addresses_of_state.items()):
             raise ValueError("a state tensor was replaced: copy into it instead")
         dev = self.device
-        hyper = LoraAdamwHyper(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                               None if lr_scale is None else _vector("lr_scale", lr_scale, 1, _F32, dev),
-                               None if grad_scale is None else _vector("grad_scale", grad_scale, 1, _F32, dev))
+        hyper = pack_hyper(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                           0 if lr_scale is None else _vector("lr_scale", lr_scale, 1, _F32, dev),
+                           0 if grad_scale is None else _vector("grad_scale", grad_scale, 1, _F32, dev))
         check("lora_adamw_step", self._lib.lora_adamw_step(self._tensors, len(self.params), self._table.data_ptr(),
                                                            self._table_bytes, ctypes.byref(self._state),
-                                                           ctypes.byref(hyper), _queue(dev)))
+                                                           hyper, _queue(dev)))

@@ -42,7 +42,8 @@ def test_gradients_that_do_not_exist_are_refused():
         torch_ops._logp_backward(types.SimpleNamespace(saved_tensors=(g, g, g)), g, g)
     with pytest.raises(RuntimeError, match="beside the loss"):
         torch_ops._loss_backward(types.SimpleNamespace(saved_tensors=(g,), inputs=5), g, g, None)
-    assert torch_ops._loss_backward(types.SimpleNamespace(saved_tensors=(g,), inputs=5), None, None, None) == (None,) * 5
+    ctx = types.SimpleNamespace(saved_tensors=(g,), inputs=5)
+    assert torch_ops._loss_backward(ctx, None, None, None) == (None,) * 5
     assert torch_ops._logp_backward(types.SimpleNamespace(saved_tensors=(g, g, g)), None, None) == (None, None)
 
 

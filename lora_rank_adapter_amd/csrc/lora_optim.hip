@@ -141,9 +141,8 @@ __device__ __forceinline__ float rotate_max(float v) {
 }
 __device__ __forceinline__ float wave_max(float v) {
   const int m = __float_as_int(rotate_max<1>(rotate_max<2>(rotate_max<4>(rotate_max<8>(v)))));
-  const float a = fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 0)), __int_as_float(__builtin_amdgcn_readlane(m, 16)));
-  const float b = fmaxf(__int_as_float(__builtin_amdgcn_readlane(m, 32)), __int_as_float(__builtin_amdgcn_readlane(m, 48)));
-  return fmaxf(a, b);
+  auto row = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(m, lane)); };
+  return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
 }
 
 // x: 4 values of each lane, one block over the wave. Returns the codes.
@@ -276,6 +275,8 @@ __device__ __forceinline__ const int32_t* chunk_map(const void* table, int64_t n
   return reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
 }
 
+// One block to a wave: 75.5 M elements with 8-bit states take 244 us so, 265
+// with two blocks to a wave and 274 with four.
 template <int BITS>
 __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
   const auto* h = static_cast<const TableHead*>(table);

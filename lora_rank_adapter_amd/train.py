@@ -261,6 +261,7 @@ class AdamW:
             raise ValueError(f"{len(self.shadows)} shadows for {len(self.params)} params")
         self._lib = _lib.load()
         self.device = self.params[0].device
+        self._shapes = [p.shape for p in self.params]
         self.bind(grads)
         n = self._lib.lora_adamw_state_elems(self._tensors, len(self.params))
         codes = torch.float8_e4m3fn if state_bits == 8 else _F32
@@ -279,10 +280,14 @@ class AdamW:
                                      at.get("v_scale"), at["step"])
 
     def bind(self, grads) -> None:
-        """Takes these gradients from now on (writes the device table on the current stream)."""
+        """Takes these gradients from now on (writes the device table on the current stream). The params may lie
+        elsewhere than before, in the shapes that they had: the states stay what they are."""
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} grads for {len(self.params)} params")
+        for i, (p, shape) in enumerate(zip(self.params, self._shapes)):
+            if p.shape != shape:
+                raise ValueError(f"param {i} has become {tuple(p.shape)}: its states are those of {tuple(shape)}")
         tensors = (LoraAdamwTensor * len(grads))()
         for i, (p, g, s) in enumerate(zip(self.params, grads, self.shadows)):
             for name, t in (("param", p), ("grad", g), ("shadow", s)):

@@ -36,6 +36,11 @@ def _queue(device: torch.device):
     return _stream(device)
 
 
+def _capturing(stream) -> bool:
+    """Whether a graph is being captured on torch's current stream, `stream` (the default stream cannot be)."""
+    return stream.value is not None and torch.cuda.is_current_stream_capturing()
+
+
 def _matrix(name: str, t: torch.Tensor, device: torch.device) -> bytes:
     shape = t.shape
     if len(shape) != 2:
@@ -243,6 +248,11 @@ class AdamW:
     param None or a bfloat16 tensor that receives a float32 param's new value. The object holds these tensors and
     a device table of their addresses; `bind` replaces the gradients, `step` refuses tensors whose memory moved.
 
+    The table and new states are written on the stream that is current in the constructor and in `bind`; a step on
+    another stream waits for that. A step that was captured into a graph goes on with the tensors bound then, also
+    after a later `bind`: its table and they are kept while the object lives (which has to be as long as the graph
+    is replayed). The graph waits for nothing: it is replayed after what the current stream holds at its capture.
+
     state_bits 32 keeps both moments in float32, 8 as e4m3 codes with a float32 scale for every 256 elements.
     state: a dict of the tensors step, m, v (and m_scale, v_scale with 8 bits) to go on from; they are used in
     place. The new ones are zeros. All of it is in `self.state`, the layout in include/lora.h.
@@ -262,6 +272,7 @@ class AdamW:
         self._lib = _lib.load()
         self.device = self.params[0].device
         self._shapes = [p.shape for p in self.params]
+        self._captured, self._kept = False, []
         self.bind(grads)
         n = self._lib.lora_adamw_state_elems(self._tensors, len(self.params))
         codes = torch.float8_e4m3fn if state_bits == 8 else _F32
@@ -276,6 +287,7 @@ class AdamW:
         self.state = dict(state)
         at = {k: _vector(k, self.state[k], c, d, self.device) for k, (c, d) in want.items()}
         self._addresses_of_state = at
+        self._mark()
         self._state = LoraAdamwState(state_bits, 0, at["m"] or None, at["v"] or None, at.get("m_scale"),
                                      at.get("v_scale"), at["step"])
 
@@ -305,9 +317,33 @@ class AdamW:
         table = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
         check("lora_adamw_table", self._lib.lora_adamw_table(tensors, len(grads), table.data_ptr(), need,
                                                              _queue(self.device)))
+        if self._captured:  # a graph holds the addresses of what is replaced here
+            self._kept.append((self._table, self._held))
+            self._captured = False
         self.grads, self._tensors, self._table, self._table_bytes = grads, tensors, table, need
         self._held = self.params + grads + [s for s in self.shadows if s is not None]
         self._addresses = list(map(_data_ptr, self._held))
+        self._mark()
+
+    def _mark(self) -> None:
+        """The current stream has written the table and the states: steps elsewhere wait for it."""
+        stream = _queue(self.device)
+        self._streams = {stream.value}
+        if _capturing(stream):  # nothing to wait for: the graph writes them when it runs
+            self._written, self._captured = None, True
+        else:
+            self._written = torch.cuda.Event()
+            self._written.record(torch.cuda.current_stream(self.device))
+
+    def _admit(self, stream) -> None:
+        """The first step on `stream`, the current one, since it was written elsewhere: the memory that the object
+        allocated there is not given away before this stream is done with it."""
+        current = torch.cuda.current_stream(self.device)
+        if self._written is not None:
+            current.wait_event(self._written)
+        for t in (self._table, *self.state.values()):
+            t.record_stream(current)
+        self._streams.add(stream.value)
 
     def step(self, lr_scale: torch.Tensor | None = None, grad_scale: torch.Tensor | None = None) -> None:
         """One step on the current stream. lr_scale, grad_scale: None or float32 [] tensors on the device that
@@ -317,9 +353,14 @@ class AdamW:
         if any(self.state[k].data_ptr() != a for k, a in self._addresses_of_state.items()):
             raise ValueError("a state tensor was replaced: copy into it instead")
         dev = self.device
+        stream = _queue(dev)
+        if _capturing(stream):
+            self._captured = True
+        elif stream.value not in self._streams:
+            self._admit(stream)
         hyper = pack_hyper(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
                            0 if lr_scale is None else _vector("lr_scale", lr_scale, 1, _F32, dev),
                            0 if grad_scale is None else _vector("grad_scale", grad_scale, 1, _F32, dev))
         check("lora_adamw_step", self._lib.lora_adamw_step(self._tensors, len(self.params), self._table.data_ptr(),
                                                            self._table_bytes, ctypes.byref(self._state),
-                                                           hyper, _queue(dev)))
+                                                           hyper, stream))

@@ -1,5 +1,10 @@
-"""What AdamW's binding holds and refuses, on the CPU: the library's launches
-are replaced by calls that do nothing, its sizes are its own."""
+"""What AdamW's binding holds, orders and refuses, on the CPU: the library's
+launches are replaced by calls that do nothing (its sizes are its own), and
+the streams by what records their use."""
+import ctypes
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -8,10 +13,11 @@ from lora_rank_adapter_amd import train
 
 
 class Library:
-    """The library without its launches; counts them."""
+    """The library without its launches, and the machine's streams: counts and notes what is done."""
 
     def __init__(self):
         self.tables = self.steps = 0
+        self.stream, self.capturing, self.log = 0, False, []
 
     def __getattr__(self, name):
         return getattr(L.load_library(), name)
@@ -28,8 +34,23 @@ class Library:
 @pytest.fixture
 def lib(monkeypatch):
     held = Library()
+
+    class Stream:
+        def wait_event(self, event):
+            held.log.append(("wait", held.stream, event.at))
+
+    class Event:
+        def record(self, stream):
+            assert not held.capturing
+            self.at = held.stream
+
     monkeypatch.setattr(train._lib, "load", lambda: held)
-    monkeypatch.setattr(train, "_queue", lambda device: None)
+    monkeypatch.setattr(train, "_queue", lambda device: ctypes.c_void_p(held.stream))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: held.capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream())
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, _: held.log.append(("used", held.stream, t.data_ptr())))
     return held
 
 
@@ -54,3 +75,53 @@ def test_bind_refuses_sizes_that_the_states_do_not_have(lib):
     opt.bind([p.clone(), q.clone()])
     opt.step()
     assert lib.tables == lib.steps == 2
+
+
+def test_what_a_captured_step_uses_is_kept(lib):
+    p = torch.zeros(300)
+    opt = L.AdamW([p], [p.clone()], 1e-3)
+    opt.step()
+    seen = [weakref.ref(t) for t in (opt._table, opt.grads[0])]
+    opt.bind([p.clone()])
+    gc.collect()
+    assert not any(r() is not None for r in seen)  # no graph: let go
+    seen = [weakref.ref(t) for t in (opt._table, opt.grads[0])]
+    lib.stream, lib.capturing = 7, True
+    opt.step()
+    lib.stream, lib.capturing = 0, False
+    for _ in range(2):
+        opt.bind([p.clone()])
+        opt.step()
+    gc.collect()
+    assert all(r() is not None for r in seen) and len(opt._kept) == 1
+    assert lib.log == []  # a capture waits for nothing and marks nothing
+
+
+def test_a_step_on_another_stream_waits_for_the_table(lib):
+    p = torch.zeros(300)
+    lib.stream = 3
+    opt = L.AdamW([p], [p.clone()], 1e-3)
+    opt.step()
+    assert lib.log == []
+    for stream in (0, 5):
+        lib.stream, lib.log = stream, []
+        opt.step()
+        opt.step()
+        assert lib.log[0] == ("wait", stream, 3)
+        assert set(lib.log[1:]) == {("used", stream, t.data_ptr()) for t in (opt._table, *opt.state.values())}
+        assert len(lib.log) == 1 + 4
+    opt.bind([p.clone()])  # now on stream 5
+    lib.stream, lib.log = 3, []
+    opt.step()
+    assert lib.log[0] == ("wait", 3, 5)
+
+
+def test_a_table_written_in_a_capture_is_not_waited_for(lib):
+    p = torch.zeros(300)
+    opt = L.AdamW([p], [p.clone()], 1e-3)
+    lib.stream, lib.capturing = 7, True
+    opt.bind([p.clone()])
+    opt.step()
+    lib.stream, lib.capturing, lib.log = 0, False, []
+    opt.step()
+    assert lib.log and all(kind == "used" for kind, *_ in lib.log)

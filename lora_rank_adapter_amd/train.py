@@ -245,8 +245,10 @@ class AdamW:
 
     params: contiguous float32 or bfloat16 tensors, updated in place; grads: their gradients in the caller's
     buffers (float32 or bfloat16; the ones that lora_bwd_dx_da and lora_bwd_db write); shadows: None, or for each
-    param None or a bfloat16 tensor that receives a float32 param's new value. The object holds these tensors and
-    a device table of their addresses; `bind` replaces the gradients, `step` refuses tensors whose memory moved.
+    param None or a bfloat16 tensor that receives a float32 param's new value. All of a param's tensors have its
+    shape: elements pair by their place, so the weights are kept the way their gradients lie (A as K x r, B as
+    r x L), not as transposes of them. The object holds these tensors and a device table of their addresses; `bind`
+    replaces the gradients, `step` refuses tensors whose memory moved.
 
     The table and new states are written on the stream that is current in the constructor and in `bind`; a step on
     another stream waits for that. A step that was captured into a graph goes on with the tensors bound then, also
@@ -305,9 +307,9 @@ class AdamW:
             for name, t in (("param", p), ("grad", g), ("shadow", s)):
                 if t is None and name == "shadow":
                     continue
-                if t.device != self.device or not t.is_contiguous() or t.numel() != p.numel():
-                    raise ValueError(f"{name} {i} must be contiguous on {self.device} with {p.numel()} elements, "
-                                     f"got {tuple(t.shape)} on {t.device}")
+                if t.device != self.device or not t.is_contiguous() or t.shape != p.shape:
+                    raise ValueError(f"{name} {i} must be contiguous on {self.device} in its param's shape "
+                                     f"{tuple(p.shape)}, got {tuple(t.shape)} on {t.device}")
             if s is not None and s.dtype is not torch.bfloat16:
                 raise ValueError(f"shadow {i} must be bfloat16, got {s.dtype}")
             tensors[i] = LoraAdamwTensor(p.data_ptr() or None, g.data_ptr() or None,

@@ -125,3 +125,16 @@ def test_a_table_written_in_a_capture_is_not_waited_for(lib):
     lib.stream, lib.capturing, lib.log = 0, False, []
     opt.step()
     assert lib.log and all(kind == "used" for kind, *_ in lib.log)
+
+
+@pytest.mark.parametrize("shapes", [((8, 24), (24, 8)), ((8, 24), (192,)), ((6,), (6, 1)), ((1, 8), (8,))])
+def test_operands_of_another_shape_are_refused(lib, shapes):
+    """Elements are paired by their place in memory: a gradient of the transposed weight has as many."""
+    p, t = torch.zeros(shapes[0]), torch.zeros(shapes[1])
+    with pytest.raises(ValueError, match="grad 0"):
+        L.AdamW([p], [t], 1e-3)
+    with pytest.raises(ValueError, match="shadow 0"):
+        L.AdamW([p], [p.clone()], 1e-3, shadows=[t.to(torch.bfloat16)])
+    L.AdamW([p], [p.clone()], 1e-3, shadows=[p.to(torch.bfloat16)])
+    L.AdamW([p.view(-1)], [t.view(-1)], 1e-3)  # flat views pair as their owner says
+    assert lib.tables == 2

@@ -375,6 +375,9 @@ int lora_gather_shrink(const int32_t* ids, const lora_t3* a, const lora_addressi
  *          once).
  *   table and out: stride_col 1, stride_row at least D, aligned to their
  *   elements (any D and any row pitch).
+ *   T and V below 2^31 - 4096, and out below 2^24 workgroups: one for every
+ *   256 vectors of 16 bytes of a row (1024 with rows of 4 times as many), or
+ *   for as many shorter rows as have 256; LORA_ERR_LIMIT above.
  */
 int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lora_mat* out, void* stream);
 
@@ -389,8 +392,10 @@ int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lor
  *   Ids outside [0, V) add no term. The tokens are grouped by id on the device
  *   and each id's terms added in an order that depends on the ids and the
  *   sizes alone (no float atomics): the same call gives the same bits. T, V
- *   below 2^31 - 4096, and T and V times the pieces of a row (one for every
- *   256 vectors of 16 bytes) below 2^31 - 256; LORA_ERR_LIMIT above.
+ *   below 2^31 - 4096, V at most 2^30 for more than 64 tokens, and the tokens'
+ *   runs (T / 8; T itself up to 64) and, without accumulate, the rows V
+ *   together below 2^24 workgroups of 256 vectors of 16 bytes, runs of pieces
+ *   of 512 columns as well; LORA_ERR_LIMIT above.
  *   workspace: lora_embed_grad_workspace_bytes(T, V, D), 256-byte aligned.
  */
 size_t lora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);
@@ -400,8 +405,11 @@ int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float scale, const l
 /*
  * Losses on next-token logits. For all of them:
  *   logits   T x V, bf16 or f32, stride_col 1, stride_row at least V, aligned
- *            to its elements (any V and any row pitch); T below 2^25, V below
- *            2^31 - 8192.
+ *            to its elements (any V and any row pitch); T below 2^24 (the
+ *            losses on log probabilities: 2^25), V at most 2^31 - 2049. A
+ *            gradient has a workgroup for every 4096 bytes begun of a row, in
+ *            all below 2^24 - 1; the policy step below 2^23 rows of more than
+ *            24 KB, 2^22 of more than 96 KB. LORA_ERR_LIMIT above.
  *   targets  int32[T] device: the token whose log probability counts. A
  *            target outside [0, V) masks its row: the row is not read, its
  *            log probability is 0 and its gradient zeros.
@@ -544,7 +552,8 @@ typedef struct {
  * The table of the tensors (device memory of lora_adamw_table_bytes, 256-byte
  * aligned), which lora_adamw_table writes on the stream and every later step
  * over the same tensors takes; it holds their addresses, so it is written
- * again when one of them moves. At most 2^23 - 1 tensors. The sizes are 0 for
+ * again when one of them moves. At most 2^23 - 1 tensors, and below 2^24
+ * chunks of 1024 elements (each tensor begins one). The sizes are 0 for
  * invalid tensors.
  */
 size_t lora_adamw_table_bytes(const lora_adamw_tensor* tensors, int64_t n);

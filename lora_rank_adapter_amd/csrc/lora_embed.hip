@@ -543,7 +543,9 @@ static int check_rows(const lora_mat* m) {
 }
 
 constexpr int64_t kMaxTokens = 0x7FFFFFFF - 4096;  // 32-bit token positions, also rounded up to a workgroup's
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+constexpr int64_t kMaxGrid = max_blocks(256);
+constexpr int kMaxSortLog2 = 21;  // 2^21 workgroups of 1024: the most that a launch holds
+static_assert((int64_t(1) << kMaxSortLog2) <= max_blocks(1024) && (int64_t(2) << kMaxSortLog2) > max_blocks(1024));
 
 struct GradPlan {
   int64_t runs, part_stride;
@@ -595,7 +597,7 @@ static GradGrid grad_grid(int64_t items, int64_t V, int64_t D, bool add) {
   const int64_t fill_pieces = ceil_div(D, int64_t(Vec<O>::N) << g.fill.lanes_log2);
   g.fill.pieces = static_cast<unsigned>(fill_pieces);
   // items, rows and their pieces are counted in 32 bits, rounded up to a workgroup's 256
-  constexpr int64_t kMost = kMaxGrid - 256;
+  constexpr int64_t kMost = 0x7FFFFFFF - 256;
   if (g.pieces > kMost || fill_pieces > kMost || items * g.pieces > kMost || V * fill_pieces > kMost) {
     g.status = LORA_ERR_LIMIT;
     return g;
@@ -629,6 +631,7 @@ static int run_grad(const GradPlan& g, const int32_t* ids, const lora_mat* dy, f
   ml = ml < 4 ? 4 : ml < 6 ? ml : 6;  // 4 to 16 groups
   const int64_t merge_pieces = ceil_div(D, int64_t(kMergeCols) << ml);
   if (merge_pieces > kMaxGrid || g.runs * merge_pieces > kMaxGrid) return LORA_ERR_LIMIT;
+  if (g.map.blocks_log2 > kMaxSortLog2) return LORA_ERR_LIMIT;
   launch(sort_kernel, dim3(1 << g.map.blocks_log2), dim3(1024), 0, st, ids, static_cast<int>(T), static_cast<int>(V),
          g.map, g.order, g.keys, g.start, g.count);
   const GradLists l = {g.order, g.keys, g.start, g.count, g.map, V, D};

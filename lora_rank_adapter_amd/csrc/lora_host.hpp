@@ -87,6 +87,9 @@ inline bool valid_dims(const lora_t3* t) {
   return operand_fits(dims, strides, 3, es > 0 ? es : 1);
 }
 
+// A launch counts the work items of its grid's x side in 32 bits.
+constexpr int64_t max_blocks(int threads) { return int64_t(0xFFFFFFFF) / threads; }
+
 // Carves 256-byte aligned sub-buffers out of a caller workspace.
 struct Carver {
   char* base;

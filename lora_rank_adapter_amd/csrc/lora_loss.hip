@@ -599,8 +599,10 @@ __global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, R
 // host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kMaxLogitRows = 0x7FFFFFFF;
-constexpr int kMaxSplits = 64;  // pieces of one row
+constexpr int64_t kMaxTokens = (int64_t(1) << 25) - 1;  // of the losses on log probabilities
+constexpr int64_t kMaxBlocks = max_blocks(256);
+constexpr int64_t kMaxRows = kMaxBlocks;  // of logits: a workgroup at least for each
+constexpr int kMaxSplits = 64;            // pieces of one row, few enough rows then
 
 // Pieces per row: about as many as give 1024 workgroups (4 per CU), of at
 // least 4096 logits each. A preference step of 700 x 128256 bfloat16 takes 98
@@ -636,7 +638,7 @@ static int check_logits(const lora_mat* m) {
   if (m->cols > 1 && m->stride_col != 1) return LORA_ERR_STRIDE;
   if (m->rows > 1 && m->stride_row < m->cols) return LORA_ERR_STRIDE;
   if (!aligned(m->ptr, elem_size(m->dtype))) return LORA_ERR_STRIDE;
-  if (m->rows > kMaxLogitRows / kMaxSplits || m->cols > 0x7FFFFFFF - 8 * kGradVecs) return LORA_ERR_LIMIT;
+  if (m->rows > kMaxRows || m->cols > 0x7FFFFFFF - 8 * kGradVecs) return LORA_ERR_LIMIT;
   return LORA_OK;
 }
 
@@ -685,7 +687,7 @@ static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->dtype != x->dtype) return LORA_ERR_DTYPE;
   if (int e = check_logits(dx)) return e;
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  return x->rows * pieces >= 0x7FFFFFFF ? LORA_ERR_LIMIT : LORA_OK;
+  return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;  // one more sums a policy loss
 }
 
 template <class E>
@@ -712,15 +714,19 @@ static void run_logit_grad(const lora_mat* x, const int32_t* targets, const floa
 // and 28, 8192 of them 737 and 1046; a row of 32000 takes 10 us either way.
 static bool policy_by_rows(int64_t T, int64_t V) { return T == 0 || T >= 128 || V <= 49152; }
 
+// 8192 rows of bfloat16 by 4, 8 and 16 waves: 4000 columns 28, 41, 82 us; 11000: 66, 67, 110;
+// 32000: 193, 170, 192; 64000: 401, 374, 345; 128256: 839, 798, 737
+static int policy_waves(const lora_mat* x) {
+  const int64_t vecs = x->cols / vec_elems(x->dtype);
+  return vecs <= 1536 ? 4 : vecs <= 6144 ? 8 : 16;
+}
+
 static void run_policy_rows(const lora_mat* x, const PolicyArgs& a, float scale, float* logp, float* terms,
                             const lora_mat* dx, hipStream_t st) {
   const int V = static_cast<int>(x->cols);
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    const int vecs = V / Vec<E>::N;
-    // 8192 rows of bfloat16 by 4, 8 and 16 waves: 4000 columns 28, 41, 82 us; 11000: 66, 67, 110;
-    // 32000: 193, 170, 192; 64000: 401, 374, 345; 128256: 839, 798, 737
-    const int waves = vecs <= 1536 ? 4 : vecs <= 6144 ? 8 : 16;
+    const int waves = policy_waves(x);
     auto* kernel = waves == 4   ? policy_row_kernel<E, 4, 6>
                    : waves == 8 ? policy_row_kernel<E, 8, 6>
                                 : policy_row_kernel<E, 16, 6>;
@@ -753,7 +759,7 @@ static PolicyArgs policy_args(const lora_policy* p) {
 using namespace lora;
 
 extern "C" size_t lora_loss_workspace_bytes(int64_t T, int64_t V) {
-  if (T < 0 || V < 0 || T > kMaxLogitRows / kMaxSplits || V > 0x7FFFFFFF - 8 * kGradVecs) return 0;
+  if (T < 0 || V < 0 || T > kMaxRows || V > 0x7FFFFFFF - 8 * kGradVecs) return 0;
   return plan_loss(T, V, nullptr).bytes;
 }
 
@@ -777,7 +783,7 @@ extern "C" int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_o
                               float* coef, void* stream) {
   if (int e = check_pref(seq_offsets, pairs, ref_logp, beta, label_smoothing, loss)) return e;
   if (T < 0) return LORA_ERR_SHAPE;
-  if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
+  if (T > kMaxTokens) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
   launch(pref_kernel<false>, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), RowPieces{},
          const_cast<float*>(logp), T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss, seq_logp, coef);
@@ -788,7 +794,7 @@ extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const l
                                 float* coef, void* stream) {
   if (int e = check_policy(policy, T, loss)) return e;
   if (T < 0 || V < 0) return LORA_ERR_SHAPE;
-  if (T > kMaxLogitRows / kMaxSplits) return LORA_ERR_LIMIT;
+  if (T > kMaxTokens) return LORA_ERR_LIMIT;
   if (T > 0 && !logp) return LORA_ERR_NULL;
   launch(policy_kernel, dim3(1), dim3(1024), 0, static_cast<hipStream_t>(stream), logp, T, V, policy_args(policy),
          loss, coef);
@@ -839,6 +845,7 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
   if (int e = check_policy(policy, T, loss)) return e;
   if (int e = check_logits(logits)) return e;
   if (int e = check_dlogits(logits, dlogits)) return e;
+  if (policy_by_rows(T, V) && T > max_blocks(64 * policy_waves(logits))) return LORA_ERR_LIMIT;
   if (T > 0 && (!logp || (V > 0 && (!logits->ptr || !dlogits->ptr)))) return LORA_ERR_NULL;
   const LossPlan l = plan_loss(T, V, workspace);
   if (T > 0)

@@ -336,7 +336,7 @@ static int measure(const lora_adamw_tensor* t, int64_t n, TableSize* size) {
     size->elems += round_up(t[i].numel, kStateBlock);
     size->chunks += ceil_div(t[i].numel, kChunk);
     if (size->elems > kMaxOperand / 4) return LORA_ERR_SHAPE;
-    if (size->chunks > 0x7FFFFFFF) return LORA_ERR_LIMIT;
+    if (size->chunks > max_blocks(256)) return LORA_ERR_LIMIT;
   }
   size->bytes = static_cast<size_t>(chunk_map_offset(n) + round_up(4 * size->chunks, 256));
   return LORA_OK;

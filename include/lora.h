@@ -480,13 +480,19 @@ int lora_policy_loss(const float* logp, int64_t T, int64_t V, const lora_policy*
  *   dlogits[t, j] = g * coef_t * ([j = y_t] - softmax(x[t])_j)
  *   with g = scale, times *grad_out (one float on the device) unless that is
  *   NULL; stats from lora_token_logp on the same logits and targets.
+ *   The entry at a likely target, g * coef_t * (1 - p), keeps the precision of
+ *   1 - p: where the row's sum is below 1.25 (bf16: 1 + 2^-8) it comes from
+ *   the other logits, which are read once more for it, or from logp, the log
+ *   probabilities that lora_token_logp gave, with lora_logit_grad_logp.
  */
 int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* coef,
                     const float* grad_out, float scale, const lora_mat* dlogits, void* stream);
+int lora_logit_grad_logp(const lora_mat* logits, const int32_t* targets, const float* stats, const float* logp,
+                         const float* coef, const float* grad_out, float scale, const lora_mat* dlogits, void* stream);
 
 /*
  * Loss and gradient in one call: what lora_token_logp, the loss and
- * lora_logit_grad with the loss's coefficients and scale = grad_scale give.
+ * lora_logit_grad_logp with the loss's coefficients and scale = grad_scale give.
  * Outputs as for these calls (loss, seq_logp or NULL, logp, dlogits). The
  * preference step's are the same bits as theirs; the policy step may take a
  * row's statistics in another order (and reads a long row from memory once).

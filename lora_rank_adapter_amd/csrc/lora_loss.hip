@@ -13,6 +13,11 @@
 // exp(x - m): exp(x - m) / s keeps the precision that
 // exp(x - lse) would lose to the rounding of a large lse.
 //
+// A likely target leaves little to the others: with t their sum, 1 - p is
+// t / s and logp is -log(1 + t), and both keep t's precision only if t is
+// summed without the target's own term. So it is summed so everywhere, and
+// the gradient at the target, c (1 - p), comes from logp as -c expm1(logp).
+//
 // Kernels:
 //   logp_kernel       one pass over a row (or one piece of it): running max and sum
 //   join_kernel       the pieces of a row joined, four lanes per row
@@ -20,6 +25,7 @@
 //   policy_kernel     each token's loss and coefficient, and their sum
 //   policy_row_kernel a row from its statistics to its gradient (policy loss)
 //   sum_kernel        the sum of the tokens' losses
+//   target_kernel     the gradient's entries at likely targets from the statistics
 //   logit_grad_kernel the gradient's rows from the statistics and coefficients
 //   policy_grad_kernel  the same from the pieces of few long rows, and the policy loss
 
@@ -39,9 +45,8 @@ __device__ __forceinline__ float exp2_raw(float v) { return __builtin_amdgcn_exp
 // does, and values of the type's lowest magnitude are ordinary values.
 //
 // s is float64 and takes the sum of a batch at a time, which is added up as a
-// tree: where the target holds nearly all of the probability the sum is 1 and
-// a hundred thousand terms of 1e-7, and one after the other in float32 they
-// are lost (logp off by 4e-6).
+// tree: a hundred thousand terms one after the other in float32 lose what is
+// small among them. The target's term is left out of it (see above).
 struct MaxSum {
   float m;
   double s;
@@ -79,11 +84,53 @@ __device__ __forceinline__ MaxSum wave_join(MaxSum v) {
   return {m, wave_sum(v.s * exp2_raw((v.m - at_max(m)) * kLog2e))};
 }
 
-// logp of the target from the row's statistics, rounded once: a loss is a
-// small difference of many, and a float32 logarithm of 10 is off by 5e-7.
-__device__ __forceinline__ float target_logp(float x, MaxSum v) {
-  return static_cast<float>(((double)x - v.m) - log(v.s));
+// A whole row from its target's logit x and the others: the statistics, and
+// logp in float64, rounded once: a loss is a small difference of many, and a
+// float32 logarithm of 10 is off by 5e-7.
+struct RowStats {
+  float x, m, e;  // the target's logit, the largest one, exp(x - m)
+  double t;       // the others' sum
+  __device__ __forceinline__ float sum() const { return static_cast<float>(t + e); }
+  __device__ __forceinline__ float logp() const {
+    return static_cast<float>(((double)x - m) - (e == 1.0f ? log1p(t) : log(t + e)));
+  }
+};
+__device__ __forceinline__ RowStats with_target(MaxSum others, float x) {
+  const float m = fmaxf(others.m, x);
+  const float z = at_max(m);
+  return {x, m, exp2_raw((x - z) * kLog2e), others.s * exp2_raw((others.m - z) * kLog2e)};
 }
+
+// Element `at` of a row's piece (-1: it is elsewhere), which the sums leave
+// out: -inf takes its place in the loaded vector that holds it.
+template <class E>
+struct LeftOut {
+  static constexpr int N = Vec<E>::N;
+  int vector;  // -1: none of the piece's vectors
+  uint32_t keep[4], put[4];
+  __device__ __forceinline__ LeftOut(int at, int vecs) {
+    vector = at >= 0 && at < vecs * N ? at / N : -1;
+    const int e = at & (N - 1), word = N == 8 ? e >> 1 : e;
+    const uint32_t mask = N == 4 ? 0xFFFFFFFFu : e & 1 ? 0xFFFF0000u : 0x0000FFFFu;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      keep[k] = k == word ? ~mask : 0xFFFFFFFFu;
+      put[k] = k == word ? mask & 0xFF80FF80u & (N == 4 ? 0xFFFF0000u : 0xFFFFFFFFu) : 0u;
+    }
+  }
+  // U vectors that are `step` (a power of two) apart, from vector i on
+  template <int U>
+  __device__ __forceinline__ void from(typename Vec<E>::type* w, int i, int step) const {
+    const int d = vector - i;
+    if ((d & ~((U - 1) * step)) != 0) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (d == u * step) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[u][k] = (w[u][k] & keep[k]) | put[k];
+      }
+  }
+};
 
 // One read of the row or piece, four 16-byte loads per lane in flight, each
 // used once (non-temporal: by the default policy 8% slower): 8192 rows of
@@ -93,7 +140,7 @@ template <class E>
 __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
                                                    const int32_t* __restrict__ targets, int V, int splits, int piece,
                                                    float* __restrict__ logp, float2* __restrict__ stats,
-                                                   float2* __restrict__ part, float* __restrict__ hit) {
+                                                   MaxSum* __restrict__ part, float* __restrict__ hits) {
   constexpr int N = Vec<E>::N, U = 4;
   __shared__ MaxSum waves[4];
   const int64_t row = blockIdx.x / (unsigned)splits;
@@ -112,6 +159,8 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   const int n = V - lo < piece ? V - lo : piece;
   const E* p = src + lo;
   const int vecs = n / N;
+  const int hit = y >= lo && y - lo < n ? y - lo : -1;
+  const LeftOut<E> target(hit, vecs);
   MaxSum r{-INFINITY, 0.0};
   int i = tid;
   for (; i + (U - 1) * 256 < vecs; i += U * 256) {
@@ -119,6 +168,7 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
     typename Vec<E>::type w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(i + u * 256) * N);
+    target.template from<U>(w, i, 256);
 #pragma unroll
     for (int u = 0; u < U; ++u) Vec<E>::unpack(w[u], f + u * N);
     add_values<U * N>(r, f);
@@ -132,11 +182,12 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
   for (int u = 0; u < U - 1; ++u) {
     if (i + u * 256 < vecs) {
       float f[N];
+      target.template from<1>(w + u, i + u * 256, 1);
       Vec<E>::unpack(w[u], f);
       add_values<N>(r, f);
     }
   }
-  if (tid < n - vecs * N) {
+  if (tid < n - vecs * N && vecs * N + tid != hit) {
     const float f = Vec<E>::value(p[vecs * N + tid]);
     add_values<1>(r, &f);
   }
@@ -147,12 +198,13 @@ __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int6
 #pragma unroll
   for (int w = 1; w < 4; ++w) all = join(all, waves[w]);
   if (splits > 1) {
-    part[row * splits + sp] = make_float2(all.m, static_cast<float>(all.s));
+    part[row * splits + sp] = all;
     // kept beside the pieces: the logits may be overwritten while they are joined
-    if (y >= lo && y - lo < n) hit[row] = Vec<E>::value(src[y]);
+    if (hit >= 0) hits[row] = Vec<E>::value(src[y]);
   } else {
-    logp[row] = target_logp(Vec<E>::value(src[y]), all);
-    stats[row] = make_float2(all.m, static_cast<float>(all.s));
+    const RowStats v = with_target(all, Vec<E>::value(src[y]));
+    logp[row] = v.logp();
+    stats[row] = make_float2(v.m, v.sum());
   }
 }
 
@@ -162,15 +214,14 @@ struct RowPieces {
   const int32_t* targets;
   int64_t V;
   int splits;
-  const float2* part;
-  const float* hit;  // the rows' target logits
+  const MaxSum* part;
+  const float* hits;  // the rows' target logits
   float2* stats;
 };
 
 struct Joined {
   bool live;  // the row is there and not masked
-  MaxSum r;
-  float logp;
+  float m, sum, logp;
 };
 
 // Row `row` for lane `sub` of its four (all of them get the result).
@@ -178,31 +229,33 @@ __device__ __forceinline__ Joined join_row(const RowPieces& a, int64_t row, int6
   constexpr int U = 8;
   const int y = row < T ? a.targets[row] : -1;
   const bool live = y >= 0 && y < a.V;
-  const float hit = live ? a.hit[row] : 0.0f;
+  const float hit = live ? a.hits[row] : 0.0f;
   MaxSum r{-INFINITY, 0.0};
   for (int sp = sub; sp < a.splits; sp += 4 * U) {
-    float2 v[U];
+    MaxSum v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      v[u] = live && sp + 4 * u < a.splits ? a.part[row * a.splits + sp + 4 * u] : make_float2(-INFINITY, 0.0f);
+      v[u] = live && sp + 4 * u < a.splits ? a.part[row * a.splits + sp + 4 * u] : MaxSum{-INFINITY, 0.0};
     float m = r.m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].x);
+    for (int u = 0; u < U; ++u) m = fmaxf(m, v[u].m);
     const float z = at_max(m);
     double s = r.s * exp2_raw((r.m - z) * kLog2e);
 #pragma unroll
-    for (int u = 0; u < U; ++u) s += (double)(v[u].y * exp2_raw((v[u].x - z) * kLog2e));
+    for (int u = 0; u < U; ++u) s += v[u].s * exp2_raw((v[u].m - z) * kLog2e);
     r = {m, s};
   }
   r = join(r, MaxSum{__shfl_xor(r.m, 1, 64), __shfl_xor(r.s, 1, 64)});
   r = join(r, MaxSum{__shfl_xor(r.m, 2, 64), __shfl_xor(r.s, 2, 64)});
-  return {live, r, live ? target_logp(hit, r) : 0.0f};
+  if (!live) return {false, 0.0f, 1.0f, 0.0f};
+  const RowStats v = with_target(r, hit);
+  return {true, v.m, v.sum(), v.logp()};
 }
 
 __device__ __forceinline__ void put_joined(const RowPieces& a, int64_t row, int64_t T, const Joined& v, float* logp) {
   if (row >= T) return;
   logp[row] = v.logp;
-  a.stats[row] = v.live ? make_float2(v.r.m, static_cast<float>(v.r.s)) : make_float2(0.0f, 1.0f);
+  a.stats[row] = make_float2(v.m, v.sum);
 }
 
 __global__ __launch_bounds__(256) void join_kernel(RowPieces a, int64_t T, float* __restrict__ logp) {
@@ -392,7 +445,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
                                                                    int64_t dx_stride) {
   constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
   __shared__ MaxSum waves[WAVES];
-  __shared__ float shared_coef;
+  __shared__ float shared_coef, shared_own;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const int y = a.targets[row];
@@ -409,6 +462,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
     return;
   }
   const int body = vecs > H * THREADS ? vecs - H * THREADS : 0;
+  const LeftOut<E> target(y, vecs);
   MaxSum r{-INFINITY, 0.0};
   int i = tid;
   for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
@@ -416,13 +470,16 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
     typename Vec<E>::type w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = vload(p + (int64_t)(i + u * THREADS) * N);
+    target.template from<U>(w, i, THREADS);
 #pragma unroll
     for (int u = 0; u < U; ++u) Vec<E>::unpack(w[u], f + u * N);
     add_values<U * N>(r, f);
   }
   for (; i < body; i += THREADS) {
     float f[N];
-    Vec<E>::unpack(vload(p + (int64_t)i * N), f);
+    typename Vec<E>::type w = vload(p + (int64_t)i * N);
+    target.template from<1>(&w, i, 1);
+    Vec<E>::unpack(w, f);
     add_values<N>(r, f);
   }
   typename Vec<E>::type held[H];
@@ -433,33 +490,37 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
   for (int h = 0; h < H; ++h) {
     if (body + tid + h * THREADS < vecs) {
       float f[N];
-      Vec<E>::unpack(held[h], f);
+      typename Vec<E>::type w = held[h];
+      target.template from<1>(&w, body + tid + h * THREADS, 1);
+      Vec<E>::unpack(w, f);
       add_values<N>(r, f);
     }
   }
   float last = 0.0f;
   if (rest < V) {
     last = Vec<E>::value(p[rest]);
-    add_values<1>(r, &last);
+    if (rest != y) add_values<1>(r, &last);
   }
-  const MaxSum own = wave_join(r);
-  if ((tid & 63) == 0) waves[tid >> 6] = own;
+  const MaxSum part = wave_join(r);
+  if ((tid & 63) == 0) waves[tid >> 6] = part;
   __syncthreads();
-  MaxSum all = waves[0];
+  MaxSum others = waves[0];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) all = join(all, waves[w]);
+  for (int w = 1; w < WAVES; ++w) others = join(others, waves[w]);
+  const RowStats all = with_target(others, Vec<E>::value(p[y]));
   if (tid == 0) {
-    const float lp = target_logp(Vec<E>::value(p[y]), all);
+    const float lp = all.logp();
     const float2 v = policy_token(a, row, lp);
     logp[row] = lp;
     terms[row] = v.x;
     shared_coef = v.y * scale;
+    shared_own = -(v.y * scale) * expm1f(lp);
   }
   __syncthreads();
   // the second pass unpacks the held vectors anew: their float32 values would take twice the registers
 #pragma unroll
   for (int h = 0; h < H; ++h) asm volatile("" : "+v"(held[h]));
-  const float c = shared_coef, cs = -c / static_cast<float>(all.s), m = at_max(all.m);
+  const float own = shared_own, cs = -shared_coef / all.sum(), m = at_max(all.m);
   auto grad = [&](typename Vec<E>::type w, int j) {
     float f[N];
     Vec<E>::unpack(w, f);
@@ -468,14 +529,11 @@ __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, i
     if (static_cast<unsigned>(y - j) < N) {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (j + e == y) f[e] += c;
+        if (j + e == y) f[e] = own;
     }
     vstore_nt(q + j, Vec<E>::pack(f));
   };
-  if (rest < V) {
-    const float g = cs * exp2_raw((last - m) * kLog2e);
-    q[rest] = Vec<E>::round(rest == y ? g + c : g);
-  }
+  if (rest < V) q[rest] = Vec<E>::round(rest == y ? own : cs * exp2_raw((last - m) * kLog2e));
 #pragma unroll
   for (int h = 0; h < H; ++h)
     if (body + tid + h * THREADS < vecs) grad(held[h], (body + tid + h * THREADS) * N);
@@ -519,8 +577,10 @@ struct GradArgs {
 };
 
 // One piece of row `row`: coefficient c, statistics st; zeros for a masked row.
-template <class E>
-__device__ __forceinline__ void grad_piece(const GradArgs<E>& a, int64_t row, int piece, int y, float c, float2 st) {
+// own(g) is the entry at the target, whose softmax's part is g = -c p.
+template <class E, class F>
+__device__ __forceinline__ void grad_piece(const GradArgs<E>& a, int64_t row, int piece, int y, float c, float2 st,
+                                           F own) {
   constexpr int N = Vec<E>::N;
   const int lo = piece * kGradVecs * N;
   const int n = a.V - lo < kGradVecs * N ? a.V - lo : kGradVecs * N;
@@ -545,25 +605,77 @@ __device__ __forceinline__ void grad_piece(const GradArgs<E>& a, int64_t row, in
     if (static_cast<unsigned>(hit - tid * N) < N) {
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (tid * N + e == hit) f[e] += c;
+        if (tid * N + e == hit) f[e] = own(f[e]);
     }
     vstore_nt(q + tid * N, Vec<E>::pack(f));
   }
   if (rest < n) {
     const float g = cs * exp2_raw((Vec<E>::value(p[rest]) - m) * kLog2e);
-    q[rest] = Vec<E>::round(rest == hit ? g + c : g);
+    q[rest] = Vec<E>::round(rest == hit ? own(g) : g);
   }
+}
+
+// s below which a row's entry at the target is not c - c p with p from the
+// rounded s: that loses 2^-24 of c, which at 1 - p = 1/5 is 2^-21.7 of the
+// entry, and 2^-16 at 2^-8, far below half a step of bfloat16. Below, the
+// entry is -c expm1(logp), or target_kernel's.
+template <class E>
+constexpr float kLikely = sizeof(E) == 2 ? 1.00390625f : 1.25f;
+
+// The entries at the targets of such rows without their log probabilities:
+// one workgroup reads the row again and sums the others, then writes the
+// entry into dx, which may be x. The gradient of 8192 rows of 128256 bfloat16
+// (686 us, one set of inputs over and over) takes 2 us more where no row is
+// likely, 225 where half of them are, 427 where all are; with the log
+// probabilities nothing.
+template <class E>
+__global__ __launch_bounds__(256) void target_kernel(GradArgs<E> a, const int32_t* __restrict__ targets,
+                                                     const float2* __restrict__ stats, const float* __restrict__ coef,
+                                                     const float* __restrict__ grad_out, float scale) {
+  constexpr int N = Vec<E>::N;
+  __shared__ double lds[4];
+  const int64_t row = blockIdx.x;
+  const int y = targets[row];
+  const float2 st = stats[row];
+  if (y < 0 || y >= a.V || !(st.y < kLikely<E>)) return;
+  const E* p = a.x + row * a.stride;
+  const int tid = threadIdx.x, vecs = a.V / N;
+  const LeftOut<E> target(y, vecs);
+  const float m = at_max(st.x);
+  double sum = 0.0;
+#pragma unroll 4
+  for (int i = tid; i < vecs; i += 256) {
+    float f[N];
+    typename Vec<E>::type w = vload(p + (int64_t)i * N);
+    target.template from<1>(&w, i, 1);
+    Vec<E>::unpack(w, f);
+    sum += sum_exp<N>(f, m);
+  }
+  const int rest = vecs * N + tid;
+  if (rest < a.V && rest != y) sum += exp2_raw((Vec<E>::value(p[rest]) - m) * kLog2e);
+  sum = block_sum<4>(sum, lds);
+  if (tid != 0) return;
+  float c = coef[row] * scale;
+  if (grad_out != nullptr) c *= *grad_out;
+  const double e = exp2_raw((Vec<E>::value(p[y]) - m) * kLog2e);
+  a.dx[row * a.dx_stride + y] = Vec<E>::round(static_cast<float>(c * (sum / (sum + e))));
 }
 
 template <class E>
 __global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(GradArgs<E> a, const int32_t* __restrict__ targets,
                                                                const float2* __restrict__ stats,
+                                                               const float* __restrict__ logp,
                                                                const float* __restrict__ coef,
                                                                const float* __restrict__ grad_out, float scale) {
   const int64_t row = blockIdx.x / (unsigned)a.pieces;
   float c = coef[row] * scale;
   if (grad_out != nullptr) c *= *grad_out;
-  grad_piece(a, row, blockIdx.x % (unsigned)a.pieces, targets[row], c, stats[row]);
+  const float2 st = stats[row];
+  const int y = targets[row];
+  grad_piece(a, row, blockIdx.x % (unsigned)a.pieces, y, c, st, [&](float g) {
+    if (!(st.y < kLikely<E>)) return g + c;
+    return logp != nullptr ? -c * expm1f(logp[row]) : Vec<E>::value(a.dx[row * a.dx_stride + y]);
+  });
 }
 
 // The second half of a policy step by pieces: every workgroup joins the
@@ -592,7 +704,8 @@ __global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, R
   const Joined v = join_row(pieces, row, T, sub);
   if (piece == 0 && threadIdx.x == 0) logp[row] = v.logp;
   const float c = v.live ? policy_token(policy, row, v.logp).y * scale : 0.0f;
-  grad_piece(a, row, piece, policy.targets[row], c, make_float2(v.r.m, static_cast<float>(v.r.s)));
+  grad_piece(a, row, piece, policy.targets[row], c, make_float2(v.m, v.sum),
+             [&](float) { return -c * expm1f(v.logp); });
 }
 
 // ---------------------------------------------------------------------------
@@ -616,16 +729,17 @@ static int row_splits(int64_t T, int64_t V) {
 }
 
 struct LossPlan {
-  float2 *stats, *part;
-  float *hit, *coef;
+  float2* stats;
+  MaxSum* part;
+  float *hits, *coef;
   size_t bytes;
 };
 
 static LossPlan plan_loss(int64_t T, int64_t V, void* ws) {
   LossPlan l{};
   Carver w(ws);
-  l.part = static_cast<float2*>(w.take(row_splits(T, V) > 1 ? T * row_splits(T, V) * sizeof(float2) : 0));
-  l.hit = static_cast<float*>(w.take(row_splits(T, V) > 1 ? T * sizeof(float) : 0));
+  l.part = static_cast<MaxSum*>(w.take(row_splits(T, V) > 1 ? T * row_splits(T, V) * sizeof(MaxSum) : 0));
+  l.hits = static_cast<float*>(w.take(row_splits(T, V) > 1 ? T * sizeof(float) : 0));
   l.stats = static_cast<float2*>(w.take(T * sizeof(float2)));
   l.coef = static_cast<float*>(w.take(T * sizeof(float)));
   l.bytes = w.used;
@@ -656,7 +770,7 @@ static void by_type(const lora_mat* x, F f) {
 }
 
 static RowPieces row_pieces(const lora_mat* x, const int32_t* targets, float2* stats, const LossPlan& l) {
-  return {targets, x->cols, row_splits(x->rows, x->cols), l.part, l.hit, stats};
+  return {targets, x->cols, row_splits(x->rows, x->cols), l.part, l.hits, stats};
 }
 
 // Statistics of the rows, or of their pieces.
@@ -668,7 +782,7 @@ static void run_logp(const lora_mat* x, const int32_t* targets, float* logp, flo
     using E = std::remove_pointer_t<decltype(e)>;
     const int piece = static_cast<int>(round_up(ceil_div(V, splits), Vec<E>::N));
     launch(logp_kernel<E>, dim3(x->rows * splits), dim3(256), 0, st, (const E*)x->ptr, x->stride_row, targets, V,
-           splits, piece, logp, stats, l.part, l.hit);
+           splits, piece, logp, stats, l.part, l.hits);
   });
 }
 
@@ -697,13 +811,16 @@ static GradArgs<E> grad_args(const lora_mat* x, const lora_mat* dx) {
           dx->stride_row,                static_cast<int>(x->cols), static_cast<int>(pieces)};
 }
 
-static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* coef,
-                           const float* grad_out, float scale, const lora_mat* dx, hipStream_t st) {
+// logp: of the rows, or null.
+static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* logp,
+                           const float* coef, const float* grad_out, float scale, const lora_mat* dx, hipStream_t st) {
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
     const GradArgs<E> a = grad_args<E>(x, dx);
-    launch(logit_grad_kernel<E>, dim3(x->rows * a.pieces), dim3(kGradVecs), 0, st, a, targets, stats, coef, grad_out,
-           scale);
+    if (logp == nullptr)
+      launch(target_kernel<E>, dim3(x->rows), dim3(256), 0, st, a, targets, stats, coef, grad_out, scale);
+    launch(logit_grad_kernel<E>, dim3(x->rows * a.pieces), dim3(kGradVecs), 0, st, a, targets, stats, logp, coef,
+           grad_out, scale);
   });
 }
 
@@ -801,16 +918,28 @@ extern "C" int lora_policy_loss(const float* logp, int64_t T, int64_t V, const l
   return launch_status();
 }
 
-extern "C" int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* coef,
-                               const float* grad_out, float scale, const lora_mat* dlogits, void* stream) {
+static int logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* logp,
+                      const float* coef, const float* grad_out, float scale, const lora_mat* dlogits, void* stream) {
   if (!logits || !dlogits) return LORA_ERR_NULL;
   if (int e = check_logits(logits)) return e;
   if (int e = check_dlogits(logits, dlogits)) return e;
   if (logits->rows == 0 || logits->cols == 0) return LORA_OK;
   if (!targets || !stats || !coef || !logits->ptr || !dlogits->ptr) return LORA_ERR_NULL;
-  run_logit_grad(logits, targets, reinterpret_cast<const float2*>(stats), coef, grad_out, scale, dlogits,
+  run_logit_grad(logits, targets, reinterpret_cast<const float2*>(stats), logp, coef, grad_out, scale, dlogits,
                  static_cast<hipStream_t>(stream));
   return launch_status();
+}
+
+extern "C" int lora_logit_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* coef,
+                               const float* grad_out, float scale, const lora_mat* dlogits, void* stream) {
+  return logit_grad(logits, targets, stats, nullptr, coef, grad_out, scale, dlogits, stream);
+}
+
+extern "C" int lora_logit_grad_logp(const lora_mat* logits, const int32_t* targets, const float* stats,
+                                    const float* logp, const float* coef, const float* grad_out, float scale,
+                                    const lora_mat* dlogits, void* stream) {
+  if (!logp && logits && logits->rows > 0 && logits->cols > 0) return LORA_ERR_NULL;
+  return logit_grad(logits, targets, stats, logp, coef, grad_out, scale, dlogits, stream);
 }
 
 extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, const int32_t* seq_offsets,
@@ -833,7 +962,7 @@ extern "C" int lora_pref_step(const lora_mat* logits, const int32_t* targets, co
   launch(join ? pref_kernel<true> : pref_kernel<false>, dim3(1), dim3(1024), 0, st,
          row_pieces(logits, targets, l.stats, l), logp, T, seq_offsets, pairs, ref_logp, beta, label_smoothing, loss,
          seq_logp, l.coef);
-  if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, l.coef, nullptr, grad_scale, dlogits, st);
+  if (T > 0 && V > 0) run_logit_grad(logits, targets, l.stats, logp, l.coef, nullptr, grad_scale, dlogits, st);
   return launch_status();
 }
 

@@ -24,7 +24,7 @@ Ops (the addressing arrays are passed as the tensors of lora_addressing):
   embed(ids, table, scale, dtype) -> scale * table[ids]     (differentiable in table)
   embed_grad(ids, dy, num_rows, scale, dtype) -> dtable
   token_logp(logits, targets) -> (logp, stats)              (logp differentiable in logits)
-  logit_grad(logits, targets, stats, coef) -> dlogits
+  logit_grad(logits, targets, stats, coef, logp=None) -> dlogits
   pref_loss(logp, seq_offsets, ref_logp, beta, label_smoothing) -> (loss, seq_logp, coef)
   policy_loss(logp, targets, vocab, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef)
     -> (loss, coef)                                         (both losses differentiable in logp)
@@ -269,17 +269,19 @@ def _(logits, targets):
 
 
 @torch.library.custom_op(f"{_NS}::logit_grad", mutates_args=(), device_types="cuda")
-def logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, coef: torch.Tensor) -> torch.Tensor:
-    return train.lora_logit_grad(logits, targets, stats, coef)
+def logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, coef: torch.Tensor,
+               logp: torch.Tensor | None = None) -> torch.Tensor:
+    return train.lora_logit_grad(logits, targets, stats, coef, logp=logp)
 
 
 @logit_grad.register_fake
-def _(logits, targets, stats, coef):
+def _(logits, targets, stats, coef, logp=None):
     return logits.new_empty(logits.shape)
 
 
 def _logp_setup(ctx, inputs, output):
-    ctx.save_for_backward(*inputs, output[1])
+    # a copy of logp: what a caller writes over it does not matter here
+    ctx.save_for_backward(*inputs, output[1], output[0].clone())
     ctx.set_materialize_grads(False)
 
 
@@ -287,8 +289,8 @@ def _logp_backward(ctx, grad, grad_stats):
     _no_grad("stats", grad_stats)
     if grad is None:
         return None, None
-    logits, targets, stats = ctx.saved_tensors
-    return torch.ops.lora_amd.logit_grad(logits, targets, stats, grad.contiguous()), None
+    logits, targets, stats, logp = ctx.saved_tensors
+    return torch.ops.lora_amd.logit_grad(logits, targets, stats, grad.contiguous(), logp), None
 
 
 torch.library.register_autograd(f"{_NS}::token_logp", _logp_backward, setup_context=_logp_setup)

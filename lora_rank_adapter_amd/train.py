@@ -174,21 +174,27 @@ def lora_policy_loss(logp: torch.Tensor, targets: torch.Tensor, vocab: int, old_
 
 
 def lora_logit_grad(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, coef: torch.Tensor,
-                    grad_out: torch.Tensor | None = None, scale: float = 1.0,
-                    dlogits: torch.Tensor | None = None) -> torch.Tensor:
+                    grad_out: torch.Tensor | None = None, scale: float = 1.0, dlogits: torch.Tensor | None = None,
+                    logp: torch.Tensor | None = None) -> torch.Tensor:
     """dlogits[t] = scale * grad_out * coef[t] * (one at targets[t] - softmax(logits[t])). stats from
-    lora_token_logp on the same logits and targets, grad_out: float32 [] on the device or None. Returns dlogits
-    [T x V] of the logits' dtype: the given tensor (it may be the logits), else a new one."""
+    lora_token_logp on the same logits and targets, logp its log probabilities (without them rows with a likely
+    target are read once more), grad_out: float32 [] on the device or None. Returns dlogits [T x V] of the logits'
+    dtype: the given tensor (it may be the logits), else a new one."""
     lib = _lib.load()
     T = logits.shape[0]
     dev = logits.device
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    check("lora_logit_grad", lib.lora_logit_grad(
-        _matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
-        _vector("stats", stats, 2 * T, _F32, dev), _vector("coef", coef, T, _F32, dev),
-        None if grad_out is None else _vector("grad_out", grad_out, 1, _F32, dev), float(scale),
-        _matrix("dlogits", dlogits, dev), _queue(dev)))
+    head = (_matrix("logits", logits, dev), _vector("targets", targets, T, _I32, dev),
+            _vector("stats", stats, 2 * T, _F32, dev))
+    lp = None if logp is None else _vector("logp", logp, T, _F32, dev)
+    rest = (_vector("coef", coef, T, _F32, dev),
+            None if grad_out is None else _vector("grad_out", grad_out, 1, _F32, dev), float(scale),
+            _matrix("dlogits", dlogits, dev), _queue(dev))
+    if logp is None:
+        check("lora_logit_grad", lib.lora_logit_grad(*head, *rest))
+    else:
+        check("lora_logit_grad_logp", lib.lora_logit_grad_logp(*head, lp, *rest))
     return dlogits
 
 

@@ -509,7 +509,8 @@ int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float gr
  *   g' = grad_scale * g
  *   m  = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
- * in float32, t counted on the device so that a captured step replays right.
+ * in float32, roots and quotients rounded correctly, t counted on the device so
+ * that a captured step replays right.
  *
  * One tensor: numel consecutive elements of param (updated in place; f32, or
  * bf16, rounded once) and grad (f32 or bf16), each aligned to its elements;
@@ -535,9 +536,7 @@ typedef struct {
  *            block (of m, of sqrt(v)) over 448, codes are rounded to nearest
  *            even; a v above zero keeps at least the smallest code; a block
  *            whose largest magnitude is below 1e-30 is stored as zeros. The
- *            update of a step uses m and v before they are rounded. Scales,
- *            roots and the update's quotient are within a few float32
- *            roundings of these formulas.
+ *            update of a step uses m and v before they are rounded.
  *   m and v 16-byte aligned. step: one int32, the number of steps taken.
  */
 typedef struct {

@@ -102,22 +102,47 @@ struct StepConst {
   float alpha, inv_root, decay, gs;
 };
 
-// Square roots and reciprocals by the approximate instructions (within one
-// step of the last place, against half a step at ten times the cost). Below
-// 2^-96 the root is taken of v * 2^64, so that a denormal v keeps its root.
+// Roots and quotients rounded correctly: the approximate instruction's result
+// and Newton steps on its residual, which a fused product gives exactly (the
+// root checked for every float32 mantissa and both parities of the exponent,
+// the quotients for 5 10^7 pairs). Fewer instructions than the compiler's own
+// sequences, which count in the 8-bit form: 75.5 M elements take 230 us, 240
+// with those, 226 with the approximate results alone. 18.9 M with 32-bit
+// states take 96 us in all three.
+
+// Below 2^-96 the root is taken of v * 2^64, so that a denormal v keeps its
+// root. Zeros, infinities and NaN go through.
 __device__ __forceinline__ float root(float v) {
   const bool small = v < 0x1p-96f;
-  const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
-  return small ? r * 0x1p-32f : r;
+  const float x = small ? v * 0x1p64f : v;
+  const float y = __builtin_amdgcn_rsqf(x), g = x * y;
+  const float r = fmaf(fmaf(-g, g, x), 0.5f * y, g);
+  constexpr int kPositive = 0x180;  // normal or denormal
+  return __builtin_amdgcn_classf(v, kPositive) ? (small ? r * 0x1p-32f : r) : v;
+}
+// b is no denormal (eps, or the root of a v above zero); a denormal quotient
+// may be off by one step.
+__device__ __forceinline__ float quotient(float a, float b) {
+  float y = __builtin_amdgcn_rcpf(b);
+  y = fmaf(fmaf(-b, y, 1.0f), y, y);
+  const float q = a * y;
+  return __builtin_amdgcn_div_fixupf(fmaf(fmaf(-b, q, a), y, q), b, a);
+}
+__device__ __forceinline__ float over_448(float a) {
+  constexpr float y = 1.0f / 448.0f;
+  const float q = a * y;
+  return __builtin_amdgcn_div_fixupf(fmaf(fmaf(-448.0f, q, a), y, q), 448.0f, a);
 }
 
-__device__ __forceinline__ void adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
+// Returns the root of the new v.
+__device__ __forceinline__ float adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
   // the fused products are written out: a tensor's steps are the same bits in either kernel
   g *= k.gs;
   m = fmaf(a.b1, m, a.c1 * g);
   v = fmaf(a.b2, v, a.c2 * (g * g));
-  // the divisor is at least eps, or the root of a v above zero: no denormal, whose reciprocal would be lost
-  p = fmaf(-(k.alpha * m), __builtin_amdgcn_rcpf(fmaf(root(v), k.inv_root, a.eps)), p * k.decay);
+  const float w = root(v);
+  p = fmaf(p, k.decay, -quotient(k.alpha * m, fmaf(w, k.inv_root, a.eps)));
+  return w;
 }
 
 // four codes of one word as values, and back (rounded to nearest even)
@@ -150,8 +175,8 @@ __device__ __forceinline__ uint32_t quantise(float* x, bool positive, float* sca
   const float amax = wave_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
   // a block below 1e-30 is stored as zeros (448 / amax stays finite above it)
   const bool some = amax >= 1e-30f;
-  const float inv = some ? 448.0f * __builtin_amdgcn_rcpf(amax) : 0.0f;
-  *scale = some ? amax * (1.0f / 448.0f) : 0.0f;
+  const float inv = some ? 448.0f / amax : 0.0f;
+  *scale = some ? over_448(amax) : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float q = x[i] * inv;
@@ -243,15 +268,14 @@ struct Block {
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      adamw(p[j], m[j], v[j], g[j], k, a);
+      const float w = adamw(p[j], m[j], v[j], g[j], k, a);
+      if constexpr (BITS == 8) v[j] = w;
       // past the tensor's end the states stay zero
       if (j >= count) m[j] = v[j] = 0.0f;
     }
     store4(e.param, e.param_bf16, i, e.vec, count, p);
     if (e.shadow != nullptr) store4(e.shadow, true, i, e.vec, count, p);
     if constexpr (BITS == 8) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = root(v[j]);
       m_code = quantise(m, false, &m_scale);
       v_code = quantise(v, true, &v_scale);
       __builtin_nontemporal_store(m_code, reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s));

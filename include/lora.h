@@ -67,7 +67,8 @@ enum {
   LORA_ERR_RANK = -5,      /* rank outside [1, 128] (single adapter) or r_max outside [1, 128] */
   LORA_ERR_WORKSPACE = -6, /* workspace NULL or smaller than lora_workspace_bytes() */
   LORA_ERR_LAUNCH = -7,    /* a HIP launch failed */
-  LORA_ERR_LIMIT = -8      /* a size exceeds a documented library limit (e.g. S > 1024) */
+  LORA_ERR_LIMIT = -8,     /* a size exceeds a documented library limit (e.g. S > 1024) */
+  LORA_ERR_VALUE = -9      /* a scalar (not a size) outside its documented range */
 };
 
 /* A 2-D matrix view: element (i, j) is at ptr + i*stride_row + j*stride_col. */
@@ -448,6 +449,7 @@ int lora_token_logp(const lora_mat* logits, const int32_t* targets, float* logp,
  *   coef         float[T], out or NULL: d loss / d logp of each token (0
  *                outside the sequences).
  *   Sums and z are kept in float64. Also with T = 0 the loss is written.
+ *   LORA_ERR_VALUE unless beta is finite and 0 <= label_smoothing <= 1.
  */
 int lora_pref_loss(const float* logp, int64_t T, const int32_t* seq_offsets, int64_t pairs, const float* ref_logp,
                    float beta, float label_smoothing, float* loss, float* seq_logp, float* coef, void* stream);
@@ -471,6 +473,8 @@ typedef struct {
  *   loss  one float, out (summed in float64; also written with T = 0).
  *   coef  float[T], out or NULL: d loss / d logp (0 for masked tokens, whose
  *         other inputs are not used).
+ *   LORA_ERR_VALUE unless 1 - clip_low <= 1 + clip_high (either may be
+ *   infinite: no clipping on that side) and kl_coef is finite.
  */
 int lora_policy_loss(const float* logp, int64_t T, int64_t V, const lora_policy* policy, float* loss, float* coef,
                      void* stream);

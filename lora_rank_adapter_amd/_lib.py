@@ -30,6 +30,7 @@ STATUS = {
     -6: "LORA_ERR_WORKSPACE",
     -7: "LORA_ERR_LAUNCH",
     -8: "LORA_ERR_LIMIT",
+    -9: "LORA_ERR_VALUE",
 }
 
 

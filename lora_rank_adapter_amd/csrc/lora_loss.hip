@@ -29,6 +29,7 @@
 //   logit_grad_kernel the gradient's rows from the statistics and coefficients
 //   policy_grad_kernel  the same from the pieces of few long rows, and the policy loss
 
+#include <cmath>
 #include <type_traits>
 
 #include "lora_host.hpp"
@@ -862,6 +863,7 @@ static int check_pref(const int32_t* offsets, int64_t pairs, const float* ref, f
                       const float* loss) {
   if (!offsets || !ref || !loss) return LORA_ERR_NULL;
   if (pairs < 1 || pairs > (int64_t(1) << 30)) return LORA_ERR_SHAPE;
+  if (!std::isfinite(beta) || !(eps >= 0.0f && eps <= 1.0f)) return LORA_ERR_VALUE;
   return LORA_OK;
 }
 
@@ -869,6 +871,7 @@ static int check_policy(const lora_policy* p, int64_t T, const float* loss) {
   if (!p || !loss) return LORA_ERR_NULL;
   if (T > 0 && (!p->targets || !p->old_logp || !p->advantages || !p->weights)) return LORA_ERR_NULL;
   if (T > 0 && p->kl_coef != 0.0f && !p->ref_logp) return LORA_ERR_NULL;
+  if (!(p->clip_low + p->clip_high >= 0.0f) || !std::isfinite(p->kl_coef)) return LORA_ERR_VALUE;
   return LORA_OK;
 }
 

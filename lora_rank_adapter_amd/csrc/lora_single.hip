@@ -1724,6 +1724,7 @@ extern "C" const char* lora_status_string(int status) {
     case LORA_ERR_WORKSPACE: return "workspace missing or too small";
     case LORA_ERR_LAUNCH: return "HIP kernel launch failed";
     case LORA_ERR_LIMIT: return "a size exceeds a library limit";
+    case LORA_ERR_VALUE: return "a scalar is outside its range";
     default: return "unknown status";
   }
 }

@@ -574,7 +574,8 @@ int lora_adamw_table(const lora_adamw_tensor* tensors, int64_t n, void* table, s
  * shadow, m and v. `tensors` are the ones that the table was written from
  * (their sizes are checked, their addresses come from the table); a table
  * written from tensors of another number or total size updates nothing but
- * the count. With no elements nothing is launched.
+ * the count. With no elements nothing is launched. LORA_ERR_VALUE unless lr and
+ * weight_decay are finite, 0 <= beta < 1 for both and eps >= 0.
  */
 int lora_adamw_step(const lora_adamw_tensor* tensors, int64_t n, void* table, size_t table_bytes,
                     const lora_adamw_state* state, const lora_adamw_hyper* hyper, void* stream);

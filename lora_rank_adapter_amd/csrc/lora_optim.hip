@@ -21,6 +21,8 @@
 //   step_kernel    the update, 256 elements per wave at a time
 //   small_step_kernel  constants and update of a few chunks, one workgroup
 
+#include <cmath>
+
 #include "lora_host.hpp"
 #include "lora_rows.hpp"
 
@@ -423,6 +425,10 @@ extern "C" int lora_adamw_step(const lora_adamw_tensor* tensors, int64_t n, void
   if (!state || !hyper) return LORA_ERR_NULL;
   if (state->bits != 8 && state->bits != 32) return LORA_ERR_DTYPE;
   if (!state->step) return LORA_ERR_NULL;
+  auto fraction = [](double b) { return b >= 0.0 && b < 1.0; };
+  if (!std::isfinite(hyper->lr) || !std::isfinite(hyper->weight_decay) || !fraction(hyper->beta1) ||
+      !fraction(hyper->beta2) || !(hyper->eps >= 0.0))
+    return LORA_ERR_VALUE;
   if (size.elems > 0) {
     if (!state->m || !state->v || (state->bits == 8 && (!state->m_scale || !state->v_scale))) return LORA_ERR_NULL;
     if (!aligned(state->m, 16) || !aligned(state->v, 16)) return LORA_ERR_STRIDE;

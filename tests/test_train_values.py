@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import lora_rank_adapter_amd as L
-from lora_rank_adapter_amd._lib import LoraPolicy
-from tests.test_train_host import FAKE, by, m
+from lora_rank_adapter_amd._lib import LoraAdamwHyper, LoraAdamwState, LoraPolicy
+from tests.test_train_host import FAKE, by, m, tensors
 
 LAUNCH, VALUE = -7, -9
 INF, NAN = math.inf, math.nan
@@ -61,3 +61,18 @@ def test_policy_scalars(lib):
             assert f(*a) == VALUE, a
         for a in ((0.2, 0.2, 0.0), (0.0, 0.0, 0.1), (0.2, INF, 0.0), (INF, INF, -0.1)):
             assert f(*a) == LAUNCH, a
+
+
+def test_adamw_scalars(lib):
+    t = tensors(1000)
+
+    def step(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, decay=0.0):
+        st = LoraAdamwState(32, 0, FAKE, FAKE, None, None, FAKE)
+        h = LoraAdamwHyper(lr, beta1, beta2, eps, decay, None, None)
+        return lib.lora_adamw_step(t, 1, FAKE, 1 << 40, by(st), by(h), None)
+
+    for bad in (dict(lr=NAN), dict(lr=INF), dict(beta1=1.0), dict(beta1=-0.1), dict(beta1=NAN), dict(beta2=1.0),
+                dict(beta2=1.5), dict(beta2=NAN), dict(eps=-1e-8), dict(eps=NAN), dict(decay=NAN), dict(decay=INF)):
+        assert step(**bad) == VALUE, bad
+    for good in (dict(), dict(lr=0.0), dict(beta1=0.0, beta2=0.0), dict(eps=0.0), dict(lr=-1e-3)):
+        assert step(**good) == LAUNCH, good

@@ -416,7 +416,8 @@ int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float scale, const l
  *            log probability is 0 and its gradient zeros.
  *   dlogits  T x V of the logits' dtype, layout rules as for logits; it may
  *            be the logits themselves (same pointer and strides), otherwise
- *            it must not overlap them. Every element is written.
+ *            it must not overlap them (LORA_ERR_STRIDE; other columns of the
+ *            same rows, with the same pitch, do not). Every element is written.
  *   workspace: lora_loss_workspace_bytes(T, V), 256-byte aligned. Its contents
  *            do not matter before a call and have no meaning after it.
  * A row whose logits are all -inf, or that holds +inf or NaN, gives NaN.

@@ -803,10 +803,29 @@ static void run_join(const lora_mat* x, const int32_t* targets, float* logp, flo
 // 3 us each); more rows are spread over the card by join_kernel.
 static bool join_in_loss(int64_t T, int64_t V) { return T > 0 && T <= kJoinRows && row_splits(T, V) > 1; }
 
+// Whether two matrices of one shape and type, with rows of consecutive
+// elements, are the same memory throughout, or have none in common.
+static bool same_or_apart(const lora_mat* x, const lora_mat* dx) {
+  if (x->rows == 0 || x->cols == 0) return true;
+  const int64_t es = static_cast<int64_t>(elem_size(x->dtype)), width = x->cols * es;
+  const int64_t a = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x->ptr));
+  const int64_t b = static_cast<int64_t>(reinterpret_cast<uintptr_t>(dx->ptr));
+  const bool pitch = x->rows == 1 || x->stride_row == dx->stride_row;
+  if (a == b && pitch) return true;
+  const int64_t a_end = a + (x->rows - 1) * x->stride_row * es + width;
+  const int64_t b_end = b + (x->rows - 1) * dx->stride_row * es + width;
+  if (b >= a_end || a >= b_end) return true;
+  if (x->rows == 1 || !pitch) return false;
+  // columns of the same rows: each begins where the other has ended
+  const int64_t step = x->stride_row * es, shift = ((b - a) % step + step) % step;
+  return shift >= width && step - shift >= width;
+}
+
 static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;
   if (dx->dtype != x->dtype) return LORA_ERR_DTYPE;
   if (int e = check_logits(dx)) return e;
+  if (!same_or_apart(x, dx)) return LORA_ERR_STRIDE;
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
   return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;  // one more sums a policy loss
 }

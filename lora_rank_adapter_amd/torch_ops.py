@@ -35,7 +35,8 @@ addressing is -1 past the active tokens, so every output is fully defined. lora_
 weights in nn.Linear layout (A_w r x K, B_w L x r); its backward casts the
 incoming float32 gradient to x's dtype for the backward kernels (which take dy
 in the input dtype) and returns gradients in the dtypes and layouts of x, A_w
-and B_w. The losses' other outputs (stats, seq_logp, coef) have no gradient: asking
+and B_w. The losses' other outputs (stats, seq_logp, coef) have no gradient, nor have
+the losses for their other inputs (ref_logp, old_logp, advantages, weights): asking
 for one raises.
 """
 from __future__ import annotations
@@ -332,5 +333,21 @@ def _loss_backward(ctx, grad, *others):
     return (None if grad is None else grad * coef,) + (None,) * (ctx.inputs - 1)
 
 
-torch.library.register_autograd(f"{_NS}::pref_loss", _loss_backward, setup_context=_loss_setup)
-torch.library.register_autograd(f"{_NS}::policy_loss", _loss_backward, setup_context=_loss_setup)
+def _constants(ctx, names: dict) -> None:
+    for i, name in names.items():
+        if ctx.needs_input_grad[i]:
+            raise RuntimeError(f"the losses have no gradient for {name}: detach it")
+
+
+def _pref_backward(ctx, grad, *others):
+    _constants(ctx, {2: "ref_logp"})
+    return _loss_backward(ctx, grad, *others)
+
+
+def _policy_backward(ctx, grad, *others):
+    _constants(ctx, {3: "old_logp", 4: "advantages", 5: "weights", 8: "ref_logp"})
+    return _loss_backward(ctx, grad, *others)
+
+
+torch.library.register_autograd(f"{_NS}::pref_loss", _pref_backward, setup_context=_loss_setup)
+torch.library.register_autograd(f"{_NS}::policy_loss", _policy_backward, setup_context=_loss_setup)

@@ -401,6 +401,20 @@ struct PolicyArgs {
   float clip_low, clip_high, kl;
 };
 
+// exp(k) - k - 1 with e = expm1(k): e - k loses it to the rounding of e near
+// 0, where it is k^2 / 2. Its series ends within 2^-28 of it at 1/2.
+__device__ __forceinline__ float exp_beyond_linear(float k, float e) {
+  float s = 1.0f / 362880.0f;
+  s = fmaf(s, k, 1.0f / 40320.0f);
+  s = fmaf(s, k, 1.0f / 5040.0f);
+  s = fmaf(s, k, 1.0f / 720.0f);
+  s = fmaf(s, k, 1.0f / 120.0f);
+  s = fmaf(s, k, 1.0f / 24.0f);
+  s = fmaf(s, k, 1.0f / 6.0f);
+  s = fmaf(s, k, 0.5f);
+  return fabsf(k) < 0.5f ? s * (k * k) : e - k;
+}
+
 // One token of the policy loss: its weighted loss and d loss / d logp. The
 // derivative is a difference of two terms that may nearly cancel, so every
 // kernel has to round them alike: no products fused with sums here.
@@ -415,7 +429,7 @@ __device__ __forceinline__ float2 policy_token(const PolicyArgs& a, int64_t t, f
   if (a.ref_logp != nullptr) {
     const float k = a.ref_logp[t] - lp;
     const float e = expm1f(k);
-    l += a.kl * (e - k);
+    l += a.kl * exp_beyond_linear(k, e);
     d -= a.kl * e;
   }
   return make_float2(w * l, w * d);

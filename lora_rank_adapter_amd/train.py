@@ -253,8 +253,8 @@ class AdamW:
     buffers (float32 or bfloat16; the ones that lora_bwd_dx_da and lora_bwd_db write); shadows: None, or for each
     param None or a bfloat16 tensor that receives a float32 param's new value. All of a param's tensors have its
     shape: elements pair by their place, so the weights are kept the way their gradients lie (A as K x r, B as
-    r x L), not as transposes of them. The object holds these tensors and a device table of their addresses; `bind`
-    replaces the gradients, `step` refuses tensors whose memory moved.
+    r x L), not as transposes of them. No two params or shadows share memory. The object holds these tensors and a
+    device table of their addresses; `bind` replaces the gradients, `step` refuses tensors whose memory moved.
 
     The table and new states are written on the stream that is current in the constructor and in `bind`; a step on
     another stream waits for that. A step that was captured into a graph goes on with the tensors bound then, also
@@ -321,6 +321,10 @@ class AdamW:
             tensors[i] = LoraAdamwTensor(p.data_ptr() or None, g.data_ptr() or None,
                                          None if s is None else s.data_ptr() or None, p.numel(), _dtype_code(p),
                                          _dtype_code(g))
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for t in self.params + self.shadows if t is not None and t.numel())
+        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            raise ValueError("params and shadows share memory: each element can be updated once in a step")
         need = self._lib.lora_adamw_table_bytes(tensors, len(grads))
         table = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
         check("lora_adamw_table", self._lib.lora_adamw_table(tensors, len(grads), table.data_ptr(), need,

@@ -138,3 +138,18 @@ def test_operands_of_another_shape_are_refused(lib, shapes):
     L.AdamW([p], [p.clone()], 1e-3, shadows=[p.to(torch.bfloat16)])
     L.AdamW([p.view(-1)], [t.view(-1)], 1e-3)  # flat views pair as their owner says
     assert lib.tables == 2
+
+
+def test_memory_given_twice_is_refused(lib):
+    """Two entries over the same elements would be updated by two workgroups at once."""
+    p, q = torch.zeros(300), torch.zeros(900)
+    g = torch.zeros(300)
+    half = torch.zeros(600, dtype=torch.bfloat16)
+    for params, shadows in (([p, p], None), ([q[:300], q[299:599]], None), ([q[300:600], q[:600]], None),
+                            ([p, q[:300]], [half[:300], half[200:500]]), ([p, q[:300]], [half[:300], half[:300]]),
+                            ([p], [p.view(torch.bfloat16)[:300]])):
+        grads = [torch.zeros(t.numel()) for t in params]
+        with pytest.raises(ValueError, match="share memory"):
+            L.AdamW(params, grads, 1e-3, shadows=shadows)
+    # neighbours in one buffer, empty tensors, and gradients that are one tensor
+    L.AdamW([q[:300], q[300:600], q[300:300]], [g, g, g[:0]], 1e-3, shadows=[half[:300], half[300:], None])

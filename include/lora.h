@@ -409,8 +409,7 @@ int lora_embed_grad(const int32_t* ids, const lora_mat* dy, float scale, const l
  *            to its elements (any V and any row pitch); T below 2^24 (the
  *            losses on log probabilities: 2^25), V at most 2^31 - 2049. A
  *            gradient has a workgroup for every 4096 bytes begun of a row, in
- *            all below 2^24 - 1; the policy step below 2^23 rows of more than
- *            24 KB, 2^22 of more than 96 KB. LORA_ERR_LIMIT above.
+ *            all below 2^24 - 1. LORA_ERR_LIMIT above.
  *   targets  int32[T] device: the token whose log probability counts. A
  *            target outside [0, V) masks its row: the row is not read, its
  *            log probability is 0 and its gradient zeros.

@@ -841,7 +841,8 @@ static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (int e = check_logits(dx)) return e;
   if (!same_or_apart(x, dx)) return LORA_ERR_STRIDE;
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;  // one more sums a policy loss
+  // One more sums a policy loss. This covers rows that a workgroup of 8 or 16 waves takes: they have 7 or 25 pieces.
+  return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;
 }
 
 template <class E>
@@ -1016,7 +1017,6 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
   if (int e = check_policy(policy, T, loss)) return e;
   if (int e = check_logits(logits)) return e;
   if (int e = check_dlogits(logits, dlogits)) return e;
-  if (policy_by_rows(T, V) && T > max_blocks(64 * policy_waves(logits))) return LORA_ERR_LIMIT;
   if (T > 0 && (!logp || (V > 0 && (!logits->ptr || !dlogits->ptr)))) return LORA_ERR_NULL;
   const LossPlan l = plan_loss(T, V, workspace);
   if (T > 0)

@@ -841,7 +841,7 @@ static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
   if (int e = check_logits(dx)) return e;
   if (!same_or_apart(x, dx)) return LORA_ERR_STRIDE;
   const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  // One more sums a policy loss. This covers rows that a workgroup of 8 or 16 waves takes: they have 7 or 25 pieces.
+  // One more sums a policy loss. This covers rows that a workgroup of 8 or 16 waves takes: they have 11 pieces or more.
   return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;
 }
 
@@ -867,16 +867,28 @@ static void run_logit_grad(const lora_mat* x, const int32_t* targets, const floa
 
 // The policy step by rows (one workgroup takes a row from its statistics to
 // its gradient, one read of it from HBM) or split (statistics, then the
-// gradient, many workgroups to a row). A row of 128256 bfloat16 keeps one CU
-// busy for 20 us: 40 of them take 20 us by rows and 16 split, 128 of them 25
-// and 28, 8192 of them 737 and 1046; a row of 32000 takes 10 us either way.
-static bool policy_by_rows(int64_t T, int64_t V) { return T == 0 || T >= 128 || V <= 49152; }
+// gradient, many workgroups to a row). By rows the time is that of one row
+// until the card is full, split it is that of all bytes. us a call, no row
+// masked, by rows and split:
+//   bfloat16  40000 columns: 40 rows 15.0, 13.4; 96 rows 15.1, 14.7
+//            128256: 40 rows 24.5, 17.1; 72 rows 24.8, 24.0; 88 rows 25.1, 27.5; 128 rows 25, 35
+//   float32   40000: 40 rows 14.7, 13.4; 56 rows 14.9, 15.2
+//            128256: 40 rows 26.4, 25.2; 48 rows 26.5, 27.9; 96 rows 29.6, 46.5
+// Rows of up to 32000 take the same either way with few of them, and less by
+// rows with more (bfloat16, 192 rows: 13.8, 20.0).
+static bool policy_by_rows(const lora_mat* x) {
+  return x->rows == 0 || x->rows >= (x->dtype == LORA_F32 ? 48 : 80) || x->cols <= 32768;
+}
 
-// 8192 rows of bfloat16 by 4, 8 and 16 waves: 4000 columns 28, 41, 82 us; 11000: 66, 67, 110;
-// 32000: 193, 170, 192; 64000: 401, 374, 345; 128256: 839, 798, 737
+// Waves to a row. us a call of 8192 rows of bfloat16 (4096 of float32), no row
+// masked, with 4, 8 and 16 waves:
+//   bfloat16  4000 columns 37, 55, 108; 16000: 94, 100, 158; 24000: 143, 141, 191;
+//            49152: 320, 289, 306; 64000: 423, 394, 377; 128256: 869, 827, 783
+//   float32   4000: 29, 34, 60; 8000: 52, 52, 69; 13000: 87, 81, 85; 24000: 160, 140, 137;
+//            32000: 216, 197, 177; 128256: 987, 862, 836
 static int policy_waves(const lora_mat* x) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
-  return vecs <= 1536 ? 4 : vecs <= 6144 ? 8 : 16;
+  return vecs <= 2560 ? 4 : vecs <= 6144 ? 8 : 16;
 }
 
 static void run_policy_rows(const lora_mat* x, const PolicyArgs& a, float scale, float* logp, float* terms,
@@ -1023,7 +1035,7 @@ extern "C" int lora_policy_step(const lora_mat* logits, const lora_policy* polic
     if (int e = check_workspace(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
   const PolicyArgs a = policy_args(policy);
-  if (policy_by_rows(T, V)) {
+  if (policy_by_rows(logits)) {
     if (T > 0) run_policy_rows(logits, a, grad_scale, logp, l.coef, dlogits, st);
     launch(sum_kernel, dim3(1), dim3(1024), 0, st, (const float*)l.coef, T, loss);
     return launch_status();

@@ -99,7 +99,8 @@ struct RowStats {
   double t;       // the others' sum
   __device__ __forceinline__ float sum() const { return static_cast<float>(t + e); }
   __device__ __forceinline__ float logp() const {
-    return static_cast<float>(((double)x - m) - (e == 1.0f ? log1p(t) : log(t + e)));
+    // t + e is at least 1; with a target that is the largest e - 1 is 0 and t keeps its own precision
+    return static_cast<float>(((double)x - m) - log1p(t + ((double)e - 1.0)));
   }
 };
 __device__ __forceinline__ RowStats with_target(MaxSum others, float x) {

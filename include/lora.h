@@ -540,7 +540,8 @@ typedef struct {
  *            block (of m, of sqrt(v)) over 448, codes are rounded to nearest
  *            even; a v above zero keeps at least the smallest code; a block
  *            whose largest magnitude is below 1e-30 is stored as zeros. The
- *            update of a step uses m and v before they are rounded.
+ *            update of a step uses m and v before they are rounded. A NaN
+ *            stays with its element, an infinite m or v makes its block NaN.
  *   m and v 16-byte aligned. step: one int32, the number of steps taken.
  */
 typedef struct {

@@ -41,7 +41,7 @@ namespace lora {
 // rest: the float32 alone is off by 1.3e-8 of every exponent, to the same side
 // in all terms of a sum (1.6e-7 of them for d from -16 to -8, 5e-9 with the
 // rest). One product more, which costs the preference step of 8192 x 128256
-// bfloat16 2 us of 792 and the policy step nothing.
+// bfloat16 2 us of 794 and the policy step nothing.
 __device__ __forceinline__ float exp_of(float d) {
   constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0c0p-26f;
   return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * kRest));
@@ -142,8 +142,8 @@ struct LeftOut {
 
 // One read of the row or piece, four 16-byte loads per lane in flight, each
 // used once (non-temporal: by the default policy 8% slower): 8192 rows of
-// 128256 bfloat16, 1.39 GB of them unmasked, in 208 us (6.7 TB/s), the rate
-// of a plain read.
+// 128256 bfloat16, 1.39 GB of them unmasked, in 217 us (6.4 TB/s, where a
+// plain read reaches 6.7).
 template <class E>
 __global__ __launch_bounds__(256) void logp_kernel(const E* __restrict__ x, int64_t stride,
                                                    const int32_t* __restrict__ targets, int V, int splits, int piece,
@@ -308,8 +308,8 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 // with fewer than 8 pairs, a part of one), 64 lanes take a pair each, and the
 // waves give their tokens the coefficients beta * dz / pairs and minus that.
 // With JOIN the log probabilities are joined from their rows' pieces first.
-// A chain of dependent loads and sums bounds it: 5.5 us for 8 pairs of 8192
-// tokens, as for one pair of 96 with its join.
+// A chain of dependent loads and sums bounds it: 5.7 us for 8 pairs of 8192
+// tokens, 6.3 for one pair of 96 with its join.
 template <bool JOIN>
 __global__ __launch_bounds__(1024) void pref_kernel(RowPieces pieces, float* logp_out, int64_t T,
                                                     const int32_t* __restrict__ offsets, int64_t pairs,
@@ -456,9 +456,9 @@ __global__ __launch_bounds__(1024) void policy_kernel(const float* __restrict__ 
 // policy step: a token's coefficient needs nothing but its own row, so one
 // workgroup takes a row from its statistics to its gradient. The row's last
 // H vectors per lane stay in registers between the two passes; the others are
-// read again, the most recently read first. 8192 x 128256 bfloat16 takes 637
+// read again, the most recently read first. 8192 x 128256 bfloat16 takes 638
 // us: 1.39 GB of unmasked rows leave the L2 once and half of them a second
-// time, 2.1 GB are written, and the vector units are two thirds busy.
+// time, 2.1 GB are written, and the vector units are three quarters busy.
 // ---------------------------------------------------------------------------
 template <class E, int WAVES, int H>
 __global__ __launch_bounds__(64 * WAVES, 8) void policy_row_kernel(const E* x, int64_t stride, int V, PolicyArgs a,
@@ -584,8 +584,9 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ ter
 // ---------------------------------------------------------------------------
 // gradient: a workgroup takes one piece of a row, a vector per lane. Memory
 // that many short workgroups write in the order of its addresses goes faster
-// than what fewer, longer ones write: 8192 x 128256 bfloat16 takes 568 us
-// with one vector per lane, 602 with two, 637 with four.
+// than what fewer, longer ones write: 8192 x 128256 bfloat16 takes 571 us
+// with one vector per lane (568 when 602 were measured with two and 637 with
+// four).
 // ---------------------------------------------------------------------------
 constexpr int kGradVecs = 256;
 
@@ -703,7 +704,8 @@ __global__ __launch_bounds__(kGradVecs) void logit_grad_kernel(GradArgs<E> a, co
 // The second half of a policy step by pieces: every workgroup joins the
 // pieces of its row and finds its coefficient itself, and one more at the end
 // of the grid sums the rows' losses, so that nothing stands between the two
-// launches (40 rows of 128256: 23 us a call, with a kernel between them 25).
+// launches (40 rows of 128256: 16.3 us a call; a kernel between the two took
+// 2 us more).
 template <class E>
 __global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, RowPieces pieces, int64_t T,
                                                                 PolicyArgs policy, float scale,
@@ -740,8 +742,9 @@ constexpr int64_t kMaxRows = kMaxBlocks;  // of logits: a workgroup at least for
 constexpr int kMaxSplits = 64;            // pieces of one row, few enough rows then
 
 // Pieces per row: about as many as give 1024 workgroups (4 per CU), of at
-// least 4096 logits each. A preference step of 700 x 128256 bfloat16 takes 98
-// us so, 101 with 2048 workgroups, 100 with 512; 700 x 32000 32.4, 34.5, 33.1.
+// least 4096 logits each. A preference step of 700 x 128256 bfloat16 takes
+// 100.0 us so, 101.1 with 2048 workgroups, 100.8 with 512; 700 x 32000 35.2,
+// 37.2, 35.1.
 static int row_splits(int64_t T, int64_t V) {
   const int64_t rows = T < 1 ? 1 : T;
   int64_t s = (1024 + rows / 2) / rows;

@@ -231,10 +231,11 @@ __device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, bool vec, 
 
 // One wave updates a block of 256 elements of a tensor, 4 per lane: what it
 // loads, and the update from there. On tensors that the caches do not hold,
-// 18.9 M elements with 32-bit states take 99 us with every access
-// non-temporal, 110 with the loads or the stores alone, 112 with neither;
-// 75.5 M with 8-bit states 229 us with all but the loads of param and grad,
-// 237 with those as well, 244 with neither stores nor loads of the floats.
+// 18.9 M elements with 32-bit states take 96 us with every access
+// non-temporal (99 when 110 were measured with the loads or the stores alone
+// and 112 with neither); 75.5 M with 8-bit states 230 us with all but the
+// loads of param and grad (229 when it was 237 with those as well and 244 with
+// neither stores nor loads of the floats).
 template <int BITS>
 struct Block {
   static constexpr bool kNt = BITS == 32;
@@ -301,8 +302,8 @@ __device__ __forceinline__ const int32_t* chunk_map(const void* table, int64_t n
   return reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
 }
 
-// One block to a wave: 75.5 M elements with 8-bit states take 244 us so, 265
-// with two blocks to a wave and 274 with four.
+// One block to a wave: 75.5 M elements with 8-bit states take 230 us so (244
+// when 265 were measured with two blocks to a wave and 274 with four).
 template <int BITS>
 __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
   const auto* h = static_cast<const TableHead*>(table);
@@ -318,8 +319,8 @@ __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64
 }
 
 // A few chunks in one workgroup, which computes the constants itself: one
-// launch instead of two. Two adapter weights of 4096 elements: 6.0 us a step
-// against 7.8; beyond kSmall chunks one CU is too slow for the data.
+// launch instead of two. Two adapter weights of 4096 elements: 6.4 us a step
+// against 7.6; beyond kSmall chunks one CU is too slow for the data.
 constexpr int kSmall = 16;
 
 template <int BITS>

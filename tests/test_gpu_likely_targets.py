@@ -137,3 +137,31 @@ def test_rows_sum_to_nothing(T, V):
     for lp in (None, logp):
         dx = f64(L.lora_logit_grad(x, y, stats, torch.ones(T, device=DEV), logp=lp))
         assert (np.abs(dx.sum(1)) <= (3 * err + 2.0 ** -21 + 4 * H / 0.2) * q + V * 1e-37).all()
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_captured_gradient_replays(given):
+    note(f"likely targets, graph {given}")
+    x, y = make(40, 9001, BF)
+    coef = torch.randn(40, device=DEV)
+    out = torch.empty_like(x)
+
+    def call(x, out):
+        logp, stats = L.lora_token_logp(x, y)
+        return L.lora_logit_grad(x, y, stats, coef, dlogits=out, logp=logp if given else None)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(x, out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(x, out)
+    for i in range(4):
+        x.mul_(0.9)  # some rows cease to be likely
+        coef.neg_()
+        want = call(x, torch.empty_like(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i

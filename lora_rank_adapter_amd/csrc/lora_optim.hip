@@ -108,19 +108,34 @@ struct StepConst {
 // and Newton steps on its residual, which a fused product gives exactly (the
 // root checked for every float32 mantissa and both parities of the exponent,
 // the quotients for 5 10^7 pairs). Fewer instructions than the compiler's own
-// sequences, which count in the 8-bit form: 75.5 M elements take 230 us, 240
-// with those, 226 with the approximate results alone. 18.9 M with 32-bit
-// states take 96 us in all three.
+// sequences, which count in the 8-bit form: 75.5 M elements take 227 us, 240
+// with those, 228 with the approximate results alone. 18.9 M with 32-bit
+// states take 97 us in all three.
 
+__device__ __forceinline__ float ordinary_root(float x) {
+  const float y = __builtin_amdgcn_rsqf(x), g = x * y;
+  return fmaf(fmaf(-g, g, x), 0.5f * y, g);
+}
 // Below 2^-96 the root is taken of v * 2^64, so that a denormal v keeps its
 // root. Zeros, infinities and NaN go through.
-__device__ __forceinline__ float root(float v) {
+__device__ __forceinline__ float any_root(float v) {
   const bool small = v < 0x1p-96f;
-  const float x = small ? v * 0x1p64f : v;
-  const float y = __builtin_amdgcn_rsqf(x), g = x * y;
-  const float r = fmaf(fmaf(-g, g, x), 0.5f * y, g);
+  const float r = ordinary_root(small ? v * 0x1p64f : v);
   constexpr int kPositive = 0x180;  // normal or denormal
   return __builtin_amdgcn_classf(v, kPositive) ? (small ? r * 0x1p-32f : r) : v;
+}
+// Four of each lane; most waves have ordinary values alone (the 8-bit form
+// with any_root for all 230 us).
+__device__ __forceinline__ void roots(const float* v, float* w) {
+  const float low = fminf(fminf(v[0], v[1]), fminf(v[2], v[3]));
+  const float high = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+  if (__ballot(!(low >= 0x1p-96f && high < INFINITY)) == 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = ordinary_root(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = any_root(v[j]);
+  }
 }
 // b is no denormal (eps, or the root of a v above zero); a denormal quotient
 // may be off by one step.
@@ -136,15 +151,20 @@ __device__ __forceinline__ float over_448(float a) {
   return __builtin_amdgcn_div_fixupf(fmaf(fmaf(-448.0f, q, a), y, q), 448.0f, a);
 }
 
-// Returns the root of the new v.
-__device__ __forceinline__ float adamw(float& p, float& m, float& v, float g, const StepConst& k, const StepArgs& a) {
+// Four elements; w receives the roots of the new v.
+__device__ __forceinline__ void adamw(float* p, float* m, float* v, const float* g, const StepConst& k,
+                                      const StepArgs& a, float* w) {
   // the fused products are written out: a tensor's steps are the same bits in either kernel
-  g *= k.gs;
-  m = fmaf(a.b1, m, a.c1 * g);
-  v = fmaf(a.b2, v, a.c2 * (g * g));
-  const float w = root(v);
-  p = fmaf(p, k.decay, -quotient(k.alpha * m, fmaf(w, k.inv_root, a.eps)));
-  return w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float s = g[j] * k.gs;
+    m[j] = fmaf(a.b1, m[j], a.c1 * s);
+    v[j] = fmaf(a.b2, v[j], a.c2 * (s * s));
+  }
+  roots(v, w);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    p[j] = fmaf(p[j], k.decay, -quotient(k.alpha * m[j], fmaf(w[j], k.inv_root, a.eps)));
 }
 
 // four codes of one word as values, and back (rounded to nearest even)
@@ -231,9 +251,9 @@ __device__ __forceinline__ void store4(void* p, bool bf16, int64_t i, bool vec, 
 
 // One wave updates a block of 256 elements of a tensor, 4 per lane: what it
 // loads, and the update from there. On tensors that the caches do not hold,
-// 18.9 M elements with 32-bit states take 96 us with every access
+// 18.9 M elements with 32-bit states take 97 us with every access
 // non-temporal (99 when 110 were measured with the loads or the stores alone
-// and 112 with neither); 75.5 M with 8-bit states 230 us with all but the
+// and 112 with neither); 75.5 M with 8-bit states 227 us with all but the
 // loads of param and grad (229 when it was 237 with those as well and 244 with
 // neither stores nor loads of the floats).
 template <int BITS>
@@ -269,10 +289,11 @@ struct Block {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] *= v[j];
     }
+    float w[4];
+    adamw(p, m, v, g, k, a, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float w = adamw(p[j], m[j], v[j], g[j], k, a);
-      if constexpr (BITS == 8) v[j] = w;
+      if constexpr (BITS == 8) v[j] = w[j];
       // past the tensor's end the states stay zero
       if (j >= count) m[j] = v[j] = 0.0f;
     }
@@ -302,7 +323,7 @@ __device__ __forceinline__ const int32_t* chunk_map(const void* table, int64_t n
   return reinterpret_cast<const int32_t*>(static_cast<const char*>(table) + chunk_map_offset(n));
 }
 
-// One block to a wave: 75.5 M elements with 8-bit states take 230 us so (244
+// One block to a wave: 75.5 M elements with 8-bit states take 227 us so (244
 // when 265 were measured with two blocks to a wave and 274 with four).
 template <int BITS>
 __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64_t elems, StepArgs a) {
@@ -319,8 +340,8 @@ __global__ __launch_bounds__(256) void step_kernel(void* table, int64_t n, int64
 }
 
 // A few chunks in one workgroup, which computes the constants itself: one
-// launch instead of two. Two adapter weights of 4096 elements: 6.4 us a step
-// against 7.6; beyond kSmall chunks one CU is too slow for the data.
+// launch instead of two. Two adapter weights of 4096 elements: 6.2 us a step
+// against 8.8; beyond kSmall chunks one CU is too slow for the data.
 constexpr int kSmall = 16;
 
 template <int BITS>

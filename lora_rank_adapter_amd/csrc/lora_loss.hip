@@ -32,8 +32,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "lora_host.hpp"
-#include "lora_rows.hpp"
+#include "lora_softmax.hpp"
 
 namespace lora {
 
@@ -58,7 +57,6 @@ struct MaxSum {
   float m;
   double s;
 };
-__device__ __forceinline__ float at_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
 template <int N>
 __device__ __forceinline__ float sum_exp(const float* f, float z) {
@@ -108,37 +106,6 @@ __device__ __forceinline__ RowStats with_target(MaxSum others, float x) {
   const float z = at_max(m);
   return {x, m, exp_of(x - z), others.s * exp_of(others.m - z)};
 }
-
-// Element `at` of a row's piece (-1: it is elsewhere), which the sums leave
-// out: -inf takes its place in the loaded vector that holds it.
-template <class E>
-struct LeftOut {
-  static constexpr int N = Vec<E>::N;
-  int vector;  // -1: none of the piece's vectors
-  uint32_t keep[4], put[4];
-  __device__ __forceinline__ LeftOut(int at, int vecs) {
-    vector = at >= 0 && at < vecs * N ? at / N : -1;
-    const int e = at & (N - 1), word = N == 8 ? e >> 1 : e;
-    const uint32_t mask = N == 4 ? 0xFFFFFFFFu : e & 1 ? 0xFFFF0000u : 0x0000FFFFu;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      keep[k] = k == word ? ~mask : 0xFFFFFFFFu;
-      put[k] = k == word ? mask & 0xFF80FF80u & (N == 4 ? 0xFFFF0000u : 0xFFFFFFFFu) : 0u;
-    }
-  }
-  // U vectors that are `step` (a power of two) apart, from vector i on
-  template <int U>
-  __device__ __forceinline__ void from(typename Vec<E>::type* w, int i, int step) const {
-    const int d = vector - i;
-    if ((d & ~((U - 1) * step)) != 0) return;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (d == u * step) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[u][k] = (w[u][k] & keep[k]) | put[k];
-      }
-  }
-};
 
 // One read of the row or piece, four 16-byte loads per lane in flight, each
 // used once (non-temporal: by the default policy 8% slower): 8192 rows of
@@ -288,18 +255,6 @@ __device__ __forceinline__ void join_rows(const RowPieces& a, int64_t T, float* 
 // ---------------------------------------------------------------------------
 // losses on the log probabilities (one workgroup: a few values per token)
 // ---------------------------------------------------------------------------
-
-// The sum of v over the workgroup's waves, in their order.
-template <int WAVES = 16>
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double total = 0.0;
-  for (int w = 0; w < WAVES; ++w) total += lds[w];
-  __syncthreads();
-  return total;
-}
 
 // z = beta * ((S_c - ref_c) - (S_r - ref_r)); loss = mean of
 // -(1 - eps) log sigmoid(z) - eps log sigmoid(-z), whose derivative by z is
@@ -588,17 +543,6 @@ __global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ ter
 // with one vector per lane (568 when 602 were measured with two and 637 with
 // four).
 // ---------------------------------------------------------------------------
-constexpr int kGradVecs = 256;
-
-template <class E>
-struct GradArgs {
-  const E* x;
-  int64_t stride;
-  E* dx;  // may be x: a vector is stored by the lane that loaded it
-  int64_t dx_stride;
-  int V, pieces;
-};
-
 // One piece of row `row`: coefficient c, statistics st; zeros for a masked row.
 // own(g) is the entry at the target, whose softmax's part is g = -c p.
 template <class E, class F>
@@ -737,8 +681,6 @@ __global__ __launch_bounds__(kGradVecs) void policy_grad_kernel(GradArgs<E> a, R
 // ---------------------------------------------------------------------------
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 25) - 1;  // of the losses on log probabilities
-constexpr int64_t kMaxBlocks = max_blocks(256);
-constexpr int64_t kMaxRows = kMaxBlocks;  // of logits: a workgroup at least for each
 constexpr int kMaxSplits = 64;            // pieces of one row, few enough rows then
 
 // Pieces per row: about as many as give 1024 workgroups (4 per CU), of at
@@ -771,27 +713,8 @@ static LossPlan plan_loss(int64_t T, int64_t V, void* ws) {
   return l;
 }
 
-static int check_logits(const lora_mat* m) {
-  if (!float_dtype_ok(m->dtype)) return LORA_ERR_DTYPE;
-  if (!valid_dims(m)) return LORA_ERR_SHAPE;
-  if (m->cols > 1 && m->stride_col != 1) return LORA_ERR_STRIDE;
-  if (m->rows > 1 && m->stride_row < m->cols) return LORA_ERR_STRIDE;
-  if (!aligned(m->ptr, elem_size(m->dtype))) return LORA_ERR_STRIDE;
-  if (m->rows > kMaxRows || m->cols > 0x7FFFFFFF - 8 * kGradVecs) return LORA_ERR_LIMIT;
-  return LORA_OK;
-}
-
 static int check_workspace(const LossPlan& l, void* ws, size_t bytes) {
   return !ws || bytes < l.bytes || !aligned(ws, 256) ? LORA_ERR_WORKSPACE : LORA_OK;
-}
-
-// f with a null pointer of the logits' element type
-template <class F>
-static void by_type(const lora_mat* x, F f) {
-  if (x->dtype == LORA_F32)
-    f(static_cast<float*>(nullptr));
-  else
-    f(static_cast<uint16_t*>(nullptr));
 }
 
 static RowPieces row_pieces(const lora_mat* x, const int32_t* targets, float2* stats, const LossPlan& l) {
@@ -820,41 +743,6 @@ static void run_join(const lora_mat* x, const int32_t* targets, float* logp, flo
 // Few rows are joined by the loss's own workgroup, which saves a launch (about
 // 3 us each); more rows are spread over the card by join_kernel.
 static bool join_in_loss(int64_t T, int64_t V) { return T > 0 && T <= kJoinRows && row_splits(T, V) > 1; }
-
-// Whether two matrices of one shape and type, with rows of consecutive
-// elements, are the same memory throughout, or have none in common.
-static bool same_or_apart(const lora_mat* x, const lora_mat* dx) {
-  if (x->rows == 0 || x->cols == 0) return true;
-  const int64_t es = static_cast<int64_t>(elem_size(x->dtype)), width = x->cols * es;
-  const int64_t a = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x->ptr));
-  const int64_t b = static_cast<int64_t>(reinterpret_cast<uintptr_t>(dx->ptr));
-  const bool pitch = x->rows == 1 || x->stride_row == dx->stride_row;
-  if (a == b && pitch) return true;
-  const int64_t a_end = a + (x->rows - 1) * x->stride_row * es + width;
-  const int64_t b_end = b + (x->rows - 1) * dx->stride_row * es + width;
-  if (b >= a_end || a >= b_end) return true;
-  if (x->rows == 1 || !pitch) return false;
-  // columns of the same rows: each begins where the other has ended
-  const int64_t step = x->stride_row * es, shift = ((b - a) % step + step) % step;
-  return shift >= width && step - shift >= width;
-}
-
-static int check_dlogits(const lora_mat* x, const lora_mat* dx) {
-  if (dx->rows != x->rows || dx->cols != x->cols) return LORA_ERR_SHAPE;
-  if (dx->dtype != x->dtype) return LORA_ERR_DTYPE;
-  if (int e = check_logits(dx)) return e;
-  if (!same_or_apart(x, dx)) return LORA_ERR_STRIDE;
-  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * vec_elems(x->dtype));
-  // One more sums a policy loss. This covers rows that a workgroup of 8 or 16 waves takes: they have 11 pieces or more.
-  return x->rows * pieces >= kMaxBlocks ? LORA_ERR_LIMIT : LORA_OK;
-}
-
-template <class E>
-static GradArgs<E> grad_args(const lora_mat* x, const lora_mat* dx) {
-  const int64_t pieces = ceil_div(x->cols, int64_t(kGradVecs) * Vec<E>::N);
-  return {static_cast<const E*>(x->ptr), x->stride_row,          static_cast<E*>(dx->ptr),
-          dx->stride_row,                static_cast<int>(x->cols), static_cast<int>(pieces)};
-}
 
 // logp: of the rows, or null.
 static void run_logit_grad(const lora_mat* x, const int32_t* targets, const float2* stats, const float* logp,

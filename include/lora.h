@@ -12,7 +12,8 @@
  *     shrink, expand_fused, gather_shrink;
  *   - the operators of a training step around the adapter linears: embedding
  *     lookup and its gradient, token log probabilities with the preference
- *     and policy losses on them and the gradient of the logits, and an AdamW
+ *     and policy losses on them and the gradient of the logits, entropy and
+ *     top alternatives, distillation from a teacher's top tokens, and an AdamW
  *     step over many tensors.
  *
  * Conventions (all entry points):
@@ -508,6 +509,96 @@ int lora_pref_step(const lora_mat* logits, const int32_t* targets, const int32_t
                    void* stream);
 int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float grad_scale, float* loss, float* logp,
                      const lora_mat* dlogits, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Entropy and alternatives of next-token logits. With tau = temperature (in
+ * [1e-6, 1e6], else LORA_ERR_VALUE) and p_t = softmax(x[t] / tau):
+ *   targets  int32[T] or NULL (every row counts); rules of logits and targets
+ *            as above, a masked row has the values given in brackets.
+ *   logp     float[T], out; NULL exactly if targets is: log p_t[y_t] (0).
+ *   entropy  float[T], out: -sum_j p_t[j] log p_t[j] (0).
+ *   top_ids  int32[T][k], out: the columns of the k largest logits, largest
+ *            first, of equal ones the lowest column first; -1 past the V-th (-1).
+ *   top_logp float[T][k], out: log p_t there; -inf past the V-th (-inf).
+ *            k from 0 (both may be NULL) to 128 (LORA_ERR_LIMIT above).
+ *   stats    float[T][3], out, for the gradient: the largest logit m, the sum
+ *            of exp((x - m) / tau) over all but one of the largest, the mean of
+ *            (m - x) / tau under p (0, 0, 0).
+ * A row that holds a NaN or +inf, or nothing above -inf, has no probabilities:
+ * NaN in every output, ids -1.
+ *
+ * Workspace: 256-byte aligned; 0 for sizes beyond the limits.
+ */
+size_t lora_token_top_workspace_bytes(int64_t T, int64_t V, int64_t k);
+int lora_token_top(const lora_mat* logits, const int32_t* targets, int64_t k, double temperature, float* logp,
+                   float* entropy, int32_t* top_ids, float* top_logp, float* stats, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the logits of a loss on these log probabilities and entropies:
+ *   dlogits[t, j] = (g_t ([j = y_t] - p_j) - h_t p_j (log p_j + entropy_t)) / tau
+ *   with g = dlogp and h = dentropy (float[T]; NULL: zeros. dlogp needs
+ *   targets); targets and temperature of the lora_token_top on the same logits
+ *   that gave stats. Rules of dlogits as above; masked rows, and rows whose g
+ *   and h are both 0, are not read and become zeros.
+ */
+int lora_token_top_grad(const lora_mat* logits, const int32_t* targets, const float* stats, const float* dlogp,
+                        const float* dentropy, double temperature, const lora_mat* dlogits, void* stream);
+
+/*
+ * A teacher's top tokens, device arrays [T][k], k from 1 to 256 (LORA_ERR_LIMIT
+ * above). Ids outside [0, V) are no entries (their logp is not used); a row
+ * without any entry is masked: it is not read, its divergence is 0 and its
+ * gradient zeros. An id that occurs twice counts with both entries.
+ */
+typedef struct {
+  const int32_t* ids;
+  const float* logp;  /* log probabilities at the temperature; without rest also unnormalised */
+  int64_t k;
+  double temperature; /* of the logits, in [1e-6, 1e6] (LORA_ERR_VALUE) */
+  int32_t rest;       /* whether the tokens that no id names count as one more class */
+} lora_teacher;
+
+/*
+ * Divergence of p = softmax(x[t] / tau) from a teacher's top tokens:
+ *   rest 1: q_k = exp(logp_k), q_r = max(0, 1 - sum_k q_k) (0 if the ids name
+ *           the whole vocabulary), p_r the sum of p over the tokens that no id
+ *           names:
+ *           kl_t = sum_k q_k (log q_k - log p[id_k]) + q_r (log q_r - log p_r)
+ *   rest 0: q_k = exp(logp_k) / sum exp(logp), q_r = 0.
+ *   A term whose q is 0 is 0. kl is +inf where q is above 0 and p is 0.
+ *   kl     float[T], out.
+ *   state  float[T][k + 2], out or NULL: what lora_distill_grad takes.
+ * A row whose x holds a NaN or +inf, or nothing above -inf, gives NaN.
+ * Rules of logits as above.
+ *   workspace: lora_distill_workspace_bytes(T, V, k), 256-byte aligned; 0 for
+ *   sizes beyond the limits.
+ */
+size_t lora_distill_workspace_bytes(int64_t T, int64_t V, int64_t k);
+int lora_distill_kl(const lora_mat* logits, const lora_teacher* teacher, float* kl, float* state, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the logits of a loss with d loss / d kl = coef:
+ *   dlogits[t, j] = g coef_t d kl_t / d x[t, j], with g = scale, times *grad_out
+ *   (one float on the device) unless that is NULL; ids, k and temperature of
+ *   the lora_distill_kl on the same logits that gave state. A row whose factor
+ *   g coef_t is 0 is not read and becomes zeros. Rules of dlogits as above.
+ */
+int lora_distill_grad(const lora_mat* logits, const int32_t* top_ids, int64_t k, const float* state,
+                      const float* coef, const float* grad_out, float scale, double temperature,
+                      const lora_mat* dlogits, void* stream);
+
+/*
+ * Loss and gradient in one call:
+ *   loss = sum over t of weights_t kl_t (one float, out, summed in float64;
+ *   a weight of 0 drops its term, also where kl is infinite or NaN), kl as
+ *   above, dlogits the gradient of the loss times grad_scale. Also with T = 0
+ *   the loss is written.
+ */
+int lora_distill_step(const lora_mat* logits, const lora_teacher* teacher, const float* weights, float grad_scale,
+                      float* loss, float* kl, const lora_mat* dlogits, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 /*
  * AdamW over many tensors at once:

@@ -7,7 +7,8 @@ lora_addressing_build, lora_shrink, lora_expand_fused, lora_apply_linear,
 lora_apply_linear_noalloc, lora_gather_shrink, lora_workspace_bytes, and the kernel-timing calls
 lora_timing_begin/pause/resume/read/reserve. The operators of a training step around the adapter linears are in
 ``train``: lora_embed, lora_embed_grad, lora_token_logp, lora_pref_loss, lora_policy_loss, lora_logit_grad,
-lora_pref_step, lora_policy_step and the optimizer AdamW. Importing
+lora_pref_step, lora_policy_step, lora_token_top, lora_token_top_grad, lora_distill_kl, lora_distill_grad,
+lora_distill_step and the optimizer AdamW. Importing
 ``lora_rank_adapter_amd.torch_ops`` registers the same operations as torch
 custom ops (namespace ``lora_amd``) with fake implementations for tracing and
 torch.compile, and a differentiable ``lora_delta``.
@@ -43,4 +44,9 @@ from .train import (  # noqa: F401
     lora_logit_grad,
     lora_pref_step,
     lora_policy_step,
+    lora_token_top,
+    lora_token_top_grad,
+    lora_distill_kl,
+    lora_distill_grad,
+    lora_distill_step,
 )

@@ -50,6 +50,7 @@ class LoraMat(ctypes.Structure):
 # that take them declare c_void_p (byref of the Structure does as well).
 pack_mat = struct.Struct("=Qiiqqqq").pack        # LoraMat
 pack_policy = struct.Struct("=QQQQQfff4x").pack  # LoraPolicy
+pack_teacher = struct.Struct("=QQqdi4x").pack      # LoraTeacher
 pack_hyper = struct.Struct("=dddddQQ").pack      # LoraAdamwHyper
 
 
@@ -88,6 +89,16 @@ class LoraPolicy(ctypes.Structure):
         ("clip_low", ctypes.c_float),
         ("clip_high", ctypes.c_float),
         ("kl_coef", ctypes.c_float),
+    ]
+
+
+class LoraTeacher(ctypes.Structure):
+    _fields_ = [
+        ("ids", ctypes.c_void_p),
+        ("logp", ctypes.c_void_p),
+        ("k", ctypes.c_int64),
+        ("temperature", ctypes.c_double),
+        ("rest", ctypes.c_int32),
     ]
 
 
@@ -180,6 +191,21 @@ SIGNATURES = {
     "lora_policy_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                         ctypes.c_void_p]),
+    "lora_token_top_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "lora_token_top": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_double,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "lora_token_top_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_double, ctypes.c_void_p, ctypes.c_void_p]),
+    "lora_distill_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "lora_distill_kl": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "lora_distill_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_double,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "lora_distill_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_void_p]),
     "lora_adamw_table_bytes": (ctypes.c_size_t, [_P(LoraAdamwTensor), ctypes.c_int64]),
     "lora_adamw_state_elems": (ctypes.c_int64, [_P(LoraAdamwTensor), ctypes.c_int64]),
     "lora_adamw_table": (ctypes.c_int, [_P(LoraAdamwTensor), ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,

@@ -3,12 +3,22 @@
 // checks of logits and their gradients.
 #pragma once
 
+#include <cmath>
+
 #include "lora_host.hpp"
 #include "lora_rows.hpp"
 
 namespace lora {
 
 __device__ __forceinline__ float at_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// log2(e) / temperature as a float32 below it and the rest, which is above 0:
+// the exponent of 2 of exp(d / temperature) is d hi + d lo, -inf for d = -inf.
+struct Exponent {
+  float hi, lo;
+  __device__ __forceinline__ float of(float d) const { return fmaf(d, hi, d * lo); }
+};
+constexpr double kLn2 = 0.693147180559945309417;
 
 // Element `at` of a row's piece (-1: it is elsewhere), which the sums leave
 // out: -inf takes its place in the loaded vector that holds it.
@@ -80,6 +90,14 @@ inline int check_logits(const lora_mat* m) {
   if (!aligned(m->ptr, elem_size(m->dtype))) return LORA_ERR_STRIDE;
   if (m->rows > kMaxRows || m->cols > 0x7FFFFFFF - 8 * kGradVecs) return LORA_ERR_LIMIT;
   return LORA_OK;
+}
+
+inline bool temperature_ok(double t) { return t >= 1e-6 && t <= 1e6; }
+inline Exponent exponent_of(double temperature) {
+  const double scale = 1.4426950408889634074 / temperature;
+  float hi = static_cast<float>(scale);
+  if (static_cast<double>(hi) >= scale) hi = std::nextafterf(hi, 0.0f);
+  return {hi, static_cast<float>(scale - static_cast<double>(hi))};
 }
 
 // f with a null pointer of the logits' element type

@@ -1,5 +1,6 @@
 """Binding of the operators of a training step around the adapter linears:
-embedding lookup and gradient, the losses on next-token logits, AdamW.
+embedding lookup and gradient, the losses on next-token logits, their
+alternatives and entropy, distillation, AdamW.
 
 As in ``ops``: argument marshalling only. Vectors (ids, targets, log
 probabilities, ...) are checked here for dtype, length and layout, since the
@@ -12,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import LoraAdamwState, LoraAdamwTensor, check, pack_hyper, pack_mat, pack_policy
+from ._lib import LoraAdamwState, LoraAdamwTensor, check, pack_hyper, pack_mat, pack_policy, pack_teacher
 from .ops import _DT, _dtype_code, _stream
 
 _I32, _F32 = torch.int32, torch.float32
@@ -240,6 +241,127 @@ def lora_policy_step(logits: torch.Tensor, targets: torch.Tensor, old_logp: torc
         _matrix("logits", logits, dev), args, float(grad_scale), loss.data_ptr(), logp.data_ptr(),
         _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
     return loss, logp, dlogits
+
+
+# ---------------------------------------------------------------------------
+# alternatives and entropy
+# ---------------------------------------------------------------------------
+
+def lora_token_top(logits: torch.Tensor, targets: torch.Tensor | None = None, k: int = 0, temperature: float = 1.0,
+                   workspace: torch.Tensor | None = None):
+    """What softmax(logits / temperature) holds in each row: the log probabilities of the targets (None without
+    them), the entropy, and the k largest logits' ids and log probabilities (in order, ties to the lowest id; id -1
+    and -inf past the vocabulary). logits: T x V, targets: int32 [T]; a target outside [0, V) masks its row (0, 0,
+    -1 and -inf). Returns (logp [T], entropy [T], top_ids int32 [T x k], top_logp [T x k], stats [T x 3])."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev = logits.device
+    k = int(k)
+    y = None if targets is None else _vector("targets", targets, T, _I32, dev)
+    entropy = torch.empty(T, dtype=_F32, device=dev)
+    logp = None if targets is None else torch.empty(T, dtype=_F32, device=dev)
+    ids = torch.empty((T, max(k, 0)), dtype=_I32, device=dev)
+    top = torch.empty((T, max(k, 0)), dtype=_F32, device=dev)
+    stats = torch.empty((T, 3), dtype=_F32, device=dev)
+    ws, nbytes = _given(workspace, lib.lora_token_top_workspace_bytes(T, V, k), dev)
+    check("lora_token_top", lib.lora_token_top(
+        _matrix("logits", logits, dev), y, k, float(temperature), None if logp is None else logp.data_ptr(),
+        entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes, _queue(dev)))
+    return logp, entropy, ids, top, stats
+
+
+def lora_token_top_grad(logits: torch.Tensor, targets: torch.Tensor | None, stats: torch.Tensor,
+                        dlogp: torch.Tensor | None = None, dentropy: torch.Tensor | None = None,
+                        temperature: float = 1.0, dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the logits of a loss with d loss / d logp = dlogp and d loss / d entropy = dentropy (float32 [T]
+    or None; dlogp needs targets). stats from lora_token_top on the same logits, targets and temperature. Returns
+    dlogits [T x V] of the logits' dtype: the given tensor (it may be the logits), else a new one."""
+    lib = _lib.load()
+    T = logits.shape[0]
+    dev = logits.device
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    check("lora_token_top_grad", lib.lora_token_top_grad(
+        _matrix("logits", logits, dev), None if targets is None else _vector("targets", targets, T, _I32, dev),
+        _vector("stats", stats, 3 * T, _F32, dev), None if dlogp is None else _vector("dlogp", dlogp, T, _F32, dev),
+        None if dentropy is None else _vector("dentropy", dentropy, T, _F32, dev), float(temperature),
+        _matrix("dlogits", dlogits, dev), _queue(dev)))
+    return dlogits
+
+
+# ---------------------------------------------------------------------------
+# distillation
+# ---------------------------------------------------------------------------
+
+def _teacher(top_ids, top_logp, T, temperature, rest, dev) -> tuple[bytes, int]:
+    if top_ids.dim() != 2 or top_ids.shape != top_logp.shape:
+        raise ValueError(f"top_ids and top_logp must have one 2-D shape, got {tuple(top_ids.shape)} and "
+                         f"{tuple(top_logp.shape)}")
+    k = top_ids.shape[1]
+    return pack_teacher(_vector("top_ids", top_ids, T * k, _I32, dev), _vector("top_logp", top_logp, T * k, _F32, dev),
+                        k, temperature, int(bool(rest))), k
+
+
+def lora_distill_kl(logits: torch.Tensor, top_ids: torch.Tensor, top_logp: torch.Tensor, temperature: float = 1.0,
+                    rest: bool = True, workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Divergence of softmax(logits / temperature) from a teacher's top tokens in each row. top_ids int32 [T x k],
+    top_logp float32 [T x k]: the teacher's, as lora_token_top gives them at that temperature; ids outside [0, V)
+    are no entries, a row without any is masked. rest: the other tokens' probability counts as one more class,
+    otherwise the teacher's are normalised over its ids (top_logp may then be its logits over the temperature).
+    Returns (kl [T], state [T x (k + 2)] for lora_distill_grad)."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev = logits.device
+    teacher, k = _teacher(top_ids, top_logp, T, temperature, rest, dev)
+    kl = torch.empty(T, dtype=_F32, device=dev)
+    state = torch.empty((T, k + 2), dtype=_F32, device=dev)
+    ws, nbytes = _given(workspace, lib.lora_distill_workspace_bytes(T, V, k), dev)
+    check("lora_distill_kl", lib.lora_distill_kl(_matrix("logits", logits, dev), teacher, kl.data_ptr(),
+                                                 state.data_ptr(), ws.data_ptr(), nbytes, _queue(dev)))
+    return kl, state
+
+
+def lora_distill_grad(logits: torch.Tensor, top_ids: torch.Tensor, state: torch.Tensor, coef: torch.Tensor,
+                      temperature: float = 1.0, grad_out: torch.Tensor | None = None, scale: float = 1.0,
+                      dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits[t] = scale * grad_out * coef[t] * d kl[t] / d logits[t]. top_ids, state and temperature of the
+    lora_distill_kl on the same logits, coef: float32 [T], grad_out: float32 [] on the device or None. Returns
+    dlogits [T x V] of the logits' dtype: the given tensor (it may be the logits), else a new one."""
+    lib = _lib.load()
+    T = logits.shape[0]
+    dev = logits.device
+    if top_ids.dim() != 2:
+        raise ValueError(f"top_ids: expected a 2-D tensor, got shape {tuple(top_ids.shape)}")
+    k = top_ids.shape[1]
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    check("lora_distill_grad", lib.lora_distill_grad(
+        _matrix("logits", logits, dev), _vector("top_ids", top_ids, T * k, _I32, dev), k,
+        _vector("state", state, T * (k + 2), _F32, dev), _vector("coef", coef, T, _F32, dev),
+        None if grad_out is None else _vector("grad_out", grad_out, 1, _F32, dev), float(scale), float(temperature),
+        _matrix("dlogits", dlogits, dev), _queue(dev)))
+    return dlogits
+
+
+def lora_distill_step(logits: torch.Tensor, top_ids: torch.Tensor, top_logp: torch.Tensor, weights: torch.Tensor,
+                      temperature: float = 1.0, rest: bool = True, grad_scale: float = 1.0,
+                      dlogits: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """loss = sum of weights * kl and the gradient of its logits in one call (see lora_distill_kl). weights: float32
+    [T], a token's share of the loss, e.g. temperature^2 / number of tokens; a weight of zero drops its term. Returns
+    (loss [], kl [T], dlogits [T x V], times grad_scale)."""
+    lib = _lib.load()
+    T, V = logits.shape
+    dev = logits.device
+    teacher, k = _teacher(top_ids, top_logp, T, temperature, rest, dev)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    kl = torch.empty(T, dtype=_F32, device=dev)
+    loss = kl.new_empty(())
+    ws, nbytes = _given(workspace, lib.lora_distill_workspace_bytes(T, V, k), dev)
+    check("lora_distill_step", lib.lora_distill_step(
+        _matrix("logits", logits, dev), teacher, _vector("weights", weights, T, _F32, dev), float(grad_scale),
+        loss.data_ptr(), kl.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
+    return loss, kl, dlogits
 
 
 # ---------------------------------------------------------------------------

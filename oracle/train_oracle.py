@@ -130,3 +130,78 @@ def quantise(x, positive):
     if positive:
         code = np.where((q > 0) & (code == 0), E4M3_MIN, code)
     return code.reshape(-1), scale
+
+
+def token_top(logits, targets, k, tau):
+    """(logp, entropy, top_ids, top_logp, stats); targets None: no row is masked, logp None"""
+    x = _f64(logits)
+    T, V = x.shape
+    off = np.zeros(T, bool) if targets is None else masked(targets, V)
+    logp, entropy, stats = np.zeros(T), np.zeros(T), np.zeros((T, 3))
+    ids, top = np.full((T, k), -1, np.int64), np.full((T, k), -np.inf)
+    for t in np.flatnonzero(~off):
+        m = x[t].max() if V else -np.inf
+        if not np.isfinite(m):
+            logp[t] = entropy[t] = np.nan
+            stats[t], top[t] = np.nan, np.nan
+            continue
+        d = (x[t] - m) / tau
+        e = np.exp(d)
+        r = np.delete(e, x[t].argmax()).sum()
+        gap = (e * np.where(e > 0, -d, 0.0)).sum() / (1 + r)
+        stats[t], entropy[t] = (m, r, gap), np.log1p(r) + gap
+        if targets is not None:
+            logp[t] = d[targets[t]] - np.log1p(r)
+        order = np.argsort(-x[t], kind="stable")[:k]
+        ids[t, :len(order)] = order
+        top[t, :len(order)] = d[order] - np.log1p(r)
+    return None if targets is None else logp, entropy, ids, top, stats
+
+
+def token_top_grad(logits, targets, dlogp, dentropy, tau):
+    x = _f64(logits)
+    _, entropy, _, _, _ = token_top(x, targets, 0, tau)
+    p = softmax(x / tau)
+    with np.errstate(all="ignore"):
+        out = -_f64(dentropy)[:, None] * np.where(p > 0, p * (np.log(p) + entropy[:, None]), 0 * p)
+    out -= _f64(dlogp)[:, None] * p
+    if targets is not None:
+        y, off = np.asarray(targets), masked(targets, x.shape[1])
+        live = np.flatnonzero(~off)
+        out[live, y[live]] += _f64(dlogp)[live]
+        out[off] = 0.0
+    return out / tau
+
+
+def distill(logits, ids, logp, tau, rest):
+    """(kl, d kl / d logits by row)"""
+    x, ids, logp = _f64(logits), np.asarray(ids), _f64(logp)
+    T, V = x.shape
+    kl, dx = np.zeros(T), np.zeros((T, V))
+    for t in range(T):
+        on = (ids[t] >= 0) & (ids[t] < V)
+        if not on.any():
+            continue
+        i, lq = ids[t][on], logp[t][on]
+        z = x[t] / tau
+        with np.errstate(all="ignore"):
+            lse = z.max() + np.log(np.exp(z - z.max()).sum())
+            other = np.ones(V, bool)
+            other[i] = False
+            if not rest:
+                lq = lq - (lq.max() + np.log(np.exp(lq - lq.max()).sum()))
+            q, lp = np.exp(lq), z[i] - lse
+            kl[t] = np.where(q > 0, q * (lq - lp), 0.0 * lp).sum()
+            total = q.sum()
+            dx[t] = 0.0
+            if rest and other.any():
+                q_r = max(0.0, 1.0 - total)
+                top = z[other].max()
+                l_r = top + np.log(np.exp(z[other] - top).sum())
+                if q_r > 0:
+                    kl[t] += q_r * (np.log(q_r) - (l_r - lse))
+                    dx[t, other] -= q_r * np.exp(z[other] - l_r)
+                total += q_r
+            dx[t] += total * np.exp(z - lse)
+            np.subtract.at(dx[t], i, q)
+    return kl, dx / tau

@@ -1,0 +1,353 @@
+"""Entropy, top alternatives and their gradient against the float64 definitions.
+
+Error bounds (H = 2^-24, half a step of float32; u = (m - x) / tau for a row's
+largest logit m). A kernel may take its exponents relative to another logit of
+the row than m: the largest of a run of at least 4096 columns (of the whole
+row where that is shorter), which lies reach (in natural units) below m at
+most, and never more than 64 binary orders. An exponential: the difference from the reference, its product with
+log2(e) / tau and that constant are rounded, which moves the exponent by at
+most 3 H (u + reach), and the exponential itself by at most 2^-23. Sums in
+float32 are trees of up to 2^10 terms, 16 H with the rounding of what is
+carried between them:
+    e_j = 3 H (u_j + reach) + 2^-23 + 16 H          (relative, of one term)
+    err(r) <= sum over the others of e^-u_j e_j + H r
+    err(log1p(r)) <= err(r) / (1 + r)
+    err(gap) <= sum p_j (u_j e_j + 3 H (u_j + reach)) + gap err(r) / (1 + r) + H gap
+    err(logp) <= err(log1p(r)) + 2 H |logp|
+    err(entropy) <= err(log1p(r)) + err(gap) + H entropy
+The gradient takes r and gap in float32 (3 H more for the factor made of them):
+    tau err(dx_j) <= p_j f_j (|g| + |h| |gap - u_j|) + |h| p_j (err(gap) + 6 H (gap + u_j))
+                     + [j = y] |g| (6 H (1 - p) + p (err(log1p(r)) + 3 H u_y + 4 H |logp|))
+    with f_j = 3 H u_j + 2^-23 + 8 H + err(r) / (1 + r)
+and half a step of the output's type, and 1e-37 for flushed denormals."""
+import numpy as np
+import pytest
+import torch
+
+import lora_rank_adapter_amd as L
+from oracle import train_oracle as O
+from tests.gpu_util import DEV, note
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+H = 2.0 ** -24
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def make(T, V, dtype, seed=0, pad=0, shift=0, std=2.0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    buf = torch.randn(T * (V + pad) + shift + 1, device=DEV, generator=g).mul_(std).to(dtype)
+    x = buf[shift:shift + T * (V + pad)].view(T, V + pad)[:, :V]
+    y = torch.randint(0, V, (T,), device=DEV, dtype=torch.int32, generator=g)
+    x[torch.arange(T, device=DEV), y.long()] += 4.0
+    y[::5] = torch.tensor([-100, V, -1, 2 ** 31 - 1], device=DEV, dtype=torch.int32).repeat(T)[:len(y[::5])]
+    if T == 1:
+        y[0] = V // 2
+    return x, y
+
+
+def reach(x64, tau):
+    """How far below a row's largest logit the largest of a run of 4096 columns can be: each holds a whole block of
+    2048 that begins at a multiple of it."""
+    T, V = x64.shape
+    if V <= 4096:
+        return np.zeros(T)
+    blocks = x64[:, :V // 2048 * 2048].reshape(T, -1, 2048).max(2)
+    return np.minimum((x64.max(1) - blocks.min(1)) / tau, 64 * np.log(2))
+
+
+def errors(x64, tau):
+    """(u, p, err(log1p(r)), err(gap)) by row"""
+    u = (x64.max(1, keepdims=True) - x64) / tau
+    w = np.exp(-u)
+    u = np.where(np.isfinite(u), u, 0.0)
+    total = w.sum(1)
+    p = w / total[:, None]
+    e = 3 * H * (u + reach(x64, tau)[:, None]) + 2.0 ** -23 + 16 * H
+    others = w.copy()
+    others[np.arange(len(u)), x64.argmax(1)] = 0.0
+    err_r = ((others * e).sum(1) + H * others.sum(1)) / total
+    gap = (p * u).sum(1)
+    err_gap = (p * (u * e + 3 * H * (u + reach(x64, tau)[:, None]) * (u > 0))).sum(1) + gap * err_r + H * gap
+    return u, p, err_r, err_gap
+
+
+def close(got, want, tol, what=""):
+    got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
+    tol = np.broadcast_to(tol, want.shape)
+    fine = np.isfinite(want)
+    assert np.array_equal(got[~fine], want[~fine], equal_nan=True), what
+    err = np.abs(got[fine] - want[fine])
+    assert (err <= tol[fine]).all(), (what, float((err / np.maximum(tol[fine], 1e-300)).max()))
+
+
+def check(x, y, k, tau, out):
+    x64, yn = f64(x), None if y is None else y.cpu().numpy()
+    logp, entropy, ids, top, stats = O.token_top(x64, yn, k, tau)
+    _, _, e_r, e_gap = errors(x64, tau)
+    live = np.ones(len(x64), bool) if yn is None else ~O.masked(yn, x64.shape[1])
+    assert (out[0] is None) == (y is None)
+    if y is not None:
+        close(f64(out[0]), logp, live * (e_r + 2 * H * np.abs(logp)), "logp")
+    close(f64(out[1]), entropy, live * (e_r + e_gap + H * entropy), "entropy")
+    assert np.array_equal(out[2].cpu().numpy(), ids), "ids"
+    with np.errstate(all="ignore"):
+        close(f64(out[3]), top, e_r[:, None] + 2 * H * np.abs(top), "top")
+    close(f64(out[4])[:, 0], stats[:, 0], 0, "m")
+    close(f64(out[4])[:, 1], stats[:, 1], live * (e_r * (1 + stats[:, 1]) + H * stats[:, 1]), "r")
+    close(f64(out[4])[:, 2], stats[:, 2], live * e_gap, "gap")
+
+
+def grad_bounds(x64, y, g, h, tau):
+    u, p, e_r, e_gap = errors(x64, tau)
+    gap = (p * u).sum(1, keepdims=True)
+    g, h = np.abs(g)[:, None], np.abs(h)[:, None]
+    f = 3 * H * u + 2.0 ** -23 + 8 * H + e_r[:, None]
+    tol = p * f * (g + h * np.abs(gap - u)) + h * p * (e_gap[:, None] + 6 * H * (gap + u))
+    if y is not None:
+        live = np.flatnonzero(~O.masked(y, x64.shape[1]))
+        at = (live, y[live])
+        lp = np.log(p[at])
+        tol[at] += g[live, 0] * (6 * H * (1 - p[at]) + p[at] * (e_r[live] + 3 * H * u[at] + 4 * H * np.abs(lp)))
+    return tol / tau
+
+
+def check_grad(dx, x64, y, g, h, tau, dtype, what=""):
+    want = O.token_top_grad(x64, y, g, h, tau)
+    tol = grad_bounds(x64, y, g, h, tau)
+    if y is not None:
+        tol[O.masked(y, x64.shape[1])] = 0.0
+    tol = np.where(tol > 0, tol + 1e-37, 0.0)
+    close(f64(dx), want, tol + torch.finfo(dtype).eps / 2 * (np.abs(want) + tol), what)
+
+
+SHAPES = [(1, 1, 0, 0, 3), (1, 2, 0, 0, 1), (5, 7, 0, 1, 7), (3, 64, 0, 0, 64), (9, 1023, 1, 1, 20),
+          (40, 1024, 0, 0, 5), (2, 32003, 0, 0, 128), (6, 40000, 5, 3, 64), (1, 128256, 0, 0, 20),
+          (2100, 515, 0, 0, 8), (70, 8209, 0, 0, 33), (300, 20011, 0, 1, 16), (7, 131, 0, 0, 128), (12, 70001, 0, 0, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T,V,pad,shift,k", SHAPES)
+def test_alternatives_and_gradient(dtype, T, V, pad, shift, k):
+    note(f"top {dtype} {T} {V} {pad} {shift} {k}")
+    tau = (1.0, 0.7, 2.0)[V % 3]
+    x, y = make(T, V, dtype, T + V, pad, shift)
+    before = x.clone()
+    out = L.lora_token_top(x, y, k, tau)
+    assert out[2].shape == out[3].shape == (T, k)
+    check(x, y, k, tau, out)
+    every = L.lora_token_top(x, None, k, tau)
+    check(x, None, k, tau, every)
+    again = L.lora_token_top(x, y, k, tau)
+    assert all(torch.equal(a, b) for a, b in zip(out, again)) and torch.equal(x, before)
+
+    x64, yn = f64(x), y.cpu().numpy()
+    off = O.masked(yn, V)
+    g, h = torch.randn(T, device=DEV), torch.randn(T, device=DEV)
+    g[off] = float("nan")  # a masked token's are not used
+    h[off] = float("nan")
+    g64, h64 = np.where(off, 0, f64(g)), np.where(off, 0, f64(h))
+    buf = torch.full((T * (V + pad) + shift + 1,), 9.0, device=DEV, dtype=dtype)
+    dx = buf[shift:shift + T * (V + pad)].view(T, V + pad)[:, :V]
+    assert L.lora_token_top_grad(x, y, out[4], g, h, tau, dlogits=dx) is dx
+    check_grad(dx, x64, yn, g64, h64, tau, dtype, "both")
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    rest[shift:shift + T * (V + pad)].view(T, V + pad)[:, :V] = False
+    assert bool((buf[rest] == 9.0).all())
+    check_grad(L.lora_token_top_grad(x, y, out[4], dlogp=g, temperature=tau), x64, yn, g64, 0 * g64, tau, dtype, "logp")
+    check_grad(L.lora_token_top_grad(x, None, every[4], dentropy=torch.nan_to_num(h), temperature=tau), x64, None,
+               0 * g64, np.nan_to_num(f64(h)), tau, dtype, "entropy")
+    assert not L.lora_token_top_grad(x, None, every[4], temperature=tau).any()
+    L.lora_token_top_grad(x, y, out[4], g, h, tau, dlogits=x)
+    assert torch.equal(x, dx)
+
+
+def ranked(x, k):
+    """ids of the k largest of each row, ties to the lowest"""
+    return torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :k].int()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("V", [50, 9001, 128256])
+@pytest.mark.parametrize("k", [1, 20, 128])
+def test_orders_that_a_guess_would_miss(dtype, V, k):
+    """Rows whose largest logits lie anywhere: ascending, descending, all equal, few values, the largest at the end,
+    zeros of both signs, huge steps, and vocabularies of which little is left."""
+    note(f"orders {dtype} {V} {k}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V + k)
+    n = torch.arange(V, device=DEV, dtype=torch.float32)
+    rows = [n / V * 10, -n / V * 10, torch.zeros(V, device=DEV), (n % 3), n.clone().fill_(-5.0), torch.sin(n) * 0.0,
+            n / V * 200 - 100, torch.randn(V, device=DEV, generator=g) * 1e-3, torch.randn(V, device=DEV, generator=g)]
+    rows[4][V - 1:] = 7.0
+    rows[4][V // 2:V // 2 + 3] = 6.0
+    for keep in (1, 7, 60):  # masked down to a few columns, by -inf and by the lowest value
+        for low in (-float("inf"), torch.finfo(dtype).min):
+            r = torch.full((V,), low, device=DEV)
+            at = torch.randperm(V, device=DEV, generator=g)[:keep]
+            r[at] = torch.randn(len(at), device=DEV, generator=g)
+            rows.append(r)
+    r = torch.full((V,), -float("inf"), device=DEV)  # nothing for a long while, then everything
+    r[V * 3 // 4:] = torch.randn(V - V * 3 // 4, device=DEV, generator=g) * 3
+    rows.append(r)
+    rows.append(torch.full((V,), torch.finfo(dtype).min, device=DEV))  # uniform
+    rows.append(torch.where(n % 2 == 0, 1e38, -1e38))
+    x = torch.stack(rows).to(dtype)
+    out = L.lora_token_top(x, None, k, 1.0)
+    kk = min(k, V)
+    assert torch.equal(out[2][:, :kk], ranked(x, kk))
+    assert (out[2][:, kk:] == -1).all() and torch.isneginf(out[3][:, kk:]).all()
+    x64 = f64(x)
+    with np.errstate(all="ignore"):
+        d = x64 - x64.max(1, keepdims=True)
+        e = np.exp(d)
+        lse = np.log(e.sum(1))
+        p = e / e.sum(1, keepdims=True)
+        gap = np.where(p > 0, -p * d, 0).sum(1)
+        # exponents relative to a logit up to 64 binary orders below the largest
+        far = np.minimum(64 * np.log(2), np.where(np.isfinite(d), -d, 0).max(1))
+        step = 3 * H * (np.where(p > 0, -d, 0) + far[:, None]) + 2.0 ** -23 + 16 * H
+        tol = (p * step).sum(1) + H
+        close(f64(out[3])[:, :kk], np.take_along_axis(d, f64(out[2])[:, :kk].astype(int), 1) - lse[:, None],
+              tol[:, None] + 2 * H * np.abs(np.take_along_axis(d, f64(out[2])[:, :kk].astype(int), 1) - lse[:, None]),
+              "top")
+        tol_gap = np.where(p > 0, p * (-d * step + 3 * H * (far[:, None] - d)), 0).sum(1) + gap * tol + H * gap
+        close(f64(out[1]), lse + gap, tol + tol_gap + H * (lse + gap), "entropy")
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("V", [40, 9001, 40000])
+def test_rows_without_probabilities(dtype, V):
+    note(f"undefined {dtype} {V}")
+    x, _ = make(6, V, dtype, 3)
+    x[0] = -float("inf")
+    x[1, V // 3] = float("inf")
+    x[2, V - 1] = float("nan")
+    x[3] = float("nan")
+    x[4] = float("nan")              # masked by its target: not read
+    y = torch.tensor([2, 2, 2, 2, V, 3], dtype=torch.int32, device=DEV)
+    logp, entropy, ids, top, stats = L.lora_token_top(x, y, 9, 1.5)
+    for t in (logp, entropy, top, stats):
+        assert torch.isnan(t[:4]).all() and not torch.isnan(t[4:]).any()
+    assert (ids[:5] == -1).all() and (ids[5] >= 0).all()
+    assert logp[4] == entropy[4] == 0 and torch.isneginf(top[4]).all() and not stats[4].any()
+    g = torch.ones(6, device=DEV)
+    dx = L.lora_token_top_grad(x, y, stats, g, g, 1.5)
+    assert torch.isnan(dx[:4]).all() and not dx[4].any() and torch.isfinite(dx[5]).all()
+    # a masked vocabulary: no probability, no gradient
+    x[5, V // 2:] = -float("inf")
+    y[5] = 3
+    logp, entropy, ids, top, stats = L.lora_token_top(x, y, 9, 1.5)
+    check(x[5:], y[5:], 9, 1.5, (logp[5:], entropy[5:], ids[5:], top[5:], stats[5:]))
+    dx = L.lora_token_top_grad(x, y, stats, g, g, 1.5)
+    assert not dx[5, V // 2:].any()
+    y[5] = V - 1                     # a target without probability
+    logp, _, _, _, stats = L.lora_token_top(x, y, 0, 1.5)
+    assert torch.isneginf(logp[5])
+    dx = L.lora_token_top_grad(x, y, stats, g, 0 * g, 1.5)
+    assert abs(float(dx[5, V - 1]) - 1 / 1.5) <= torch.finfo(dtype).eps
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("V", [33, 5000, 128256])
+@pytest.mark.parametrize("lead", [12.0, 25.0, 60.0])
+def test_likely_tokens_keep_what_little_is_left(dtype, V, lead):
+    """One token far ahead, at the row's beginning, middle or end: entropy and 1 - p are small and relatively exact."""
+    note(f"likely {dtype} {V} {lead}")
+    x, y = make(6, V, dtype, V, std=1.0)
+    y[:] = torch.tensor([0, V // 2, V - 1, 0, V // 2, V - 1], device=DEV)
+    x[torch.arange(6, device=DEV), y.long()] = lead
+    out = L.lora_token_top(x, y, 2, 1.0)
+    check(x, y, 2, 1.0, out)
+    g, h = torch.ones(6, device=DEV), torch.full((6,), -0.5, device=DEV)
+    dx = L.lora_token_top_grad(x, y, out[4], g, h, 1.0)
+    check_grad(dx, f64(x), y.cpu().numpy(), f64(g), f64(h), 1.0, dtype)
+
+
+def test_gradient_against_differences():
+    note("top gradient by differences")
+    T, V, tau, eps = 8, 400, 0.8, 2.0 ** -6
+    x, y = make(T, V, F, 11)
+    y[0], y[5] = 3, 7
+    g, h = torch.randn(T, device=DEV), torch.randn(T, device=DEV)
+    dx = f64(L.lora_token_top_grad(x, y, L.lora_token_top(x, y, 0, tau)[4], g, h, tau))
+    u = torch.randn(T, V, device=DEV)
+    up, down = ((x + s * eps * u) for s in (1, -1))
+    diff = np.zeros(T)
+    for v, s in ((up, 1), (down, -1)):
+        logp, entropy, *_ = L.lora_token_top(v, y, 0, tau)
+        diff += s * (f64(g) * f64(logp) + f64(h) * f64(entropy)) / (2 * eps)
+    # of the third order eps^2 |u / tau|^3 (|g| + 30 |h|) / 6 at most, |u| below 5; of the values 2^-20 / eps
+    tol = (np.abs(f64(g)) + 30 * np.abs(f64(h))) * (eps ** 2 * (5 / tau) ** 3 / 6 + 2.0 ** -20 / eps * 4)
+    assert (np.abs((dx * f64(u)).sum(1) - diff) <= tol).all()
+
+
+def test_rows_beyond_32_bit_offsets():
+    note("alternatives beyond 2^31 elements")
+    T, V = 40_000, 65_000  # 2.6e9 elements
+    x = torch.zeros(T, V, dtype=BF, device=DEV)
+    y = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    rows = [0, 36_000, T - 1]
+    for r in rows:
+        x[r].normal_()
+        x[r, V - 1] = 9.0
+        y[r] = V - 1
+    out = L.lora_token_top(x, y, 4, 1.0)
+    at = torch.tensor(rows, device=DEV)
+    check(x[at], y[at], 4, 1.0, tuple(t[at] for t in out))
+    assert (out[2][1] == -1).all()
+    g, h = torch.ones(T, device=DEV), torch.ones(T, device=DEV)
+    dx = L.lora_token_top_grad(x, y, out[4], g, h, 1.0, dlogits=x.clone())
+    check_grad(dx[at], f64(x[at]), y[at].cpu().numpy(), np.ones(3), np.ones(3), 1.0, BF)
+    assert not dx[1].any()
+
+
+def test_replayed_graph_and_other_stream():
+    note("alternatives in a graph")
+    T, V, k = 33, 20011, 12
+    x, y = make(T, V, BF, 5)
+    x[3] = torch.arange(V, device=DEV) / V
+    g, h = torch.randn(T, device=DEV), torch.randn(T, device=DEV)
+    lib = L.load_library()
+    ws = torch.empty(lib.lora_token_top_workspace_bytes(T, V, k), dtype=torch.uint8, device=DEV)
+
+    def step():
+        out = L.lora_token_top(x, y, k, 0.9, workspace=ws)
+        return *out, L.lora_token_top_grad(x, y, out[4], g, h, 0.9)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in range(4):
+        x.copy_(make(T, V, BF, 20 + seed)[0])
+        x[4] = torch.arange(V, device=DEV).float() / V
+        graph.replay()
+        torch.cuda.synchronize()
+        ws.fill_(255)
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), seed
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+
+
+def test_empty_inputs():
+    note("alternatives of nothing")
+    x = torch.empty(0, 50, device=DEV)
+    out = L.lora_token_top(x, torch.empty(0, dtype=torch.int32, device=DEV), 3)
+    assert [t.shape for t in out] == [(0,), (0,), (0, 3), (0, 3), (0, 3)]
+    x = torch.empty(4, 0, device=DEV)
+    logp, entropy, ids, top, stats = L.lora_token_top(x, torch.zeros(4, dtype=torch.int32, device=DEV), 3)
+    assert not logp.any() and not entropy.any() and (ids == -1).all() and torch.isneginf(top).all()
+    logp, entropy, ids, top, stats = L.lora_token_top(x, None, 3)
+    assert logp is None and torch.isnan(entropy).all() and (ids == -1).all() and torch.isnan(top).all()
+    assert L.lora_token_top_grad(x, None, stats).shape == (4, 0)

@@ -10,7 +10,8 @@
 // the log probabilities and their gradients; every term of gap is positive.
 //
 // Kernels:
-//   top_kernel       a workgroup to a row: the statistics, the k largest logits
+//   top_kernel       one pass over a row (or one piece of it): the statistics, the k largest logits
+//   top_join_kernel  the pieces of a row joined
 //   top_grad_kernel  the gradient's rows from the statistics
 
 #include <type_traits>
@@ -36,10 +37,12 @@ __device__ __forceinline__ uint64_t entry_of(float x, int column) {
 }
 __device__ __forceinline__ int column_of(uint64_t entry) { return static_cast<int>(0xFFFFFFFFu - (uint32_t)entry); }
 
-// A row's statistics; undefined (a NaN, +inf, or nothing above -inf): NaN.
+// A row's statistics, or those of a piece of it. A row with a NaN, with +inf or
+// with nothing above -inf has no probabilities; r is NaN with a NaN, and 0 in a
+// piece with nothing above -inf.
 struct TopStats {
   float m;
-  double r, gap;
+  double r, gap;  // gap: in a piece times 1 + r
   __device__ __forceinline__ bool defined() const { return m > -INFINITY && m < INFINITY && r == r; }
 };
 
@@ -51,7 +54,7 @@ struct TopOut {
   double inv_temperature;
 };
 
-// What a row gives, by all threads of a workgroup; entries: the k largest in
+// What a row gives, by all threads of a workgroup; entries: its k largest in
 // order, `count` of them.
 __device__ __forceinline__ void put_row(const TopOut& o, int64_t row, const TopStats& v, bool target, float x,
                                         const uint64_t* entries, int count) {
@@ -87,162 +90,482 @@ __device__ __forceinline__ void put_masked(const TopOut& o, int64_t row) {
   }
 }
 
-// f(value, column) for each of the thread's elements of a row.
-template <class E, int THREADS, class F>
-__device__ __forceinline__ void each_element(const E* p, int V, F f) {
-  constexpr int N = Vec<E>::N;
-  const int vecs = V / N;
-  for (int i = threadIdx.x; i < vecs; i += THREADS) {
-    float v[N];
-    Vec<E>::unpack(vload(p + (int64_t)i * N), v);
-#pragma unroll
-    for (int e = 0; e < N; ++e) f(v[e], i * N + e);
-  }
-  const int rest = vecs * N + threadIdx.x;
-  if (rest < V) f(Vec<E>::value(p[rest]), rest);
-}
+// ---------------------------------------------------------------------------
+// selection of the k largest of a set of entries by a workgroup
+// ---------------------------------------------------------------------------
 
-struct Kth {
-  uint32_t order;  // of the k-th largest element
-  int equal;       // how many of the elements equal to it are among the k
+constexpr int kList = 512;         // entries that are put in order at most
+constexpr float kFloor = -1e30f;   // logits below (-inf, a mask's lowest values) share one bin
+
+struct Select {
+  int hist[256];
+  int count;                 // entries in the list
+  uint32_t low;
+  int first;                 // where the largest entry came from
+  uint64_t list[kList], sorted[kMaxTop];
+  int from[kList];
 };
 
-// The k-th largest of the elements that each(f) gives f(order) of, by one
-// digit of 8 bits after the other; k is at most their number.
-template <int THREADS, class Each>
-__device__ __forceinline__ Kth kth_largest(Each each, int k, int* hist, int* found) {
-  Kth v{0u, k};
-  uint32_t mask = 0u;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += THREADS) hist[i] = 0;
-    __syncthreads();
-    each([&](uint32_t order) {
-      if ((order & mask) == v.order) atomicAdd(&hist[order >> shift & 255u], 1);
-    });
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      // lane l has the digits 255 - 4 l and the three below
-      int c[4], sum = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum += c[j] = hist[255 - 4 * threadIdx.x - j];
-      int upto = sum;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int other = __shfl_up(upto, d, 64);
-        if ((int)threadIdx.x >= d) upto += other;
-      }
-      int above = upto - sum;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (above < v.equal && v.equal <= above + c[j]) {
-          found[0] = 255 - 4 * threadIdx.x - j;
-          found[1] = v.equal - above;
-        }
-        above += c[j];
-      }
-    }
-    __syncthreads();
-    v.order |= static_cast<uint32_t>(found[0]) << shift;
-    v.equal = found[1];
-    mask |= 255u << shift;
+// 255 bins of equal width from hi down to lo and below, and the one of kFloor.
+struct Bins {
+  float hi, scale;
+  __device__ __forceinline__ Bins(float hi, float lo) : hi(hi), scale(lo < hi ? 254.0f / (hi - lo) : 0.0f) {}
+  __device__ __forceinline__ int of(float f) const {
+    return f >= kFloor ? (int)fmaxf(fminf((hi - f) * scale, 254.0f), 0.0f) : 255;
   }
-  return v;
+};
+
+// The bin of the k-th entry, from bin 0 on; 255 if there are fewer. Every wave
+// finds it for itself.
+__device__ __forceinline__ int kth_bin(const int* hist, int k) {
+  const int lane = threadIdx.x & 63;
+  int c[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sum += c[j] = hist[4 * lane + j];
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int other = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += other;
+  }
+  const uint64_t reached = __ballot(upto >= k);
+  if (reached == 0) return 255;
+  int before = upto - sum, bin = 4 * lane;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    before += c[j];
+    if (before < k) ++bin;
+  }
+  return __shfl(bin, __builtin_ctzll(reached), 64);
 }
 
+template <int THREADS>
+__device__ __forceinline__ void clear(Select& l) {
+  for (int i = threadIdx.x; i < 256; i += THREADS) l.hist[i] = 0;
+  if (threadIdx.x == 0) l.count = 0;
+}
+
+// Puts l.list in order, the first k of it into l.sorted.
+template <int THREADS>
+__device__ __forceinline__ void sort_list(Select& l, int n, int k) {
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const uint64_t e = l.list[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += l.list[j] > e;
+    if (rank < k) l.sorted[rank] = e;
+    if (rank == 0) l.first = l.from[i];
+  }
+  __syncthreads();
+}
+
+// The k largest of the entries that each(f) gives f(value, column, from) of,
+// in order; hi is the largest value, lo one that k entries reach. False if too
+// many share the k-th's bin. Starts from a cleared l, with a barrier behind it.
+template <int THREADS, class Each>
+__device__ __forceinline__ bool select_top(Each each, float hi, float lo, int k, Select& l) {
+  const Bins bins(hi, lo);
+  each([&](float f, int, int) { atomicAdd(&l.hist[bins.of(f)], 1); });
+  __syncthreads();
+  const int last = kth_bin(l.hist, k);
+  each([&](float f, int column, int from) {
+    if (bins.of(f) > last) return;
+    const int at = atomicAdd(&l.count, 1);
+    if (at >= kList) return;
+    l.list[at] = entry_of(f, column);
+    l.from[at] = from;
+  });
+  __syncthreads();
+  if (l.count > kList) return false;
+  sort_list<THREADS>(l, l.count, k);
+  return true;
+}
+
+// The same for any entries, in eight passes over them: the k-th entry by one
+// digit of 8 bits after the other, then all from it on. k is at most their number.
+template <int THREADS, class Each>
+__device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
+  uint64_t kth = 0, mask = 0;
+  int want = k;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    __syncthreads();
+    clear<THREADS>(l);
+    __syncthreads();
+    each([&](float f, int column, int) {
+      const uint64_t e = entry_of(f, column);
+      if ((e & mask) == kth) atomicAdd(&l.hist[255 - (int)(e >> shift & 255)], 1);
+    });
+    __syncthreads();
+    const int bin = kth_bin(l.hist, want);
+    for (int i = 0; i < bin; ++i) want -= l.hist[i];
+    kth |= static_cast<uint64_t>(255 - bin) << shift;
+    mask |= static_cast<uint64_t>(255) << shift;
+  }
+  each([&](float f, int column, int) {
+    const uint64_t e = entry_of(f, column);
+    if (e < kth) return;
+    const int at = atomicAdd(&l.count, 1);
+    if (at >= kList) return;
+    l.list[at] = e;
+    l.from[at] = -1;
+  });
+  __syncthreads();
+  sort_list<THREADS>(l, l.count < kList ? l.count : kList, k);
+}
+
+// ---------------------------------------------------------------------------
+// statistics and alternatives: a workgroup reads its row, or its piece of one,
+// once. Its first 32 elements per lane are held while the largest of each lane
+// are compared: the k-th of these is reached by k elements at least, so only
+// vectors that reach it can matter. They go to a list in LDS, together with
+// those of the rest of the row, a few hundred in all, and the k largest are
+// found among them. The sums are relative to the largest logit of these first
+// elements, which a row's largest one exceeds by little: no running maximum.
+//
+// Where that does not hold the row is read again: for the sums if a logit is 64
+// binary orders above the reference, for the alternatives if the list
+// overflows (logits that rise along the row, ties without end) or holds fewer
+// than k (a vocabulary masked down to a few tokens).
+// ---------------------------------------------------------------------------
+
+constexpr int kHits = 1024;             // vectors in the list of a workgroup
+constexpr float kAbove = 64.0f;         // binary orders that a logit may be above the reference
+constexpr int kMaxPiece = 131072;       // elements of a row that one workgroup takes
+constexpr int kMaxSplits = 64;
+
+// Sums of a vector's exponentials e = 2^a and of e a.
+struct VecSums {
+  float s, w;
+};
+
+template <int N>
+__device__ __forceinline__ float tree(const float* f) {
+  if constexpr (N == 1)
+    return f[0];
+  else
+    return tree<N / 2>(f) + tree<N / 2>(f + N / 2);
+}
+
+template <int N>
+__device__ __forceinline__ VecSums vec_sums(const float* f, float z, Exponent s) {
+  float e[N], w = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float a = s.of(f[i] - z);
+    e[i] = __builtin_amdgcn_exp2f(a);
+    w = fmaf(e[i], fmaxf(a, -256.0f), w);  // e is 0 there, and 0 times -inf is not
+  }
+  return {tree<N>(e), w};
+}
+
+// Vector i of n elements; -inf past the last.
 template <class E>
-__global__ __launch_bounds__(256) void top_kernel(const E* __restrict__ x, int64_t stride,
-                                                  const int32_t* __restrict__ targets, int V, Exponent s, TopOut out) {
-  constexpr int N = Vec<E>::N, THREADS = 256;
-  __shared__ float wave_m[4];
-  __shared__ int wave_at[4];
-  __shared__ double lds[4];
-  __shared__ int hist[256], found[2], count, wave_ties[4];
-  __shared__ uint64_t list[kMaxTop], sorted[kMaxTop];
+__device__ __forceinline__ typename Vec<E>::type vec_at(const E* p, int i, int n) {
+  constexpr int N = Vec<E>::N;
+  constexpr uint32_t low = N == 8 ? 0xFF80FF80u : 0xFF800000u;
+  typename Vec<E>::type w = {low, low, low, low};
+  if ((i + 1) * N <= n) return vload_nt(p + (int64_t)i * N);
+#pragma unroll
+  for (int e = 0; e < N - 1; ++e) {
+    if (i * N + e >= n) continue;
+    if constexpr (N == 8)
+      w[e / 2] = e & 1 ? (w[e / 2] & 0xFFFFu) | (uint32_t)p[i * N + e] << 16 : (w[e / 2] & 0xFFFF0000u) | p[i * N + e];
+    else
+      w[e] = __float_as_uint(p[i * N + e]);
+  }
+  return w;
+}
+
+template <int N>
+__device__ __forceinline__ float vec_max(const float* f) {
+  float m = f[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, f[i]);
+  return m;
+}
+
+struct TopPiece {
+  double r, gap;
+  float m;
+};
+
+// Where a piece of a row goes (splits > 1).
+struct TopParts {
+  TopPiece* stats;    // [T][splits]
+  uint64_t* entries;  // [T][splits][k], 0 past the piece's elements
+};
+
+template <class E, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4) void top_kernel(const E* __restrict__ x, int64_t stride,
+                                                            const int32_t* __restrict__ targets, int V, int splits,
+                                                            int piece, Exponent s, TopOut out, TopParts parts) {
+  constexpr int N = Vec<E>::N, U = 32 / N, THREADS = 64 * WAVES;
+  using V4 = typename Vec<E>::type;
+  __shared__ Select l;
+  __shared__ uint4 hit[kHits];
+  __shared__ int hit_at[kHits];
+  __shared__ int hits;
+  __shared__ float wave_hi[WAVES], wave_lo[WAVES];
+  __shared__ double wave_s[WAVES], wave_w[WAVES];
+  __shared__ TopStats shared;
+  const int64_t row = blockIdx.x / (unsigned)splits;
+  const int sp = (int)(blockIdx.x % (unsigned)splits);
+  const int tid = threadIdx.x;
+  const int y = targets != nullptr ? targets[row] : -1;
+  const bool target = y >= 0 && y < V;
+  if (targets != nullptr && !target) {
+    if (splits == 1) put_masked(out, row);
+    return;
+  }
+  const int lo = sp * piece;
+  const int n = V - lo < piece ? V - lo : piece;
+  const E* p = x + row * stride + lo;
+  const int vecs = (n + N - 1) / N, whole = n / N;
+  const int k = out.k < 1 ? 1 : out.k;  // the largest one is needed in any case
+  const int kk = k < n ? k : n;
+
+  V4 w[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) w[u] = vec_at(p, tid + u * THREADS < vecs ? tid + u * THREADS : vecs, n);
+  if (tid == 0) {
+    hits = 0;
+    l.low = 0xFFFFFFFFu;
+    l.first = -1;  // of a row without elements
+    l.sorted[0] = 0;
+  }
+  clear<THREADS>(l);
+  float mine = -INFINITY;  // the lane's largest
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float f[N];
+    Vec<E>::unpack(w[u], f);
+    mine = fmaxf(mine, vec_max<N>(f));
+  }
+  float hi = mine, low = mine >= kFloor ? mine : INFINITY;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    hi = fmaxf(hi, __shfl_xor(hi, d, 64));
+    low = fminf(low, __shfl_xor(low, d, 64));
+  }
+  if ((tid & 63) == 0) {
+    wave_hi[tid >> 6] = hi;
+    wave_lo[tid >> 6] = low;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < WAVES; ++v) {
+    hi = fmaxf(hi, wave_hi[v]);
+    low = fminf(low, wave_lo[v]);
+  }
+  const float z = at_max(hi);
+  float reach = -INFINITY;  // vectors with an element from here on are listed: all of few
+  if (vecs > 2 * k) {
+    const Bins bins(hi, low);
+    const int b = bins.of(mine);
+    atomicAdd(&l.hist[b], 1);
+    __syncthreads();
+    const int last = kth_bin(l.hist, k);
+    if (b <= last) atomicMin(&l.low, order_of(mine));
+    __syncthreads();
+    reach = last < 255 ? value_of(l.low) : kFloor;
+  }
+
+  // a lane keeps the sums of the listed vector that holds its largest logit apart
+  double sum = 0.0, wsum = 0.0;
+  VecSums held{0.0f, 0.0f};
+  float held_m = -INFINITY;
+  int held_at = -1;
+  auto take = [&](V4 v, int i) {
+    float f[N];
+    Vec<E>::unpack(v, f);
+    const float m = vec_max<N>(f);
+    VecSums t = vec_sums<N>(f, z, s);
+    if (m >= reach) {
+      const int at = atomicAdd(&hits, 1);
+      if (at < kHits) {
+        hit[at] = make_uint4(v[0], v[1], v[2], v[3]);
+        hit_at[at] = i;
+      }
+      if (m > held_m) {
+        const VecSums before = held;
+        held = t;
+        t = before;
+        held_m = m;
+        held_at = i;
+      }
+    }
+    sum += t.s;
+    wsum += t.w;
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid + u * THREADS < vecs) take(w[u], tid + u * THREADS);
+  int base = U * THREADS;
+  for (; base + U * THREADS <= whole; base += U * THREADS) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) take(w[u], base + tid + u * THREADS);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (base + tid + u * THREADS < vecs) w[u] = vec_at(p, base + tid + u * THREADS, n);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (base + tid + u * THREADS < vecs) take(w[u], base + tid + u * THREADS);
+
+  // the k largest
+  float m = held_m;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  if ((tid & 63) == 0) wave_hi[tid >> 6] = m;
+  clear<THREADS>(l);
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
+  auto listed = [&](auto f) {
+    for (int i = tid; i < hits; i += THREADS) {
+      const uint4 h = hit[i];
+      const V4 v = {h.x, h.y, h.z, h.w};
+      float e[N];
+      Vec<E>::unpack(v, e);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (e[j] >= reach && hit_at[i] * N + j < n) f(e[j], lo + hit_at[i] * N + j, i);
+    }
+  };
+  auto all = [&](auto f) {
+    for (int i = tid; i < vecs; i += THREADS) {
+      float e[N];
+      Vec<E>::unpack(vec_at(p, i, n), e);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i * N + j < n) f(e[j], lo + i * N + j, -1);
+    }
+  };
+  bool found = hits <= kHits && select_top<THREADS>(listed, m, reach < kFloor ? kFloor : reach, kk, l);
+  if (found && l.count < kk) found = false;
+  if (!found) select_exactly<THREADS>(all, kk, l);
+  const int top = column_of(l.sorted[0]) - lo, top_at = top / N;
+  m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
+
+  // the sums over all but the largest, relative to `from`
+  float from = z;
+  const bool again = s.of(m - z) > kAbove || (m < kFloor && m != z && m > -INFINITY);
+  if (again) {
+    from = m;
+    sum = wsum = 0.0;
+    for (int i = tid; i < vecs; i += THREADS) {
+      float f[N];
+      Vec<E>::unpack(vec_at(p, i, n), f);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i * N + j == top) f[j] = -INFINITY;
+      const VecSums t = vec_sums<N>(f, from, s);
+      sum += t.s;
+      wsum += t.w;
+    }
+  } else if (held_at != top_at) {
+    sum += held.s;
+    wsum += held.w;
+  }
+  sum = wave_sum(sum);
+  wsum = wave_sum(wsum);
+  if ((tid & 63) == 0) {
+    wave_s[tid >> 6] = sum;
+    wave_w[tid >> 6] = wsum;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int v = 1; v < WAVES; ++v) {
+      sum += wave_s[v];
+      wsum += wave_w[v];
+    }
+    if (!again && m > -INFINITY) {
+      float f[N];
+      if (l.first >= 0) {
+        const uint4 h = hit[l.first];
+        const V4 v = {h.x, h.y, h.z, h.w};
+        Vec<E>::unpack(v, f);
+      } else {
+        Vec<E>::unpack(vec_at(p, top_at, n), f);
+      }
+      if (m < reach) {  // not held: all logits are below kFloor, those equal to the largest count 1 and the others 0
+        const VecSums with = vec_sums<N>(f, from, s);
+        sum -= with.s;
+        wsum -= with.w;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (top_at * N + j == top) f[j] = -INFINITY;
+      const VecSums others = vec_sums<N>(f, from, s);
+      sum += others.s;
+      wsum += others.w;
+    }
+    const double d = ((double)m - from) * out.inv_temperature, one = exp(d);
+    shared = m > -INFINITY ? TopStats{m, sum / one, (sum * d - wsum * kLn2) / one} : TopStats{m, sum, 0.0};
+  }
+  __syncthreads();
+  TopStats v = shared;
+  if (splits > 1) {
+    const int64_t at = row * splits + sp;
+    if (tid == 0) parts.stats[at] = {v.r, v.gap, v.m};
+    if (tid < k) parts.entries[at * k + tid] = tid < kk ? l.sorted[tid] : 0;
+    return;
+  }
+  v.gap /= 1.0 + v.r;
+  put_row(out, row, v, target, target ? Vec<E>::value(x[row * stride + y]) : 0.0f, l.sorted, kk);
+}
+
+// The pieces of a row: their statistics by one wave, the k largest of their
+// largest by the workgroup.
+template <class E>
+__global__ __launch_bounds__(256) void top_join_kernel(const E* __restrict__ x, int64_t stride,
+                                                       const int32_t* __restrict__ targets, int V, int splits,
+                                                       TopOut out, TopParts parts) {
+  __shared__ Select l;
+  __shared__ TopStats shared;
+  __shared__ float shared_lo;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const int y = targets != nullptr ? targets[row] : -1;
   const bool target = y >= 0 && y < V;
   if (targets != nullptr && !target) return put_masked(out, row);
-  const E* p = x + row * stride;
-  const int vecs = V / N;
-  // the first of the largest logits
-  float m = -INFINITY;
-  int at = 0x7FFFFFFF;
-  each_element<E, THREADS>(p, V, [&](float f, int j) {
-    if (f > m) {
-      m = f;
-      at = j;
-    }
-  });
+  const int k = out.k < 1 ? 1 : out.k;
+  const int kk = k < V ? k : V;
+  const uint64_t* entries = parts.entries + row * splits * k;
+  clear<256>(l);
+  if (tid < 64) {
+    const TopPiece* piece = parts.stats + row * splits + tid;
+    const bool on = tid < splits;
+    const TopStats v = on ? TopStats{piece->m, piece->r, piece->gap} : TopStats{-INFINITY, 0.0, 0.0};
+    // what the piece's k-th largest reaches, k entries of the row do
+    const uint64_t last = on ? entries[tid * k + k - 1] : 0;
+    float m = v.m, lo = last != 0 ? value_of(static_cast<uint32_t>(last >> 32)) : -INFINITY;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const float om = __shfl_xor(m, d, 64);
-    const int oat = __shfl_xor(at, d, 64);
-    if (om > m || (om == m && oat < at)) {
-      m = om;
-      at = oat;
+    for (int d = 32; d >= 1; d >>= 1) {
+      m = fmaxf(m, __shfl_xor(m, d, 64));
+      lo = fmaxf(lo, __shfl_xor(lo, d, 64));
+    }
+    const uint64_t top = __ballot(v.m == m);
+    const bool holds = top != 0 && tid == __builtin_ctzll(top);  // the largest logit, whose 1 is not in r
+    const double d = ((double)m - v.m) * out.inv_temperature;
+    const double f = holds ? 1.0 : v.m > -INFINITY ? exp(-d) : 0.0;
+    const double r = wave_sum(holds ? v.r : f * (1.0 + v.r));
+    const double gap = wave_sum(f > 0.0 ? f * (v.gap + (holds ? 0.0 : d * (1.0 + v.r))) : 0.0);
+    if (tid == 0) {
+      shared = {m, r, gap / (1.0 + r)};
+      shared_lo = lo;
     }
   }
-  if ((tid & 63) == 0) {
-    wave_m[tid >> 6] = m;
-    wave_at[tid >> 6] = at;
-  }
-  if (tid == 0) count = 0;
   __syncthreads();
-  m = wave_m[0];
-  at = wave_at[0];
-  for (int w = 1; w < 4; ++w) {
-    if (wave_m[w] > m || (wave_m[w] == m && wave_at[w] < at)) {
-      m = wave_m[w];
-      at = wave_at[w];
-    }
-  }
-  // the sums over the others
-  double r = 0.0, g = 0.0;
-  const float z = at_max(m);
-  each_element<E, THREADS>(p, V, [&](float f, int j) {
-    if (j == at) return;
-    const float a = s.of(f - z), e = __builtin_amdgcn_exp2f(a);
-    r += e;
-    g -= (double)e * fmaxf(a, -256.0f);
-  });
-  r = block_sum<4>(r, lds);
-  g = block_sum<4>(g, lds);
-  const TopStats stats{m, r, g * kLn2 / (1.0 + r)};
-  // the k largest: all above the k-th, then the first ones equal to it
-  const int k = out.k < V ? out.k : V;
-  if (k > 0) {
-    const Kth kth = kth_largest<THREADS>(
-        [&](auto f) { each_element<E, THREADS>(p, V, [&](float v, int) { f(order_of(v)); }); }, k, hist, found);
-    each_element<E, THREADS>(p, V, [&](float v, int j) {
-      if (order_of(v) > kth.order) list[atomicAdd(&count, 1)] = entry_of(v, j);
-    });
-    int want = kth.equal, have = k - kth.equal;
-    for (int j0 = 0; j0 < V && want > 0; j0 += THREADS) {
-      const int j = j0 + tid;
-      const bool tie = j < V && order_of(Vec<E>::value(p[j])) == kth.order;
-      const uint64_t lanes = __ballot(tie);
-      if ((tid & 63) == 0) wave_ties[tid >> 6] = __popcll(lanes);
-      __syncthreads();
-      int before = __popcll(lanes & ((1ull << (tid & 63)) - 1)), all = 0;
-      for (int w = 0; w < 4; ++w) {
-        before += w < (tid >> 6) ? wave_ties[w] : 0;
-        all += wave_ties[w];
-      }
-      if (tie && before < want) list[have + before] = entry_of(value_of(kth.order), j);
-      have += all < want ? all : want;
-      want -= all < want ? all : want;
-      __syncthreads();
-    }
-    __syncthreads();
-    if (tid < k) {
-      int rank = 0;
-      for (int i = 0; i < k; ++i) rank += list[i] > list[tid];
-      sorted[rank] = list[tid];
-    }
-    __syncthreads();
-  }
-  put_row(out, row, stats, target, target ? Vec<E>::value(p[y]) : 0.0f, sorted, k);
+  const TopStats v = shared;
+  auto each = [&](auto f) {
+    for (int i = tid; i < splits * k; i += 256)
+      if (entries[i] != 0) f(value_of(static_cast<uint32_t>(entries[i] >> 32)), column_of(entries[i]), -1);
+  };
+  if (out.k > 0 && !select_top<256>(each, v.m, shared_lo < kFloor ? kFloor : shared_lo, kk, l))
+    select_exactly<256>(each, kk, l);
+  put_row(out, row, v, target, target ? Vec<E>::value(x[row * stride + y]) : 0.0f, l.sorted, kk);
 }
 
 // ---------------------------------------------------------------------------
@@ -308,13 +631,58 @@ __global__ __launch_bounds__(kGradVecs) void top_grad_kernel(GradArgs<E> a, cons
 // host side
 // ---------------------------------------------------------------------------
 
+// Pieces of a row: about as many as give 1024 workgroups, of at least 4096
+// logits each and at most what one workgroup takes.
+static int top_splits(int64_t T, int64_t V) {
+  const int64_t rows = T < 1 ? 1 : T;
+  int64_t splits = (1024 + rows / 2) / rows;
+  const int64_t most = ceil_div(V, 4096), least = ceil_div(V, kMaxPiece);
+  splits = splits < most ? splits : most;
+  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  return static_cast<int>(splits > least ? splits : least > 1 ? least : 1);
+}
+
+// Waves of a workgroup, the fewest of 4, 8 and 16 with which a row of logits in
+// no particular order lists half of what there is room for: with G lanes the
+// k-th largest of their first 32 elements each is reached by a share of
+// -log(1 - k / G) / 32.
+static int top_waves(int64_t piece, int k) {
+  for (int waves = 4; waves < 16; waves *= 2)
+    if (k < 64 * waves && -std::log(1.0 - k / (64.0 * waves)) / 32.0 * piece <= kHits / 2) return waves;
+  return 16;
+}
+
+struct TopPlan {
+  int splits, piece, waves;
+  bool fits;  // one launch
+  TopParts parts;
+  size_t bytes;
+};
+
+static TopPlan plan_top(int64_t T, int64_t V, int64_t k, void* ws) {
+  TopPlan l{};
+  l.splits = top_splits(T, V);
+  l.piece = static_cast<int>(round_up(ceil_div(V, l.splits), 8));
+  l.waves = top_waves(l.piece, static_cast<int>(k));
+  l.fits = T * l.splits <= max_blocks(64 * l.waves);
+  Carver w(ws);
+  const int64_t pieces = l.splits > 1 ? T * l.splits : 0;
+  l.parts.stats = static_cast<TopPiece*>(w.take(pieces * sizeof(TopPiece)));
+  l.parts.entries = static_cast<uint64_t*>(w.take(pieces * (k < 1 ? 1 : k) * sizeof(uint64_t)));
+  l.bytes = w.used > 0 ? w.used : 256;
+  return l;
+}
+
+constexpr int64_t kMaxVocab = int64_t(kMaxSplits) * kMaxPiece;
+
 }  // namespace lora
 
 using namespace lora;
 
 extern "C" size_t lora_token_top_workspace_bytes(int64_t T, int64_t V, int64_t k) {
-  if (T < 0 || V < 0 || k < 0 || T > kMaxRows || V > 0x7FFFFFFF - 8 * kGradVecs || k > kMaxTop) return 0;
-  return 256;
+  if (T < 0 || V < 0 || k < 0 || T > kMaxRows || V > kMaxVocab || k > kMaxTop) return 0;
+  const TopPlan l = plan_top(T, V, k, nullptr);
+  return l.fits ? l.bytes : 0;
 }
 
 extern "C" int lora_token_top(const lora_mat* logits, const int32_t* targets, int64_t k, double temperature,
@@ -323,19 +691,25 @@ extern "C" int lora_token_top(const lora_mat* logits, const int32_t* targets, in
   if (!logits) return LORA_ERR_NULL;
   if (int e = check_logits(logits)) return e;
   if (k < 0) return LORA_ERR_SHAPE;
-  if (k > kMaxTop) return LORA_ERR_LIMIT;
+  if (k > kMaxTop || logits->cols > kMaxVocab) return LORA_ERR_LIMIT;
   if (!temperature_ok(temperature)) return LORA_ERR_VALUE;
-  const int64_t T = logits->rows;
+  const int64_t T = logits->rows, V = logits->cols;
+  const TopPlan l = plan_top(T, V, k, workspace);
+  if (!l.fits) return LORA_ERR_LIMIT;
   if (T == 0) return LORA_OK;
-  if (!entropy || !stats || (logits->cols > 0 && !logits->ptr)) return LORA_ERR_NULL;
+  if (!entropy || !stats || (V > 0 && !logits->ptr)) return LORA_ERR_NULL;
   if ((targets != nullptr) != (logp != nullptr) || (k > 0 && (!top_ids || !top_logp))) return LORA_ERR_NULL;
-  const size_t need = lora_token_top_workspace_bytes(T, logits->cols, k);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return LORA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < l.bytes || !aligned(workspace, 256)) return LORA_ERR_WORKSPACE;
   const TopOut out{logp, entropy, top_ids, top_logp, stats, static_cast<int>(k), 1.0 / temperature};
+  auto st = static_cast<hipStream_t>(stream);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(top_kernel<E>, dim3(T), dim3(256), 0, static_cast<hipStream_t>(stream), (const E*)logits->ptr,
-           logits->stride_row, targets, static_cast<int>(logits->cols), exponent_of(temperature), out);
+    auto* kernel = l.waves == 4 ? top_kernel<E, 4> : l.waves == 8 ? top_kernel<E, 8> : top_kernel<E, 16>;
+    launch(kernel, dim3(T * l.splits), dim3(64 * l.waves), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
+           static_cast<int>(V), l.splits, l.piece, exponent_of(temperature), out, l.parts);
+    if (l.splits > 1)
+      launch(top_join_kernel<E>, dim3(T), dim3(256), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
+             static_cast<int>(V), l.splits, out, l.parts);
   });
   return launch_status();
 }

@@ -17,9 +17,11 @@
 // out. The teacher's tokens and the sums of a row are joined in float64.
 //
 // Kernels:
-//   distill_row_kernel   a workgroup to a row: the divergence, and what the gradient takes
-//   distill_grad_kernel  the gradient's rows
-//   distill_sum_kernel   the weighted sum of the rows' divergences
+//   distill_row_kernel    a row by one workgroup, to its divergence or to its gradient
+//   distill_piece_kernel  the others' sum of a piece of a row
+//   distill_join_kernel   the pieces of a row joined: the divergence, and what the gradient takes
+//   distill_grad_kernel   the gradient's rows from that
+//   distill_sum_kernel    the weighted sum of the rows' divergences
 
 #include <type_traits>
 
@@ -28,7 +30,6 @@
 namespace lora {
 
 constexpr int kMaxTeacher = 256;       // tokens of a teacher for each row
-constexpr int kChunkVecs = 16384;      // vectors of a row whose elements' bits are in LDS at a time
 constexpr int kStateHead = 2;          // state of a row: m, a, and a value for each of the teacher's tokens
 
 struct Teacher {
@@ -47,208 +48,425 @@ struct Others {
 
 // The teacher's tokens of one row, in LDS.
 struct Tokens {
-  int id[kMaxTeacher];        // -1: none
-  float x[kMaxTeacher];       // the row's logits there
-  float b[kMaxTeacher];       // tau dx there
-  double q[kMaxTeacher];
-  int twice, named;           // whether an id occurs twice; how many ids there are
+  int id[kMaxTeacher];   // -1: none
+  double q[kMaxTeacher]; // if an id occurs twice
+  int twice;
 };
-
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmax(v, __shfl_xor(v, d, 64));
-  return v;
-}
 
 struct Row {
-  float kl, a;  // tau dx = a exp((x - m) / tau) for the others
+  double kl, a;  // tau dx = a exp((x - m) / tau) for the others
+  float b;       // tau dx at this thread's token
 };
 
-// By one wave: a row's divergence and gradient factors from the others' sum.
-// Entries that name a token twice count both, the token once.
-__device__ __forceinline__ Row finish_row(const Teacher& t, int64_t row, int V, Others o, Tokens& k) {
-  constexpr int J = kMaxTeacher / 64;
-  const int lane = threadIdx.x & 63;
-  const float* logp = t.logp + row * t.k;
-  double lq[J], lp[J];
-  bool on[J], first[J];
-  double top = o.s > 0.0 ? (double)o.m : -INFINITY, most = -INFINITY;
+// A row's divergence and gradient factors from the others' sum, by all threads
+// of a workgroup: the thread i has the teacher's i-th token, `x` the row's logit
+// there. Entries that name a token twice count both, the token once.
+template <int WAVES>
+__device__ __forceinline__ Row finish_row(const Teacher& t, int64_t row, int V, Others o, float x, Tokens& k) {
+  __shared__ float most[2][WAVES];
+  __shared__ double sums[5][WAVES];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const bool on = tid < t.k && k.id[tid] >= 0;
+  bool first = on;
+  if (on && k.twice)
+    for (int e = 0; e < tid; ++e) first = first && k.id[e] != k.id[tid];
+  const float logq = on ? t.logp[row * t.k + tid] : -INFINITY;
+  float top = on ? x : -INFINITY, likely = logq;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int i = lane + 64 * j;
-    on[j] = first[j] = i < t.k && k.id[i] >= 0;
-    lq[j] = on[j] ? (double)logp[i] : -INFINITY;
-    lp[j] = on[j] ? (double)k.x[i] : -INFINITY;
-    top = fmax(top, lp[j]);
-    most = fmax(most, lq[j]);
-    if (on[j] && k.twice)
-      for (int e = 0; e < i; ++e) first[j] = first[j] && k.id[e] != k.id[i];
+  for (int d = 32; d >= 1; d >>= 1) {
+    top = fmaxf(top, __shfl_xor(top, d, 64));
+    likely = fmaxf(likely, __shfl_xor(likely, d, 64));
   }
-  top = wave_max(top);
-  double total = 0.0, z = 0.0;
-  if (!t.rest) {
-    most = wave_max(most);
-#pragma unroll
-    for (int j = 0; j < J; ++j) z += on[j] ? exp(lq[j] - most) : 0.0;
-    most += log(wave_sum(z));
+  if ((tid & 63) == 0) {
+    most[0][wave] = top;
+    most[1][wave] = likely;
   }
-  int named = 0;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    lp[j] = (lp[j] - top) * t.inv_temperature;
-    if (first[j]) total += exp(lp[j]);
-    named += __popcll(__ballot(first[j]));
+  __syncthreads();
+  top = o.s > 0.0 ? o.m : -INFINITY;
+  likely = -INFINITY;
+  for (int w = 0; w < WAVES; ++w) {
+    top = fmaxf(top, most[0][w]);
+    likely = fmaxf(likely, most[1][w]);
   }
-  const double others = o.s > 0.0 ? o.s * exp((o.m - top) * t.inv_temperature) : o.s;
-  total = wave_sum(total) + others;
+  // the sum that x's token is part of, relative to the largest logit; the teacher's, to its largest
+  double lp = ((double)x - top) * t.inv_temperature, lq = logq;
+  double p = 0.0, z = 0.0, tokens = first ? 1.0 : 0.0;
+  if (wave * 64 < t.k) {
+    if (!t.rest) lq -= likely;
+    if (first) p = exp(lp);
+    if (on) z = exp(lq);
+    const double p_sum = wave_sum(p), z_sum = wave_sum(z);
+    tokens = wave_sum(tokens);
+    if ((tid & 63) == 0) {
+      sums[0][wave] = p_sum;
+      sums[1][wave] = z_sum;
+      sums[2][wave] = tokens;
+    }
+  }
+  __syncthreads();
+  const double others = o.s > 0.0 ? o.s * exp(((double)o.m - top) * t.inv_temperature) : o.s;
+  double total = others, all = 0.0, named = 0.0;
+  for (int w = 0; w * 64 < t.k; ++w) {
+    total += sums[0][w];
+    all += sums[1][w];
+    named += sums[2][w];
+  }
   // a NaN, +inf (their difference from the largest is NaN) or nothing above -inf
   if (!(top > -INFINITY)) total = NAN;
-  const double log_total = log(total);
-  double q[J], all = 0.0, kl = 0.0;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    lp[j] -= log_total;
-    if (!t.rest) lq[j] -= most;
-    q[j] = on[j] ? exp(lq[j]) : 0.0;
-    all += q[j];
-    if (on[j] && q[j] != 0.0) kl += q[j] * (lq[j] - lp[j]);
-    if (k.twice && lane + 64 * j < t.k) k.q[lane + 64 * j] = q[j];
+  double q = z;
+  if (!t.rest) {
+    q = z / all;
+    lq -= log(all);
+    all = all == all ? 1.0 : all;
   }
-  all = wave_sum(all);
-  kl = wave_sum(kl);
+  lp -= log(total);
+  if (wave * 64 < t.k) {
+    if (k.twice && tid < t.k) k.q[tid] = q;
+    const double part = wave_sum(on && q != 0.0 ? q * (lq - lp) : 0.0);
+    if ((tid & 63) == 0) sums[3][wave] = part;
+  }
+  __syncthreads();
+  double kl = 0.0;
+  for (int w = 0; w * 64 < t.k; ++w) kl += sums[3][w];
   const double p_rest = others / total;
   double q_rest = 0.0;
   if (t.rest && named < V) {
-    q_rest = all < 1.0 ? 1.0 - all : 0.0;
-    if (!(all == all)) q_rest = all;
+    q_rest = all < 1.0 ? 1.0 - all : all == all ? 0.0 : all;
     if (q_rest != 0.0) kl += q_rest * (log(q_rest) - log(p_rest));
     all += q_rest;
   }
-  double a = (all * p_rest - q_rest) / o.s;
-  if (o.s == 0.0) a = 0.0;                       // the others hold nothing
+  double a = o.s == 0.0 ? 0.0 : (all * p_rest - q_rest) / o.s;  // 0: the others hold nothing
   if (!(total == total) || !(all == all)) a = kl = NAN;
-  __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int i = lane + 64 * j;
-    if (i >= t.k) continue;
-    double held = q[j];
-    if (on[j] && k.twice) {
-      held = 0.0;
-      for (int e = 0; e < t.k; ++e) held += k.id[e] == k.id[i] ? k.q[e] : 0.0;
-    }
-    k.b[i] = on[j] ? static_cast<float>(all * exp(lp[j]) - held) : 0.0f;
+  double given = q;
+  if (on && k.twice) {
+    given = 0.0;
+    for (int e = 0; e < t.k; ++e) given += k.id[e] == k.id[tid] ? k.q[e] : 0.0;
   }
-  return {static_cast<float>(kl), static_cast<float>(a)};
+  return {kl, a, on ? static_cast<float>(all * exp(lp) - given) : 0.0f};
 }
 
-// The teacher's tokens of a row and its logits there; whether there is any.
-template <class E, int THREADS>
-__device__ __forceinline__ bool load_tokens(const Teacher& t, int64_t row, const E* p, int V, Tokens& k) {
+// The ids of a row's tokens (-1: none) into k; whether there is any.
+template <int THREADS>
+__device__ __forceinline__ bool load_ids(const Teacher& t, int64_t row, int V, Tokens& k) {
   const int tid = threadIdx.x;
   bool on = false;
-  if (tid < kMaxTeacher) {
-    const int id = tid < t.k ? t.ids[row * t.k + tid] : -1;
+  if (tid < t.k) {
+    const int id = t.ids[row * t.k + tid];
     on = id >= 0 && id < V;
     k.id[tid] = on ? id : -1;
-    k.x[tid] = on ? Vec<E>::value(p[id]) : 0.0f;
   }
   if (tid == 0) k.twice = 0;
   return __syncthreads_or(on);
 }
 
-// Sets the bits of the teacher's tokens among the elements of the vectors
-// [base, base + kChunkVecs): bit e of byte v for element e of vector base + v
-// (the row's last elements are of one more vector).
+// Sets the bits of the tokens among the elements [lo, lo + n) of a row: bit e
+// of byte v for element e of the piece's vector v (the last one may be in part).
 template <int N, int THREADS>
-__device__ __forceinline__ void mark_tokens(const Teacher& t, Tokens& k, int base, uint32_t* bits) {
+__device__ __forceinline__ void mark_tokens(const Teacher& t, Tokens& k, int lo, int n, uint32_t* bits) {
   const int tid = threadIdx.x;
-  uint4* clear = reinterpret_cast<uint4*>(bits);
-  for (int i = tid; i < kChunkVecs / 16; i += THREADS) clear[i] = zero4();
+  uint4* words = reinterpret_cast<uint4*>(bits);
+  for (int i = tid; i < (n / N + 16) / 16; i += THREADS) words[i] = zero4();
   __syncthreads();
-  if (tid < t.k && k.id[tid] >= 0) {
-    const int v = k.id[tid] / N - base;
-    if (v >= 0 && v < kChunkVecs) {
-      const uint32_t bit = 1u << (8 * (v & 3) + k.id[tid] % N);
-      if (atomicOr(&bits[v >> 2], bit) & bit) k.twice = 1;
-    }
+  if (tid < t.k && k.id[tid] >= lo && k.id[tid] - lo < n) {
+    const int at = k.id[tid] - lo, v = at / N;
+    const uint32_t bit = 1u << (8 * (v & 3) + at % N);
+    if (atomicOr(&bits[v >> 2], bit) & bit) k.twice = 1;
   }
   __syncthreads();
 }
 
+// A vector with -inf in the place of the teacher's tokens.
 template <class E>
-__global__ __launch_bounds__(256) void distill_row_kernel(const E* __restrict__ x, int64_t stride, int V, Teacher t,
-                                                          Exponent s, float* __restrict__ kl,
-                                                          float* __restrict__ state) {
-  constexpr int N = Vec<E>::N, THREADS = 256;
+__device__ __forceinline__ void leave_out(float* f, uint32_t off) {
+  if (off == 0) return;
+#pragma unroll
+  for (int e = 0; e < Vec<E>::N; ++e)
+    if (off >> e & 1u) f[e] = -INFINITY;
+}
+
+template <int N>
+__device__ __forceinline__ float sum_exp(const float* f, float z, Exponent s) {
+  if constexpr (N == 1)
+    return __builtin_amdgcn_exp2f(s.of(f[0] - z));
+  else
+    return sum_exp<N / 2>(f, z, s) + sum_exp<N / 2>(f + N / 2, z, s);
+}
+
+// The largest of the workgroup's v.
+template <int WAVES>
+__device__ __forceinline__ float block_max(float v, float* lds) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) v = fmaxf(v, lds[w]);
+  __syncthreads();
+  return v;
+}
+
+constexpr float kAbove = 64.0f;  // binary orders that a logit may be above the reference
+
+// One pass over n elements from p on, but for those whose bits are set. The
+// exponents are relative to the largest of the first vectors, which the others
+// exceed by little: no running maximum. Where one is kAbove binary orders
+// larger the elements are read again. The last H vectors per lane stay in
+// `held` (as read), the elements past the last vector in `last`.
+template <class E, int WAVES, int H>
+struct OthersPass {
+  static constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
+  using V4 = typename Vec<E>::type;
+  int vecs, body, rest;
+  V4 held[H];
+  float last;
+
+  __device__ __forceinline__ Others run(const E* p, int n, const uint8_t* byte, Exponent s, float* lds_f,
+                                        double* lds_d) {
+    const int tid = threadIdx.x;
+    vecs = n / N;
+    rest = vecs * N + tid;
+    body = vecs > H * THREADS ? vecs - H * THREADS : 0;
+    float m = -INFINITY;
+    auto largest = [&](V4 w, int i) {
+      float f[N];
+      Vec<E>::unpack(w, f);
+      leave_out<E>(f, byte[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
+    };
+    V4 w[U];
+    last = rest < n ? Vec<E>::value(p[rest]) : -INFINITY;
+    const bool left = rest < n && !(byte[vecs] >> tid & 1u);
+    if (body > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (tid + u * THREADS < body) w[u] = vload(p + (int64_t)(tid + u * THREADS) * N);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (tid + u * THREADS < body) largest(w[u], tid + u * THREADS);
+    } else {
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(tid + h * THREADS) * N);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (tid + h * THREADS < vecs) largest(held[h], tid + h * THREADS);
+    }
+    if (left) m = fmaxf(m, last);
+    m = block_max<WAVES>(m, lds_f);
+    const float first = m;
+    float z = at_max(m);
+    double sum = 0.0;
+    auto take = [&](V4 v, int i) {
+      float f[N];
+      Vec<E>::unpack(v, f);
+      leave_out<E>(f, byte[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
+      sum += sum_exp<N>(f, z, s);
+    };
+    if (left) sum += __builtin_amdgcn_exp2f(s.of(last - z));
+    if (body > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (tid + u * THREADS < body) take(w[u], tid + u * THREADS);
+      int i = tid + U * THREADS;
+      for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = vload(p + (int64_t)(i + u * THREADS) * N);
+#pragma unroll
+        for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+      }
+      for (; i < body; i += THREADS) take(vload(p + (int64_t)i * N), i);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (body + tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(body + tid + h * THREADS) * N);
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (body + tid + h * THREADS < vecs) take(held[h], body + tid + h * THREADS);
+    m = block_max<WAVES>(m, lds_f);
+    if (s.of(m - z) > kAbove || (first == -INFINITY && m > -INFINITY)) {
+      z = m;
+      sum = left ? __builtin_amdgcn_exp2f(s.of(last - z)) : 0.0;
+      for (int i = tid; i < vecs; i += THREADS) take(vload(p + (int64_t)i * N), i);
+    }
+    return {z, block_sum<WAVES>(sum, lds_d)};
+  }
+};
+
+// A row's divergence and state in memory; zeros for a masked one.
+__device__ __forceinline__ void put_row(float* kl, float* state, const Teacher& t, int64_t row, float m, const Row& r) {
+  if (threadIdx.x == 0) kl[row] = static_cast<float>(r.kl);
+  if (state == nullptr) return;
+  float* out = state + row * (t.k + kStateHead);
+  if (threadIdx.x == 0) {
+    out[0] = m;
+    out[1] = static_cast<float>(r.a);
+  }
+  if ((int)threadIdx.x < t.k) out[kStateHead + threadIdx.x] = r.b;
+}
+
+// A row by one workgroup: the divergence, and with GRAD the gradient at once,
+// for which the row's last H vectors per lane stay in registers and the others
+// are read again, the most recently read first.
+template <class E, int WAVES, bool GRAD>
+__global__ __launch_bounds__(64 * WAVES, 8) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
+                                                                    Exponent s, float* __restrict__ kl,
+                                                                    float* __restrict__ state,
+                                                                    const float* __restrict__ weights, float scale,
+                                                                    E* dx, int64_t dx_stride) {
+  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES, H = GRAD ? 6 : 1;
+  using V4 = typename Vec<E>::type;
+  extern __shared__ uint4 dynamic[];
   __shared__ Tokens tokens;
-  __shared__ __align__(16) uint32_t bits[kChunkVecs / 4];
-  __shared__ double lds[4];
-  __shared__ float wave_m[4];
+  __shared__ double lds_d[WAVES];
+  __shared__ float lds_f[WAVES];
+  uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
+  // dx may be x: no restrict on it, and a vector is stored by the lane that loaded it
   const E* p = x + row * stride;
-  float* out = state == nullptr ? nullptr : state + row * (t.k + kStateHead);
-  if (!load_tokens<E, THREADS>(t, row, p, V, tokens)) {
-    if (tid == 0) kl[row] = 0.0f;
-    if (out != nullptr)
-      for (int i = tid; i < t.k + kStateHead; i += THREADS) out[i] = 0.0f;
+  E* q = dx + row * dx_stride;
+  const int vecs = V / N;
+  auto zeros = [&] {
+    const V4 zero = {0u, 0u, 0u, 0u};
+    for (int i = tid; i < vecs; i += THREADS) vstore_nt(q + (int64_t)i * N, zero);
+    if (vecs * N + tid < V) q[vecs * N + tid] = Vec<E>::round(0.0f);
+  };
+  if (!load_ids<THREADS>(t, row, V, tokens)) {
+    put_row(kl, state, t, row, 0.0f, Row{0.0, 0.0, 0.0f});
+    if constexpr (GRAD) zeros();
     return;
   }
-  const int vecs = V / N;
-  const uint8_t* byte = reinterpret_cast<const uint8_t*>(bits);
-  // f(value) for the others' elements
-  auto others = [&](auto f) {
-    for (int base = 0; base <= vecs; base += kChunkVecs) {
-      mark_tokens<N, THREADS>(t, tokens, base, bits);
-      const int end = vecs - base < kChunkVecs ? vecs - base : kChunkVecs;
-      for (int i = tid; i < end; i += THREADS) {
-        float v[N];
-        Vec<E>::unpack(vload(p + (int64_t)(base + i) * N), v);
-        const uint32_t off = byte[i];
+  const float mine = tid < t.k && tokens.id[tid] >= 0 ? Vec<E>::value(p[tokens.id[tid]]) : 0.0f;
+  mark_tokens<N, THREADS>(t, tokens, 0, V, bits);
+  OthersPass<E, WAVES, H> pass;
+  const Others others = pass.run(p, V, reinterpret_cast<const uint8_t*>(bits), s, lds_f, lds_d);
+  const Row r = finish_row<WAVES>(t, row, V, others, mine, tokens);
+  put_row(kl, state, t, row, others.m, r);
+  if constexpr (GRAD) {
+    const float c = weights[row] * scale;
+    if (c == 0.0f) return zeros();
+    // the second pass unpacks the held vectors anew: their float32 values would take twice the registers
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (!(off >> e & 1u)) f(v[e]);
-      }
-      if (end < kChunkVecs && tid < V - vecs * N && !(byte[end] >> tid & 1u)) f(Vec<E>::value(p[vecs * N + tid]));
-      __syncthreads();
+    for (int h = 0; h < H; ++h) asm volatile("" : "+v"(pass.held[h]));
+    const float a = static_cast<float>(r.a), factor = a == 0.0f ? 0.0f : c * a, m = others.m;
+    auto grad = [&](V4 w, int i) {
+      float f[N];
+      Vec<E>::unpack(w, f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] = factor * __builtin_amdgcn_exp2f(s.of(f[e] - m));
+      vstore_nt(q + (int64_t)i * N, Vec<E>::pack(f));
+    };
+    if (pass.rest < V) q[pass.rest] = Vec<E>::round(factor * __builtin_amdgcn_exp2f(s.of(pass.last - m)));
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (pass.body + tid + h * THREADS < vecs) grad(pass.held[h], pass.body + tid + h * THREADS);
+    // the lane's vectors of the body, last first
+    int i = tid < pass.body ? tid + (pass.body - 1 - tid) / THREADS * THREADS : -1;
+    for (; i - (U - 1) * THREADS >= 0; i -= U * THREADS) {
+      V4 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(i - u * THREADS) * N);
+#pragma unroll
+      for (int u = 0; u < U; ++u) grad(w[u], i - u * THREADS);
     }
-  };
-  float m = -INFINITY;
-  others([&](float v) { m = fmaxf(m, v); });
+    for (; i >= 0; i -= THREADS) grad(vload_nt(p + (int64_t)i * N), i);
+    // the entries at the teacher's tokens, over what the vectors put there
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid < t.k && tokens.id[tid] >= 0) q[tokens.id[tid]] = Vec<E>::round(c * r.b);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few or long rows in pieces
+// ---------------------------------------------------------------------------
+
+struct Pieces {
+  Others* part;  // [T][splits]
+  float* x;      // [T][k]: the logits at the teacher's tokens (kept here: they may be overwritten)
+};
+
+template <class E>
+__global__ __launch_bounds__(256) void distill_piece_kernel(const E* __restrict__ x, int64_t stride, int V, int splits,
+                                                            int piece, Teacher t, Exponent s, Pieces pieces) {
+  constexpr int N = Vec<E>::N, THREADS = 256;
+  extern __shared__ uint4 dynamic[];
+  __shared__ Tokens tokens;
+  __shared__ double lds_d[4];
+  __shared__ float lds_f[4];
+  uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
+  const int64_t row = blockIdx.x / (unsigned)splits;
+  const int sp = (int)(blockIdx.x % (unsigned)splits);
+  const int tid = threadIdx.x;
+  if (!load_ids<THREADS>(t, row, V, tokens)) return;
+  const int lo = sp * piece;
+  const int n = V - lo < piece ? V - lo : piece;
+  const E* p = x + row * stride + lo;
+  if (tid < t.k && tokens.id[tid] >= lo && tokens.id[tid] - lo < n)
+    pieces.x[row * t.k + tid] = Vec<E>::value(p[tokens.id[tid] - lo]);
+  mark_tokens<N, THREADS>(t, tokens, lo, n, bits);
+  OthersPass<E, 4, 1> pass;
+  const Others others = pass.run(p, n, reinterpret_cast<const uint8_t*>(bits), s, lds_f, lds_d);
+  if (tid == 0) pieces.part[row * splits + sp] = others;
+}
+
+// A row's pieces joined, by one workgroup.
+__global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Teacher t, Pieces pieces,
+                                                           float* __restrict__ kl, float* __restrict__ state) {
+  __shared__ Tokens tokens;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
+  if (!load_ids<256>(t, row, V, tokens)) return put_row(kl, state, t, row, 0.0f, Row{0.0, 0.0, 0.0f});
+  const bool on = tid < t.k && tokens.id[tid] >= 0;
+  const float mine = on ? pieces.x[row * t.k + tid] : 0.0f;
+  if (on)
+    for (int e = 0; e < tid; ++e)
+      if (tokens.id[e] == tokens.id[tid]) tokens.twice = 1;
+  const Others v = lane < splits ? pieces.part[row * splits + lane] : Others{-INFINITY, 0.0};
+  float m = v.s > 0.0 ? v.m : -INFINITY;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  if ((tid & 63) == 0) wave_m[tid >> 6] = m;
+  m = at_max(m);
+  const Others all{m, wave_sum(v.s > 0.0 ? v.s * exp(((double)v.m - m) * t.inv_temperature) : v.s)};
   __syncthreads();
-  m = at_max(fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3])));
-  if (tid == 0) tokens.twice = 0;
+  put_row(kl, state, t, row, m, finish_row<4>(t, row, V, all, mine, tokens));
+}
+
+template <int WAVES>
+__device__ __forceinline__ void sum_losses(const float* kl, const float* weights, int64_t T, float* loss) {
+  __shared__ double lds[WAVES];
   double sum = 0.0;
-  others([&](float v) { sum += __builtin_amdgcn_exp2f(s.of(v - m)); });
-  sum = block_sum<4>(sum, lds);
-  if (tid < 64) {
-    const Row r = finish_row(t, row, V, Others{m, sum}, tokens);
-    if (tid == 0) {
-      kl[row] = r.kl;
-      if (out != nullptr) {
-        out[0] = m;
-        out[1] = r.a;
-      }
-    }
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < T; t += 64 * WAVES) {
+    const float w = weights[t];
+    if (w != 0.0f) sum += (double)w * kl[t];
   }
-  __syncthreads();
-  if (out != nullptr && tid < t.k) out[kStateHead + tid] = tokens.b[tid];
+  sum = block_sum<WAVES>(sum, lds);
+  if (threadIdx.x == 0) *loss = static_cast<float>(sum);
+}
+
+__global__ __launch_bounds__(1024) void distill_sum_kernel(const float* __restrict__ kl,
+                                                           const float* __restrict__ weights, int64_t T,
+                                                           float* __restrict__ loss) {
+  sum_losses<16>(kl, weights, T, loss);
 }
 
 // A workgroup takes one piece of a row, a vector per lane; the entries at the
-// teacher's tokens follow once the vectors are written.
+// teacher's tokens follow once the vectors are written. One more at the end of
+// the grid sums the rows' losses.
 template <class E>
 __global__ __launch_bounds__(kGradVecs) void distill_grad_kernel(GradArgs<E> a, const int32_t* __restrict__ ids, int k,
                                                                  const float* __restrict__ state,
                                                                  const float* __restrict__ coef,
                                                                  const float* __restrict__ grad_out, float scale,
-                                                                 Exponent s) {
+                                                                 Exponent s, int64_t T, const float* __restrict__ kl,
+                                                                 float* __restrict__ loss) {
   constexpr int N = Vec<E>::N;
   const int64_t row = blockIdx.x / (unsigned)a.pieces;
+  if (row == T) return sum_losses<kGradVecs / 64>(kl, coef, T, loss);
   const int lo = (blockIdx.x % (unsigned)a.pieces) * kGradVecs * N;
   const int n = a.V - lo < kGradVecs * N ? a.V - lo : kGradVecs * N;
   const int tid = threadIdx.x;
@@ -283,25 +501,49 @@ __global__ __launch_bounds__(kGradVecs) void distill_grad_kernel(GradArgs<E> a, 
   }
 }
 
-__global__ __launch_bounds__(1024) void distill_sum_kernel(const float* __restrict__ kl,
-                                                           const float* __restrict__ weights, int64_t T,
-                                                           float* __restrict__ loss) {
-  __shared__ double lds[16];
-  double sum = 0.0;
-  for (int64_t t = threadIdx.x; t < T; t += 1024) {
-    const float w = weights[t];
-    if (w != 0.0f) sum += (double)w * kl[t];
-  }
-  sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) *loss = static_cast<float>(sum);
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 
-static size_t state_bytes(int64_t T, int64_t k) {
-  return static_cast<size_t>(round_up(T * (k + kStateHead) * (int64_t)sizeof(float), 256));
+constexpr int kMaxPieceVecs = 32768;  // vectors of a row that one workgroup takes: a byte of LDS for each
+constexpr int kMaxSplits = 64;
+constexpr int64_t kMaxVocab = int64_t(kMaxSplits) * kMaxPieceVecs * 4;
+
+// Pieces of a row: about as many as give 1024 workgroups, of at least 4096
+// logits each.
+static int piece_splits(int64_t T, int64_t V) {
+  const int64_t rows = T < 1 ? 1 : T;
+  int64_t splits = (1024 + rows / 2) / rows;
+  const int64_t most = ceil_div(V, 4096), least = ceil_div(V, int64_t(kMaxPieceVecs) * 4);
+  splits = splits < most ? splits : most;
+  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  return static_cast<int>(splits > least ? splits : least > 1 ? least : 1);
+}
+
+// Whether one workgroup takes a whole row.
+static bool by_rows(const lora_mat* x) {
+  return x->cols / vec_elems(x->dtype) < kMaxPieceVecs && (piece_splits(x->rows, x->cols) == 1 || x->rows >= 80);
+}
+
+static int row_waves(const lora_mat* x) {
+  const int64_t vecs = x->cols / vec_elems(x->dtype);
+  return vecs <= 2560 ? 4 : vecs <= 6144 ? 8 : 16;
+}
+
+struct DistillPlan {
+  float* state;
+  Pieces pieces;
+  size_t bytes;
+};
+
+static DistillPlan plan_distill(int64_t T, int64_t V, int64_t k, void* ws) {
+  DistillPlan l{};
+  Carver w(ws);
+  l.state = static_cast<float*>(w.take(T * (k + kStateHead) * sizeof(float)));
+  l.pieces.part = static_cast<Others*>(w.take(T * piece_splits(T, V) * sizeof(Others)));
+  l.pieces.x = static_cast<float*>(w.take(T * k * sizeof(float)));
+  l.bytes = w.used > 0 ? w.used : 256;
+  return l;
 }
 
 static int check_teacher(const lora_teacher* t, int64_t T) {
@@ -317,21 +559,48 @@ static Teacher teacher_of(const lora_teacher* t) {
   return {t->ids, t->logp, static_cast<int>(t->k), t->rest != 0, 1.0 / t->temperature};
 }
 
-static void run_rows(const lora_mat* x, const lora_teacher* t, float* kl, float* state, hipStream_t st) {
+static size_t bit_bytes(int64_t elems, int n) { return static_cast<size_t>(round_up(elems / n + 1, 16)); }
+
+// The rows whole: divergences (and states), with dx their gradients too.
+static void run_rows(const lora_mat* x, const lora_teacher* t, float* kl, float* state, const float* weights,
+                     float scale, const lora_mat* dx, hipStream_t st) {
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    launch(distill_row_kernel<E>, dim3(x->rows), dim3(256), 0, st, (const E*)x->ptr, x->stride_row,
-           static_cast<int>(x->cols), teacher_of(t), exponent_of(t->temperature), kl, state);
+    const int waves = row_waves(x);
+    auto* kernel = dx == nullptr ? (waves == 4   ? distill_row_kernel<E, 4, false>
+                                    : waves == 8 ? distill_row_kernel<E, 8, false>
+                                                 : distill_row_kernel<E, 16, false>)
+                                 : (waves == 4   ? distill_row_kernel<E, 4, true>
+                                    : waves == 8 ? distill_row_kernel<E, 8, true>
+                                                 : distill_row_kernel<E, 16, true>);
+    launch(kernel, dim3(x->rows), dim3(64 * waves), bit_bytes(x->cols, Vec<E>::N), st, (const E*)x->ptr, x->stride_row,
+           static_cast<int>(x->cols), teacher_of(t), exponent_of(t->temperature), kl, state, weights, scale,
+           dx == nullptr ? (E*)nullptr : (E*)dx->ptr, dx == nullptr ? int64_t(0) : dx->stride_row);
   });
 }
 
+// The rows in pieces: divergences and states.
+static void run_pieces(const lora_mat* x, const lora_teacher* t, const DistillPlan& l, float* kl, float* state,
+                       hipStream_t st) {
+  const int splits = piece_splits(x->rows, x->cols), V = static_cast<int>(x->cols);
+  by_type(x, [&](auto* e) {
+    using E = std::remove_pointer_t<decltype(e)>;
+    const int piece = static_cast<int>(round_up(ceil_div(V, splits), Vec<E>::N));
+    launch(distill_piece_kernel<E>, dim3(x->rows * splits), dim3(256), bit_bytes(piece, Vec<E>::N), st,
+           (const E*)x->ptr, x->stride_row, V, splits, piece, teacher_of(t), exponent_of(t->temperature), l.pieces);
+  });
+  launch(distill_join_kernel, dim3(x->rows), dim3(256), 0, st, V, splits, teacher_of(t), l.pieces, kl, state);
+}
+
 static void run_grad(const lora_mat* x, const int32_t* ids, int k, const float* state, const float* coef,
-                     const float* grad_out, float scale, double temperature, const lora_mat* dx, hipStream_t st) {
+                     const float* grad_out, float scale, double temperature, const lora_mat* dx, const float* kl,
+                     float* loss, hipStream_t st) {
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
     const GradArgs<E> a = grad_args<E>(x, dx);
-    launch(distill_grad_kernel<E>, dim3(x->rows * a.pieces), dim3(kGradVecs), 0, st, a, ids, k, state, coef, grad_out,
-           static_cast<float>((double)scale / temperature), exponent_of(temperature));
+    launch(distill_grad_kernel<E>, dim3(x->rows * a.pieces + (loss != nullptr)), dim3(kGradVecs), 0, st, a, ids, k,
+           state, coef, grad_out, static_cast<float>((double)scale / temperature), exponent_of(temperature), x->rows,
+           kl, loss);
   });
 }
 
@@ -340,25 +609,38 @@ static void run_grad(const lora_mat* x, const int32_t* ids, int k, const float* 
 using namespace lora;
 
 extern "C" size_t lora_distill_workspace_bytes(int64_t T, int64_t V, int64_t k) {
-  if (T < 0 || V < 0 || k < 1 || T > kMaxRows || V > 0x7FFFFFFF - 8 * kGradVecs || k > kMaxTeacher) return 0;
-  return state_bytes(T, k) + 256;
+  if (T < 0 || V < 0 || k < 1 || T > kMaxRows || V > kMaxVocab || k > kMaxTeacher) return 0;
+  return plan_distill(T, V, k, nullptr).bytes;
 }
 
-static int check_distill_workspace(const lora_mat* x, const lora_teacher* t, void* ws, size_t bytes) {
-  return !ws || bytes < lora_distill_workspace_bytes(x->rows, x->cols, t->k) || !aligned(ws, 256)
-             ? LORA_ERR_WORKSPACE
-             : LORA_OK;
+// The checks that the divergence and the step share; `blocks`: workgroups of 64 * waves of the largest launch.
+static int check_distill(const lora_mat* x, const lora_teacher* t) {
+  if (int e = check_teacher(t, x->rows)) return e;
+  if (x->cols > kMaxVocab) return LORA_ERR_LIMIT;
+  const bool rows = by_rows(x);
+  const int64_t blocks = rows ? x->rows : x->rows * piece_splits(x->rows, x->cols);
+  return blocks > max_blocks(rows ? 64 * row_waves(x) : 256) ? LORA_ERR_LIMIT : LORA_OK;
+}
+
+static int check_plan(const DistillPlan& l, void* ws, size_t bytes) {
+  return !ws || bytes < l.bytes || !aligned(ws, 256) ? LORA_ERR_WORKSPACE : LORA_OK;
 }
 
 extern "C" int lora_distill_kl(const lora_mat* logits, const lora_teacher* teacher, float* kl, float* state,
                                void* workspace, size_t workspace_bytes, void* stream) {
   if (!logits) return LORA_ERR_NULL;
   if (int e = check_logits(logits)) return e;
-  if (int e = check_teacher(teacher, logits->rows)) return e;
-  if (logits->rows == 0) return LORA_OK;
-  if (!kl || (logits->cols > 0 && !logits->ptr)) return LORA_ERR_NULL;
-  if (int e = check_distill_workspace(logits, teacher, workspace, workspace_bytes)) return e;
-  run_rows(logits, teacher, kl, state, static_cast<hipStream_t>(stream));
+  if (int e = check_distill(logits, teacher)) return e;
+  const int64_t T = logits->rows, V = logits->cols;
+  if (T == 0) return LORA_OK;
+  if (!kl || (V > 0 && !logits->ptr)) return LORA_ERR_NULL;
+  const DistillPlan l = plan_distill(T, V, teacher->k, workspace);
+  if (int e = check_plan(l, workspace, workspace_bytes)) return e;
+  auto st = static_cast<hipStream_t>(stream);
+  if (by_rows(logits))
+    run_rows(logits, teacher, kl, state, nullptr, 0.0f, nullptr, st);
+  else
+    run_pieces(logits, teacher, l, kl, state, st);
   return launch_status();
 }
 
@@ -373,7 +655,7 @@ extern "C" int lora_distill_grad(const lora_mat* logits, const int32_t* top_ids,
   if (!temperature_ok(temperature)) return LORA_ERR_VALUE;
   if (logits->rows == 0 || logits->cols == 0) return LORA_OK;
   if (!top_ids || !state || !coef || !logits->ptr || !dlogits->ptr) return LORA_ERR_NULL;
-  run_grad(logits, top_ids, static_cast<int>(k), state, coef, grad_out, scale, temperature, dlogits,
+  run_grad(logits, top_ids, static_cast<int>(k), state, coef, grad_out, scale, temperature, dlogits, nullptr, nullptr,
            static_cast<hipStream_t>(stream));
   return launch_status();
 }
@@ -385,16 +667,21 @@ extern "C" int lora_distill_step(const lora_mat* logits, const lora_teacher* tea
   if (int e = check_logits(logits)) return e;
   if (int e = check_dlogits(logits, dlogits)) return e;
   const int64_t T = logits->rows, V = logits->cols;
-  if (int e = check_teacher(teacher, T)) return e;
+  if (int e = check_distill(logits, teacher)) return e;
   if (!loss || (T > 0 && (!weights || !kl || (V > 0 && (!logits->ptr || !dlogits->ptr))))) return LORA_ERR_NULL;
+  const DistillPlan l = plan_distill(T, V, teacher->k, workspace);
   if (T > 0)
-    if (int e = check_distill_workspace(logits, teacher, workspace, workspace_bytes)) return e;
+    if (int e = check_plan(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
-  float* state = static_cast<float*>(workspace);
-  if (T > 0) run_rows(logits, teacher, kl, state, st);
-  if (T > 0 && V > 0)
-    run_grad(logits, teacher->ids, static_cast<int>(teacher->k), state, weights, nullptr, grad_scale,
-             teacher->temperature, dlogits, st);
+  if (T > 0 && V > 0 && !by_rows(logits)) {
+    run_pieces(logits, teacher, l, kl, l.state, st);
+    run_grad(logits, teacher->ids, static_cast<int>(teacher->k), l.state, weights, nullptr, grad_scale,
+             teacher->temperature, dlogits, kl, loss, st);
+    return launch_status();
+  }
+  if (T > 0)
+    run_rows(logits, teacher, kl, nullptr, weights, static_cast<float>((double)grad_scale / teacher->temperature),
+             dlogits, st);
   launch(distill_sum_kernel, dim3(1), dim3(1024), 0, st, (const float*)kl, weights, T, loss);
   return launch_status();
 }

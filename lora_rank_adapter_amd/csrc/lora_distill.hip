@@ -59,18 +59,17 @@ struct Row {
 };
 
 // A row's divergence and gradient factors from the others' sum, by all threads
-// of a workgroup: the thread i has the teacher's i-th token, `x` the row's logit
-// there. Entries that name a token twice count both, the token once.
+// of a workgroup: thread i has the teacher's i-th token `id`, with the row's
+// logit x there and the teacher's log probability. Entries that name a token twice count both, the token once.
 template <int WAVES>
-__device__ __forceinline__ Row finish_row(const Teacher& t, int64_t row, int V, Others o, float x, Tokens& k) {
+__device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int id, float x, float logq, Tokens& k) {
   __shared__ float most[2][WAVES];
   __shared__ double sums[5][WAVES];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const bool on = tid < t.k && k.id[tid] >= 0;
+  const bool on = id >= 0;
   bool first = on;
   if (on && k.twice)
-    for (int e = 0; e < tid; ++e) first = first && k.id[e] != k.id[tid];
-  const float logq = on ? t.logp[row * t.k + tid] : -INFINITY;
+    for (int e = 0; e < tid; ++e) first = first && k.id[e] != id;
   float top = on ? x : -INFINITY, likely = logq;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
@@ -140,39 +139,41 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int64_t row, int V, 
   double given = q;
   if (on && k.twice) {
     given = 0.0;
-    for (int e = 0; e < t.k; ++e) given += k.id[e] == k.id[tid] ? k.q[e] : 0.0;
+    for (int e = 0; e < t.k; ++e) given += k.id[e] == id ? k.q[e] : 0.0;
   }
   return {kl, a, on ? static_cast<float>(all * exp(lp) - given) : 0.0f};
 }
 
-// The ids of a row's tokens (-1: none) into k; whether there is any.
-template <int THREADS>
-__device__ __forceinline__ bool load_ids(const Teacher& t, int64_t row, int V, Tokens& k) {
-  const int tid = threadIdx.x;
+// Whether a row has a token at all; every wave looks for itself.
+__device__ __forceinline__ bool any_token(const Teacher& t, int64_t row, int V) {
   bool on = false;
-  if (tid < t.k) {
-    const int id = t.ids[row * t.k + tid];
-    on = id >= 0 && id < V;
-    k.id[tid] = on ? id : -1;
-  }
-  if (tid == 0) k.twice = 0;
-  return __syncthreads_or(on);
+  for (int i = threadIdx.x & 63; i < t.k; i += 64) on = on || static_cast<unsigned>(t.ids[row * t.k + i]) < (unsigned)V;
+  return __ballot(on) != 0;
 }
 
-// Sets the bits of the tokens among the elements [lo, lo + n) of a row: bit e
-// of byte v for element e of the piece's vector v (the last one may be in part).
+// This thread's token of a row, -1 if it has none.
+__device__ __forceinline__ int token_id(const Teacher& t, int64_t row, int V) {
+  if ((int)threadIdx.x >= t.k) return -1;
+  const int id = t.ids[row * t.k + threadIdx.x];
+  return id >= 0 && id < V ? id : -1;
+}
+
+// The bits of the teacher's tokens among the elements [lo, lo + n) of a row:
+// bit e of byte v for element e of the piece's vector v (the last one may be
+// in part). A barrier between the two, and one behind the second.
 template <int N, int THREADS>
-__device__ __forceinline__ void mark_tokens(const Teacher& t, Tokens& k, int lo, int n, uint32_t* bits) {
-  const int tid = threadIdx.x;
+__device__ __forceinline__ void clear_bits(int n, uint32_t* bits, Tokens& k) {
   uint4* words = reinterpret_cast<uint4*>(bits);
-  for (int i = tid; i < (n / N + 16) / 16; i += THREADS) words[i] = zero4();
-  __syncthreads();
-  if (tid < t.k && k.id[tid] >= lo && k.id[tid] - lo < n) {
-    const int at = k.id[tid] - lo, v = at / N;
-    const uint32_t bit = 1u << (8 * (v & 3) + at % N);
-    if (atomicOr(&bits[v >> 2], bit) & bit) k.twice = 1;
-  }
-  __syncthreads();
+  for (int i = threadIdx.x; i < (n / N + 16) / 16; i += THREADS) words[i] = zero4();
+  if (threadIdx.x == 0) k.twice = 0;
+}
+template <int N>
+__device__ __forceinline__ void set_bit(int id, int lo, int n, uint32_t* bits, Tokens& k) {
+  if ((int)threadIdx.x < kMaxTeacher) k.id[threadIdx.x] = id;
+  if (id < lo || id - lo >= n) return;
+  const int v = (id - lo) / N;
+  const uint32_t bit = 1u << (8 * (v & 3) + (id - lo) % N);
+  if (atomicOr(&bits[v >> 2], bit) & bit) k.twice = 1;
 }
 
 // A vector with -inf in the place of the teacher's tokens.
@@ -192,7 +193,7 @@ __device__ __forceinline__ float sum_exp(const float* f, float z, Exponent s) {
     return sum_exp<N / 2>(f, z, s) + sum_exp<N / 2>(f + N / 2, z, s);
 }
 
-// The largest of the workgroup's v.
+// The largest of the workgroup's v; lds is used once.
 template <int WAVES>
 __device__ __forceinline__ float block_max(float v, float* lds) {
 #pragma unroll
@@ -201,18 +202,24 @@ __device__ __forceinline__ float block_max(float v, float* lds) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) v = fmaxf(v, lds[w]);
-  __syncthreads();
   return v;
 }
 
 constexpr float kAbove = 64.0f;  // binary orders that a logit may be above the reference
 
+template <int WAVES>
+struct PassLds {
+  float first[WAVES], most[WAVES];
+  double sum[WAVES];
+};
+
 // One pass over n elements from p on, but for those whose bits are set. The
 // exponents are relative to the largest of the first vectors, which the others
 // exceed by little: no running maximum. Where one is kAbove binary orders
-// larger the elements are read again. The last H vectors per lane stay in
-// `held` (as read), the elements past the last vector in `last`.
-template <class E, int WAVES, int H>
+// larger the elements are read anew. The last H vectors per lane stay in
+// `held` (as read), the elements past the last vector in `last`. AGAIN: the
+// elements will be read once more.
+template <class E, int WAVES, int H, bool AGAIN>
 struct OthersPass {
   static constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
   using V4 = typename Vec<E>::type;
@@ -220,16 +227,20 @@ struct OthersPass {
   V4 held[H];
   float last;
 
-  __device__ __forceinline__ Others run(const E* p, int n, const uint8_t* byte, Exponent s, float* lds_f,
-                                        double* lds_d) {
+  static __device__ __forceinline__ V4 load(const E* at) {
+    if constexpr (AGAIN) return vload(at);
+    return vload_nt(at);
+  }
+
+  __device__ __forceinline__ Others run(const E* p, int n, const uint8_t* byte, Exponent s, PassLds<WAVES>& lds) {
     const int tid = threadIdx.x;
     vecs = n / N;
     rest = vecs * N + tid;
     body = vecs > H * THREADS ? vecs - H * THREADS : 0;
     float m = -INFINITY;
-    auto largest = [&](V4 w, int i) {
+    auto largest = [&](V4 v, int i) {
       float f[N];
-      Vec<E>::unpack(w, f);
+      Vec<E>::unpack(v, f);
       leave_out<E>(f, byte[i]);
 #pragma unroll
       for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
@@ -240,7 +251,7 @@ struct OthersPass {
     if (body > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (tid + u * THREADS < body) w[u] = vload(p + (int64_t)(tid + u * THREADS) * N);
+        if (tid + u * THREADS < body) w[u] = load(p + (int64_t)(tid + u * THREADS) * N);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (tid + u * THREADS < body) largest(w[u], tid + u * THREADS);
@@ -253,7 +264,7 @@ struct OthersPass {
         if (tid + h * THREADS < vecs) largest(held[h], tid + h * THREADS);
     }
     if (left) m = fmaxf(m, last);
-    m = block_max<WAVES>(m, lds_f);
+    m = block_max<WAVES>(m, lds.first);
     const float first = m;
     float z = at_max(m);
     double sum = 0.0;
@@ -273,11 +284,11 @@ struct OthersPass {
       int i = tid + U * THREADS;
       for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = vload(p + (int64_t)(i + u * THREADS) * N);
+        for (int u = 0; u < U; ++u) w[u] = load(p + (int64_t)(i + u * THREADS) * N);
 #pragma unroll
         for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
       }
-      for (; i < body; i += THREADS) take(vload(p + (int64_t)i * N), i);
+      for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), i);
 #pragma unroll
       for (int h = 0; h < H; ++h)
         if (body + tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(body + tid + h * THREADS) * N);
@@ -285,13 +296,18 @@ struct OthersPass {
 #pragma unroll
     for (int h = 0; h < H; ++h)
       if (body + tid + h * THREADS < vecs) take(held[h], body + tid + h * THREADS);
-    m = block_max<WAVES>(m, lds_f);
+    m = block_max<WAVES>(m, lds.most);
     if (s.of(m - z) > kAbove || (first == -INFINITY && m > -INFINITY)) {
       z = m;
       sum = left ? __builtin_amdgcn_exp2f(s.of(last - z)) : 0.0;
-      for (int i = tid; i < vecs; i += THREADS) take(vload(p + (int64_t)i * N), i);
+      for (int i = tid; i < vecs; i += THREADS) take(load(p + (int64_t)i * N), i);
     }
-    return {z, block_sum<WAVES>(sum, lds_d)};
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int v = 0; v < WAVES; ++v) sum += lds.sum[v];
+    return {z, sum};
   }
 };
 
@@ -311,17 +327,16 @@ __device__ __forceinline__ void put_row(float* kl, float* state, const Teacher& 
 // for which the row's last H vectors per lane stay in registers and the others
 // are read again, the most recently read first.
 template <class E, int WAVES, bool GRAD>
-__global__ __launch_bounds__(64 * WAVES, 8) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
+__global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : 8) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
                                                                     Exponent s, float* __restrict__ kl,
                                                                     float* __restrict__ state,
                                                                     const float* __restrict__ weights, float scale,
                                                                     E* dx, int64_t dx_stride) {
-  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES, H = GRAD ? 6 : 1;
+  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES, H = !GRAD ? 1 : WAVES == 4 ? 10 : 16;
   using V4 = typename Vec<E>::type;
   extern __shared__ uint4 dynamic[];
   __shared__ Tokens tokens;
-  __shared__ double lds_d[WAVES];
-  __shared__ float lds_f[WAVES];
+  __shared__ PassLds<WAVES> lds;
   uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
@@ -334,16 +349,21 @@ __global__ __launch_bounds__(64 * WAVES, 8) void distill_row_kernel(const E* x, 
     for (int i = tid; i < vecs; i += THREADS) vstore_nt(q + (int64_t)i * N, zero);
     if (vecs * N + tid < V) q[vecs * N + tid] = Vec<E>::round(0.0f);
   };
-  if (!load_ids<THREADS>(t, row, V, tokens)) {
+  const int id = token_id(t, row, V);
+  clear_bits<N, THREADS>(V, bits, tokens);
+  if (!any_token(t, row, V)) {
     put_row(kl, state, t, row, 0.0f, Row{0.0, 0.0, 0.0f});
     if constexpr (GRAD) zeros();
     return;
   }
-  const float mine = tid < t.k && tokens.id[tid] >= 0 ? Vec<E>::value(p[tokens.id[tid]]) : 0.0f;
-  mark_tokens<N, THREADS>(t, tokens, 0, V, bits);
-  OthersPass<E, WAVES, H> pass;
-  const Others others = pass.run(p, V, reinterpret_cast<const uint8_t*>(bits), s, lds_f, lds_d);
-  const Row r = finish_row<WAVES>(t, row, V, others, mine, tokens);
+  const float mine = id >= 0 ? Vec<E>::value(p[id]) : 0.0f;
+  const float logq = id >= 0 ? t.logp[row * t.k + tid] : -INFINITY;
+  __syncthreads();
+  set_bit<N>(id, 0, V, bits, tokens);
+  __syncthreads();
+  OthersPass<E, WAVES, H, GRAD> pass;
+  const Others others = pass.run(p, V, reinterpret_cast<const uint8_t*>(bits), s, lds);
+  const Row r = finish_row<WAVES>(t, V, others, id, mine, logq, tokens);
   put_row(kl, state, t, row, others.m, r);
   if constexpr (GRAD) {
     const float c = weights[row] * scale;
@@ -376,7 +396,7 @@ __global__ __launch_bounds__(64 * WAVES, 8) void distill_row_kernel(const E* x, 
     // the entries at the teacher's tokens, over what the vectors put there
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (tid < t.k && tokens.id[tid] >= 0) q[tokens.id[tid]] = Vec<E>::round(c * r.b);
+    if (id >= 0) q[id] = Vec<E>::round(c * r.b);
   }
 }
 
@@ -395,21 +415,23 @@ __global__ __launch_bounds__(256) void distill_piece_kernel(const E* __restrict_
   constexpr int N = Vec<E>::N, THREADS = 256;
   extern __shared__ uint4 dynamic[];
   __shared__ Tokens tokens;
-  __shared__ double lds_d[4];
-  __shared__ float lds_f[4];
+  __shared__ PassLds<4> lds;
   uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
   const int64_t row = blockIdx.x / (unsigned)splits;
   const int sp = (int)(blockIdx.x % (unsigned)splits);
   const int tid = threadIdx.x;
-  if (!load_ids<THREADS>(t, row, V, tokens)) return;
   const int lo = sp * piece;
   const int n = V - lo < piece ? V - lo : piece;
   const E* p = x + row * stride + lo;
-  if (tid < t.k && tokens.id[tid] >= lo && tokens.id[tid] - lo < n)
-    pieces.x[row * t.k + tid] = Vec<E>::value(p[tokens.id[tid] - lo]);
-  mark_tokens<N, THREADS>(t, tokens, lo, n, bits);
-  OthersPass<E, 4, 1> pass;
-  const Others others = pass.run(p, n, reinterpret_cast<const uint8_t*>(bits), s, lds_f, lds_d);
+  const int id = token_id(t, row, V);
+  clear_bits<N, THREADS>(n, bits, tokens);
+  if (!any_token(t, row, V)) return;
+  if (id >= lo && id - lo < n) pieces.x[row * t.k + tid] = Vec<E>::value(p[id - lo]);
+  __syncthreads();
+  set_bit<N>(id, lo, n, bits, tokens);
+  __syncthreads();
+  OthersPass<E, 4, 1, false> pass;
+  const Others others = pass.run(p, n, reinterpret_cast<const uint8_t*>(bits), s, lds);
   if (tid == 0) pieces.part[row * splits + sp] = others;
 }
 
@@ -419,12 +441,12 @@ __global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Te
   __shared__ Tokens tokens;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
-  if (!load_ids<256>(t, row, V, tokens)) return put_row(kl, state, t, row, 0.0f, Row{0.0, 0.0, 0.0f});
-  const bool on = tid < t.k && tokens.id[tid] >= 0;
-  const float mine = on ? pieces.x[row * t.k + tid] : 0.0f;
-  if (on)
-    for (int e = 0; e < tid; ++e)
-      if (tokens.id[e] == tokens.id[tid]) tokens.twice = 1;
+  const int id = token_id(t, row, V);
+  tokens.id[tid] = id;
+  if (tid == 0) tokens.twice = 0;
+  if (!any_token(t, row, V)) return put_row(kl, state, t, row, 0.0f, Row{0.0, 0.0, 0.0f});
+  const float mine = id >= 0 ? pieces.x[row * t.k + tid] : 0.0f;
+  const float logq = id >= 0 ? t.logp[row * t.k + tid] : -INFINITY;
   const Others v = lane < splits ? pieces.part[row * splits + lane] : Others{-INFINITY, 0.0};
   float m = v.s > 0.0 ? v.m : -INFINITY;
 #pragma unroll
@@ -432,7 +454,11 @@ __global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Te
   m = at_max(m);
   const Others all{m, wave_sum(v.s > 0.0 ? v.s * exp(((double)v.m - m) * t.inv_temperature) : v.s)};
   __syncthreads();
-  put_row(kl, state, t, row, m, finish_row<4>(t, row, V, all, mine, tokens));
+  if (id >= 0)
+    for (int e = 0; e < tid; ++e)
+      if (tokens.id[e] == id) tokens.twice = 1;
+  __syncthreads();
+  put_row(kl, state, t, row, m, finish_row<4>(t, V, all, id, mine, logq, tokens));
 }
 
 template <int WAVES>
@@ -520,14 +546,25 @@ static int piece_splits(int64_t T, int64_t V) {
   return static_cast<int>(splits > least ? splits : least > 1 ? least : 1);
 }
 
-// Whether one workgroup takes a whole row.
+// Whether one workgroup takes a whole row. A few long rows leave most of the
+// card idle so; in pieces they take three launches, and a second read of all.
+// us a step of k = 64, no row masked, by rows and in pieces:
+//   bfloat16  128256 columns: 1 row 27, 18; 96 rows 31, 30; 128 rows 32, 34; 256 rows 37, 50
+//            32000: 1 row 16.8, 20.4; 192 rows 17.4, 23.5
+//   float32   128256: 48 rows 32, 29; 96 rows 36, 40
+// and of the divergence alone: 96 rows 20.5, 18.5; 192 rows 21.4, 23.5.
 static bool by_rows(const lora_mat* x) {
-  return x->cols / vec_elems(x->dtype) < kMaxPieceVecs && (piece_splits(x->rows, x->cols) == 1 || x->rows >= 80);
+  if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;
+  return x->cols <= 49152 || x->rows >= (x->dtype == LORA_F32 ? 64 : 112);
 }
 
+// Waves to a row: with the gradient eight keep 8192 of its vectors in registers,
+// four 2560. 8192 x 128256 bfloat16, k = 64, a third of the rows masked: 690 us
+// with 8 waves, 726 with 16 (one vector kept per lane: more would spill), 728
+// with 4.
 static int row_waves(const lora_mat* x) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
-  return vecs <= 2560 ? 4 : vecs <= 6144 ? 8 : 16;
+  return vecs <= 2560 ? 4 : 8;
 }
 
 struct DistillPlan {
@@ -567,12 +604,8 @@ static void run_rows(const lora_mat* x, const lora_teacher* t, float* kl, float*
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
     const int waves = row_waves(x);
-    auto* kernel = dx == nullptr ? (waves == 4   ? distill_row_kernel<E, 4, false>
-                                    : waves == 8 ? distill_row_kernel<E, 8, false>
-                                                 : distill_row_kernel<E, 16, false>)
-                                 : (waves == 4   ? distill_row_kernel<E, 4, true>
-                                    : waves == 8 ? distill_row_kernel<E, 8, true>
-                                                 : distill_row_kernel<E, 16, true>);
+    auto* kernel = dx == nullptr ? (waves == 4 ? distill_row_kernel<E, 4, false> : distill_row_kernel<E, 8, false>)
+                                 : (waves == 4 ? distill_row_kernel<E, 4, true> : distill_row_kernel<E, 8, true>);
     launch(kernel, dim3(x->rows), dim3(64 * waves), bit_bytes(x->cols, Vec<E>::N), st, (const E*)x->ptr, x->stride_row,
            static_cast<int>(x->cols), teacher_of(t), exponent_of(t->temperature), kl, state, weights, scale,
            dx == nullptr ? (E*)nullptr : (E*)dx->ptr, dx == nullptr ? int64_t(0) : dx->stride_row);

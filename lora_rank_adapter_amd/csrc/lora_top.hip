@@ -190,10 +190,20 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
     __syncthreads();
     clear<THREADS>(l);
     __syncthreads();
+    // neighbours are often equal: a thread counts a run of them before it adds it
+    int run_bin = 0, run = 0;
     each([&](float f, int column, int) {
       const uint64_t e = entry_of(f, column);
-      if ((e & mask) == kth) atomicAdd(&l.hist[255 - (int)(e >> shift & 255)], 1);
+      if ((e & mask) != kth) return;
+      const int bin = 255 - (int)(e >> shift & 255);
+      if (bin != run_bin) {
+        if (run > 0) atomicAdd(&l.hist[run_bin], run);
+        run_bin = bin;
+        run = 0;
+      }
+      ++run;
     });
+    if (run > 0) atomicAdd(&l.hist[run_bin], run);
     __syncthreads();
     const int bin = kth_bin(l.hist, want);
     for (int i = 0; i < bin; ++i) want -= l.hist[i];
@@ -228,6 +238,7 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // ---------------------------------------------------------------------------
 
 constexpr int kHits = 1024;             // vectors in the list of a workgroup
+constexpr int kListed = 640;
 constexpr float kAbove = 64.0f;         // binary orders that a logit may be above the reference
 constexpr int kMaxPiece = 131072;       // elements of a row that one workgroup takes
 constexpr int kMaxSplits = 64;
@@ -245,14 +256,15 @@ __device__ __forceinline__ float tree(const float* f) {
     return tree<N / 2>(f) + tree<N / 2>(f + N / 2);
 }
 
-template <int N>
-__device__ __forceinline__ VecSums vec_sums(const float* f, float z, Exponent s) {
+// a(f) is the exponent of a logit.
+template <int N, class F>
+__device__ __forceinline__ VecSums vec_sums(const float* f, F a) {
   float e[N], w = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float a = s.of(f[i] - z);
-    e[i] = __builtin_amdgcn_exp2f(a);
-    w = fmaf(e[i], fmaxf(a, -256.0f), w);  // e is 0 there, and 0 times -inf is not
+    const float b = a(f[i]);
+    e[i] = __builtin_amdgcn_exp2f(b);
+    w = fmaf(e[i], fmaxf(b, -256.0f), w);  // e is 0 there, and 0 times -inf is not
   }
   return {tree<N>(e), w};
 }
@@ -357,6 +369,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
     low = fminf(low, wave_lo[v]);
   }
   const float z = at_max(hi);
+  // Two products instead of a difference and two: what `shift` lost to rounding moves all exponents alike, the largest
+  // logit's too. A reference below kFloor (or nearly that far up) would overflow here: such a piece is read again.
+  const float shift = -z * s.hi;
+  auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
   float reach = -INFINITY;  // vectors with an element from here on are listed: all of few
   if (vecs > 2 * k) {
     const Bins bins(hi, low);
@@ -374,17 +390,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
   VecSums held{0.0f, 0.0f};
   float held_m = -INFINITY;
   int held_at = -1;
+  auto list = [&](V4 v, int i) {
+    const int at = atomicAdd(&hits, 1);
+    if (at >= kHits) return;
+    hit[at] = make_uint4(v[0], v[1], v[2], v[3]);
+    hit_at[at] = i;
+  };
   auto take = [&](V4 v, int i) {
     float f[N];
     Vec<E>::unpack(v, f);
     const float m = vec_max<N>(f);
-    VecSums t = vec_sums<N>(f, z, s);
+    VecSums t = vec_sums<N>(f, exponent);
     if (m >= reach) {
-      const int at = atomicAdd(&hits, 1);
-      if (at < kHits) {
-        hit[at] = make_uint4(v[0], v[1], v[2], v[3]);
-        hit_at[at] = i;
-      }
+      list(v, i);
       if (m > held_m) {
         const VecSums before = held;
         held = t;
@@ -442,17 +460,42 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
         if (i * N + j < n) f(e[j], lo + i * N + j, -1);
     }
   };
+  if (hits > kHits) {
+    // too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on
+    const Bins bins(m, reach < kFloor ? kFloor : reach);
+    const int b = bins.of(held_m);
+    atomicAdd(&l.hist[b], 1);
+    __syncthreads();
+    const int last = kth_bin(l.hist, k);
+    if (tid == 0) {
+      hits = last < 255 ? 0 : kHits + 1;
+      l.low = 0xFFFFFFFFu;
+    }
+    __syncthreads();
+    if (b <= last) atomicMin(&l.low, order_of(held_m));
+    clear<THREADS>(l);
+    __syncthreads();
+    if (last < 255) {
+      reach = value_of(l.low);
+      for (int i = tid; i < vecs; i += THREADS) {
+        float f[N];
+        const V4 v = vec_at(p, i, n);
+        Vec<E>::unpack(v, f);
+        if (vec_max<N>(f) >= reach) list(v, i);
+      }
+    }
+    __syncthreads();
+  }
   bool found = hits <= kHits && select_top<THREADS>(listed, m, reach < kFloor ? kFloor : reach, kk, l);
   if (found && l.count < kk) found = false;
   if (!found) select_exactly<THREADS>(all, kk, l);
   const int top = column_of(l.sorted[0]) - lo, top_at = top / N;
   m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
 
-  // the sums over all but the largest, relative to `from`
-  float from = z;
-  const bool again = s.of(m - z) > kAbove || (m < kFloor && m != z && m > -INFINITY);
+  // the sums over all but the largest
+  const bool again = s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
+  auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
-    from = m;
     sum = wsum = 0.0;
     for (int i = tid; i < vecs; i += THREADS) {
       float f[N];
@@ -460,7 +503,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
 #pragma unroll
       for (int j = 0; j < N; ++j)
         if (i * N + j == top) f[j] = -INFINITY;
-      const VecSums t = vec_sums<N>(f, from, s);
+      const VecSums t = vec_sums<N>(f, from_m);
       sum += t.s;
       wsum += t.w;
     }
@@ -480,6 +523,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
       sum += wave_s[v];
       wsum += wave_w[v];
     }
+    double d = 0.0;  // the largest logit's exponent
     if (!again && m > -INFINITY) {
       float f[N];
       if (l.first >= 0) {
@@ -489,20 +533,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
       } else {
         Vec<E>::unpack(vec_at(p, top_at, n), f);
       }
-      if (m < reach) {  // not held: all logits are below kFloor, those equal to the largest count 1 and the others 0
-        const VecSums with = vec_sums<N>(f, from, s);
-        sum -= with.s;
-        wsum -= with.w;
-      }
 #pragma unroll
       for (int j = 0; j < N; ++j)
         if (top_at * N + j == top) f[j] = -INFINITY;
-      const VecSums others = vec_sums<N>(f, from, s);
+      const VecSums others = vec_sums<N>(f, exponent);
       sum += others.s;
       wsum += others.w;
+      d = (double)m * s.hi + ((double)m * s.lo + shift);
     }
-    const double d = ((double)m - from) * out.inv_temperature, one = exp(d);
-    shared = m > -INFINITY ? TopStats{m, sum / one, (sum * d - wsum * kLn2) / one} : TopStats{m, sum, 0.0};
+    const double one = exp2(d);
+    shared = m > -INFINITY ? TopStats{m, sum / one, (sum * d - wsum) * kLn2 / one} : TopStats{m, sum, 0.0};
   }
   __syncthreads();
   TopStats v = shared;
@@ -643,12 +683,13 @@ static int top_splits(int64_t T, int64_t V) {
 }
 
 // Waves of a workgroup, the fewest of 4, 8 and 16 with which a row of logits in
-// no particular order lists half of what there is room for: with G lanes the
+// no particular order lists kListed vectors at most (a count that varies by an
+// eighth, and kHits have room): with G lanes the
 // k-th largest of their first 32 elements each is reached by a share of
 // -log(1 - k / G) / 32.
 static int top_waves(int64_t piece, int k) {
   for (int waves = 4; waves < 16; waves *= 2)
-    if (k < 64 * waves && -std::log(1.0 - k / (64.0 * waves)) / 32.0 * piece <= kHits / 2) return waves;
+    if (k < 64 * waves && -std::log(1.0 - k / (64.0 * waves)) / 32.0 * piece <= kListed) return waves;
   return 16;
 }
 

@@ -237,10 +237,7 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // than k (a vocabulary masked down to a few tokens).
 // ---------------------------------------------------------------------------
 
-constexpr int kHits = 1024;             // vectors in the list of a workgroup
-constexpr int kListed = 640;
 constexpr float kAbove = 64.0f;         // binary orders that a logit may be above the reference
-constexpr int kMaxPiece = 131072;       // elements of a row that one workgroup takes
 constexpr int kMaxSplits = 64;
 
 // Sums of a vector's exponentials e = 2^a and of e a.
@@ -256,17 +253,31 @@ __device__ __forceinline__ float tree(const float* f) {
     return tree<N / 2>(f) + tree<N / 2>(f + N / 2);
 }
 
-// a(f) is the exponent of a logit.
-template <int N, class F>
-__device__ __forceinline__ VecSums vec_sums(const float* f, F a) {
-  float e[N], w = 0.0f;
+// a(f) is the exponent of a logit. 0 times -inf is not 0: a vector with such an
+// exponent (a logit of -inf) is summed once more without it, which costs less
+// than a bound on every exponent (8192 x 128256: 251 -> 238 us).
+template <class E, class F>
+__device__ __forceinline__ VecSums vec_sums(typename Vec<E>::type v, F a) {
+  constexpr int N = Vec<E>::N;
+  float f[N], w = 0.0f;
+  Vec<E>::unpack(v, f);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float b = a(f[i]);
-    e[i] = __builtin_amdgcn_exp2f(b);
-    w = fmaf(e[i], fmaxf(b, -256.0f), w);  // e is 0 there, and 0 times -inf is not
+    f[i] = __builtin_amdgcn_exp2f(b);
+    w = fmaf(f[i], b, w);
   }
-  return {tree<N>(e), w};
+  const float sum = tree<N>(f);
+  if (w != w) {
+    Vec<E>::unpack(v, f);
+    w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float b = a(f[i]);
+      w = fmaf(__builtin_amdgcn_exp2f(b), fmaxf(b, -256.0f), w);
+    }
+  }
+  return {sum, w};
 }
 
 // Vector i of n elements; -inf past the last.
@@ -306,15 +317,15 @@ struct TopParts {
   uint64_t* entries;  // [T][splits][k], 0 past the piece's elements
 };
 
-template <class E, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4) void top_kernel(const E* __restrict__ x, int64_t stride,
+template <class E, int WAVES, int HITS>
+__global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(const E* __restrict__ x, int64_t stride,
                                                             const int32_t* __restrict__ targets, int V, int splits,
                                                             int piece, Exponent s, TopOut out, TopParts parts) {
   constexpr int N = Vec<E>::N, U = 32 / N, THREADS = 64 * WAVES;
   using V4 = typename Vec<E>::type;
   __shared__ Select l;
-  __shared__ uint4 hit[kHits];
-  __shared__ int hit_at[kHits];
+  __shared__ uint4 hit[HITS];
+  __shared__ int hit_at[HITS];
   __shared__ int hits;
   __shared__ float wave_hi[WAVES], wave_lo[WAVES];
   __shared__ double wave_s[WAVES], wave_w[WAVES];
@@ -392,15 +403,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
   int held_at = -1;
   auto list = [&](V4 v, int i) {
     const int at = atomicAdd(&hits, 1);
-    if (at >= kHits) return;
+    if (at >= HITS) return;
     hit[at] = make_uint4(v[0], v[1], v[2], v[3]);
     hit_at[at] = i;
   };
-  auto take = [&](V4 v, int i) {
+  auto take = [&](V4 v, int i) -> VecSums {
     float f[N];
     Vec<E>::unpack(v, f);
     const float m = vec_max<N>(f);
-    VecSums t = vec_sums<N>(f, exponent);
+    VecSums t = vec_sums<E>(v, exponent);
     if (m >= reach) {
       list(v, i);
       if (m > held_m) {
@@ -411,25 +422,35 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
         held_at = i;
       }
     }
-    sum += t.s;
-    wsum += t.w;
+    return t;
+  };
+  // the sums of a lane's 32 elements are float32, those of all of them float64
+  VecSums part{0.0f, 0.0f};
+  auto add = [&](VecSums t) { part = {part.s + t.s, part.w + t.w}; };
+  auto flush = [&] {
+    sum += part.s;
+    wsum += part.w;
+    part = {0.0f, 0.0f};
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (tid + u * THREADS < vecs) take(w[u], tid + u * THREADS);
+    if (tid + u * THREADS < vecs) add(take(w[u], tid + u * THREADS));
+  flush();
   int base = U * THREADS;
   for (; base + U * THREADS <= whole; base += U * THREADS) {
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
 #pragma unroll
-    for (int u = 0; u < U; ++u) take(w[u], base + tid + u * THREADS);
+    for (int u = 0; u < U; ++u) add(take(w[u], base + tid + u * THREADS));
+    flush();
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (base + tid + u * THREADS < vecs) w[u] = vec_at(p, base + tid + u * THREADS, n);
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (base + tid + u * THREADS < vecs) take(w[u], base + tid + u * THREADS);
+    if (base + tid + u * THREADS < vecs) add(take(w[u], base + tid + u * THREADS));
+  flush();
 
   // the k largest
   float m = held_m;
@@ -460,7 +481,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
         if (i * N + j < n) f(e[j], lo + i * N + j, -1);
     }
   };
-  if (hits > kHits) {
+  if (hits > HITS) {
     // too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on
     const Bins bins(m, reach < kFloor ? kFloor : reach);
     const int b = bins.of(held_m);
@@ -468,7 +489,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
     __syncthreads();
     const int last = kth_bin(l.hist, k);
     if (tid == 0) {
-      hits = last < 255 ? 0 : kHits + 1;
+      hits = last < 255 ? 0 : HITS + 1;
       l.low = 0xFFFFFFFFu;
     }
     __syncthreads();
@@ -486,7 +507,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
     }
     __syncthreads();
   }
-  bool found = hits <= kHits && select_top<THREADS>(listed, m, reach < kFloor ? kFloor : reach, kk, l);
+  bool found = hits <= HITS && select_top<THREADS>(listed, m, reach < kFloor ? kFloor : reach, kk, l);
   if (found && l.count < kk) found = false;
   if (!found) select_exactly<THREADS>(all, kk, l);
   const int top = column_of(l.sorted[0]) - lo, top_at = top / N;
@@ -494,18 +515,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
 
   // the sums over all but the largest
   const bool again = s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
+  const LeftOut<E> without_top(top, vecs);
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
     sum = wsum = 0.0;
     for (int i = tid; i < vecs; i += THREADS) {
-      float f[N];
-      Vec<E>::unpack(vec_at(p, i, n), f);
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (i * N + j == top) f[j] = -INFINITY;
-      const VecSums t = vec_sums<N>(f, from_m);
-      sum += t.s;
-      wsum += t.w;
+      V4 h = vec_at(p, i, n);
+      without_top.template from<1>(&h, i, 1);
+      const VecSums v = vec_sums<E>(h, from_m);
+      sum += v.s;
+      wsum += v.w;
     }
   } else if (held_at != top_at) {
     sum += held.s;
@@ -525,18 +544,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 5 : sizeof(E) == 2 ? 8 : 4
     }
     double d = 0.0;  // the largest logit's exponent
     if (!again && m > -INFINITY) {
-      float f[N];
-      if (l.first >= 0) {
-        const uint4 h = hit[l.first];
-        const V4 v = {h.x, h.y, h.z, h.w};
-        Vec<E>::unpack(v, f);
-      } else {
-        Vec<E>::unpack(vec_at(p, top_at, n), f);
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (top_at * N + j == top) f[j] = -INFINITY;
-      const VecSums others = vec_sums<N>(f, exponent);
+      V4 h;
+      if (l.first >= 0)
+        h = V4{hit[l.first].x, hit[l.first].y, hit[l.first].z, hit[l.first].w};
+      else
+        h = vec_at(p, top_at, n);
+      without_top.template from<1>(&h, top_at, 1);
+      const VecSums others = vec_sums<E>(h, exponent);
       sum += others.s;
       wsum += others.w;
       d = (double)m * s.hi + ((double)m * s.lo + shift);
@@ -671,30 +685,41 @@ __global__ __launch_bounds__(kGradVecs) void top_grad_kernel(GradArgs<E> a, cons
 // host side
 // ---------------------------------------------------------------------------
 
-// Pieces of a row: about as many as give 1024 workgroups, of at least 4096
-// logits each and at most what one workgroup takes.
-static int top_splits(int64_t T, int64_t V) {
-  const int64_t rows = T < 1 ? 1 : T;
-  int64_t splits = (1024 + rows / 2) / rows;
-  const int64_t most = ceil_div(V, 4096), least = ceil_div(V, kMaxPiece);
-  splits = splits < most ? splits : most;
-  splits = splits < kMaxSplits ? splits : kMaxSplits;
-  return static_cast<int>(splits > least ? splits : least > 1 ? least : 1);
+// Workgroups of 4 or 8 waves with room for so many vectors in their list.
+struct TopShape {
+  int waves, hits;
+};
+constexpr TopShape kShapes[] = {{4, 256}, {4, 1024}, {8, 1024}};
+
+// Elements of a row in no particular order that list 5/8 of what there is room
+// for: with G lanes the k-th largest of their first 32 elements each is reached
+// by a share of -log(1 - k / G) / 32 of all. That varies by 1 / sqrt(k).
+static int64_t most_elements(const TopShape& v, int k) {
+  const double lanes = 64.0 * v.waves;
+  return k >= lanes ? 0 : static_cast<int64_t>(v.hits * (5.0 / 8) * 32.0 / -std::log(1.0 - (k < 1 ? 1 : k) / lanes));
 }
 
-// Waves of a workgroup, the fewest of 4, 8 and 16 with which a row of logits in
-// no particular order lists kListed vectors at most (a count that varies by an
-// eighth, and kHits have room): with G lanes the
-// k-th largest of their first 32 elements each is reached by a share of
-// -log(1 - k / G) / 32.
-static int top_waves(int64_t piece, int k) {
-  for (int waves = 4; waves < 16; waves *= 2)
-    if (k < 64 * waves && -std::log(1.0 - k / (64.0 * waves)) / 32.0 * piece <= kListed) return waves;
-  return 16;
+// The smallest shape that a piece's list fits.
+static TopShape top_shape(int64_t piece, int k) {
+  for (const TopShape& v : kShapes)
+    if (piece <= most_elements(v, k)) return v;
+  return kShapes[2];
+}
+
+// Pieces of a row: about as many as give 1024 workgroups, of at least 4096
+// logits each and at most what a list has room for.
+static int64_t top_splits(int64_t T, int64_t V, int k) {
+  const int64_t rows = T < 1 ? 1 : T;
+  int64_t splits = (1024 + rows / 2) / rows;
+  const int64_t most = ceil_div(V, 4096), least = ceil_div(V, most_elements(kShapes[2], k));
+  splits = splits < most ? splits : most;
+  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  return splits > least ? splits : least > 1 ? least : 1;
 }
 
 struct TopPlan {
-  int splits, piece, waves;
+  int splits, piece;
+  TopShape shape;
   bool fits;  // one launch
   TopParts parts;
   size_t bytes;
@@ -702,10 +727,11 @@ struct TopPlan {
 
 static TopPlan plan_top(int64_t T, int64_t V, int64_t k, void* ws) {
   TopPlan l{};
-  l.splits = top_splits(T, V);
+  const int64_t splits = top_splits(T, V, static_cast<int>(k));
+  l.splits = static_cast<int>(splits);
   l.piece = static_cast<int>(round_up(ceil_div(V, l.splits), 8));
-  l.waves = top_waves(l.piece, static_cast<int>(k));
-  l.fits = T * l.splits <= max_blocks(64 * l.waves);
+  l.shape = top_shape(l.piece, static_cast<int>(k));
+  l.fits = splits <= kMaxSplits && T * splits <= max_blocks(64 * l.shape.waves);
   Carver w(ws);
   const int64_t pieces = l.splits > 1 ? T * l.splits : 0;
   l.parts.stats = static_cast<TopPiece*>(w.take(pieces * sizeof(TopPiece)));
@@ -714,7 +740,7 @@ static TopPlan plan_top(int64_t T, int64_t V, int64_t k, void* ws) {
   return l;
 }
 
-constexpr int64_t kMaxVocab = int64_t(kMaxSplits) * kMaxPiece;
+constexpr int64_t kMaxVocab = int64_t(1) << 22;  // 64 pieces hold it for any k
 
 }  // namespace lora
 
@@ -745,8 +771,10 @@ extern "C" int lora_token_top(const lora_mat* logits, const int32_t* targets, in
   auto st = static_cast<hipStream_t>(stream);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    auto* kernel = l.waves == 4 ? top_kernel<E, 4> : l.waves == 8 ? top_kernel<E, 8> : top_kernel<E, 16>;
-    launch(kernel, dim3(T * l.splits), dim3(64 * l.waves), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
+    auto* kernel = l.shape.hits == 256    ? top_kernel<E, 4, 256>
+                   : l.shape.waves == 4 ? top_kernel<E, 4, 1024>
+                                        : top_kernel<E, 8, 1024>;
+    launch(kernel, dim3(T * l.splits), dim3(64 * l.shape.waves), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
            static_cast<int>(V), l.splits, l.piece, exponent_of(temperature), out, l.parts);
     if (l.splits > 1)
       launch(top_join_kernel<E>, dim3(T), dim3(256), 0, st, (const E*)logits->ptr, logits->stride_row, targets,

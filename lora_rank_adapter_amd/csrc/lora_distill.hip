@@ -70,12 +70,7 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
   bool first = on;
   if (on && k.twice)
     for (int e = 0; e < tid; ++e) first = first && k.id[e] != id;
-  float top = on ? x : -INFINITY, likely = logq;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    top = fmaxf(top, __shfl_xor(top, d, 64));
-    likely = fmaxf(likely, __shfl_xor(likely, d, 64));
-  }
+  float top = lane_max(on ? x : -INFINITY), likely = lane_max(logq);
   if ((tid & 63) == 0) {
     most[0][wave] = top;
     most[1][wave] = likely;
@@ -94,8 +89,8 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
     if (!t.rest) lq -= likely;
     if (first) p = exp(lp);
     if (on) z = exp(lq);
-    const double p_sum = wave_sum(p), z_sum = wave_sum(z);
-    tokens = wave_sum(tokens);
+    const double p_sum = lane_total(p), z_sum = lane_total(z);
+    tokens = lane_total(tokens);
     if ((tid & 63) == 0) {
       sums[0][wave] = p_sum;
       sums[1][wave] = z_sum;
@@ -121,7 +116,7 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
   lp -= log(total);
   if (wave * 64 < t.k) {
     if (k.twice && tid < t.k) k.q[tid] = q;
-    const double part = wave_sum(on && q != 0.0 ? q * (lq - lp) : 0.0);
+    const double part = lane_total(on && q != 0.0 ? q * (lq - lp) : 0.0);
     if ((tid & 63) == 0) sums[3][wave] = part;
   }
   __syncthreads();
@@ -196,8 +191,7 @@ __device__ __forceinline__ float sum_exp(const float* f, float z, Exponent s) {
 // The largest of the workgroup's v; lds is used once.
 template <int WAVES>
 __device__ __forceinline__ float block_max(float v, float* lds) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  v = lane_max(v);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
 #pragma unroll
@@ -302,7 +296,7 @@ struct OthersPass {
       sum = left ? __builtin_amdgcn_exp2f(s.of(last - z)) : 0.0;
       for (int i = tid; i < vecs; i += THREADS) take(load(p + (int64_t)i * N), i);
     }
-    sum = wave_sum(sum);
+    sum = lane_total(sum);
     if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;
     __syncthreads();
     sum = 0.0;
@@ -448,11 +442,8 @@ __global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Te
   const float mine = id >= 0 ? pieces.x[row * t.k + tid] : 0.0f;
   const float logq = id >= 0 ? t.logp[row * t.k + tid] : -INFINITY;
   const Others v = lane < splits ? pieces.part[row * splits + lane] : Others{-INFINITY, 0.0};
-  float m = v.s > 0.0 ? v.m : -INFINITY;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  m = at_max(m);
-  const Others all{m, wave_sum(v.s > 0.0 ? v.s * exp(((double)v.m - m) * t.inv_temperature) : v.s)};
+  const float m = at_max(lane_max(v.s > 0.0 ? v.m : -INFINITY));
+  const Others all{m, lane_total(v.s > 0.0 ? v.s * exp(((double)v.m - m) * t.inv_temperature) : v.s)};
   __syncthreads();
   if (id >= 0)
     for (int e = 0; e < tid; ++e)

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "lora_host.hpp"
 #include "lora_rows.hpp"
@@ -11,6 +12,51 @@
 namespace lora {
 
 __device__ __forceinline__ float at_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Reductions over a wave in registers (DPP: four shifts within a row of 16
+// lanes, then the last lane of a row, and of two rows, to the rows after it),
+// which take a fraction of the time of shuffles through LDS. f(a, b) joins two
+// values; `none` changes nothing. Lane i gets the lanes 0 to i joined.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_move(int none, int v) {
+  return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xF, false);
+}
+template <class F>
+__device__ __forceinline__ int lane_scan(int v, int none, F f) {
+  v = f(v, dpp_move<0x111, 0xF>(none, v));
+  v = f(v, dpp_move<0x112, 0xF>(none, v));
+  v = f(v, dpp_move<0x114, 0xF>(none, v));
+  v = f(v, dpp_move<0x118, 0xF>(none, v));
+  v = f(v, dpp_move<0x142, 0xA>(none, v));
+  return f(v, dpp_move<0x143, 0xC>(none, v));
+}
+__device__ __forceinline__ float lane_max(float v) {
+  const int all = lane_scan(__float_as_int(v), __float_as_int(-INFINITY),
+                            [](int a, int b) { return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b))); });
+  return __int_as_float(__builtin_amdgcn_readlane(all, 63));
+}
+__device__ __forceinline__ float lane_min(float v) { return -lane_max(-v); }
+__device__ __forceinline__ int lane_sums(int v) {
+  return lane_scan(v, 0, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ double lane_total(double v) {
+  auto step = [&](auto ctrl, auto rows) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const int lo = dpp_move<ctrl(), rows()>(0, (int)u), hi = dpp_move<ctrl(), rows()>(0, (int)(u >> 32));
+    v += __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+  };
+  using std::integral_constant;
+  const integral_constant<int, 0xF> every;
+  step(integral_constant<int, 0x111>(), every);
+  step(integral_constant<int, 0x112>(), every);
+  step(integral_constant<int, 0x114>(), every);
+  step(integral_constant<int, 0x118>(), every);
+  step(integral_constant<int, 0x142>(), integral_constant<int, 0xA>());
+  step(integral_constant<int, 0x143>(), integral_constant<int, 0xC>());
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = __builtin_amdgcn_readlane((int)u, 63), hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
 
 // log2(e) / temperature as a float32 below it and the rest, which is above 0:
 // the exponent of 2 of exp(d / temperature) is d hi + d lo, -inf for d = -inf.

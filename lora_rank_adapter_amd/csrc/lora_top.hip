@@ -122,12 +122,7 @@ __device__ __forceinline__ int kth_bin(const int* hist, int k) {
   int c[4], sum = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) sum += c[j] = hist[4 * lane + j];
-  int upto = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int other = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += other;
-  }
+  const int upto = lane_sums(sum);
   const uint64_t reached = __ballot(upto >= k);
   if (reached == 0) return 255;
   int before = upto - sum, bin = 4 * lane;
@@ -136,7 +131,7 @@ __device__ __forceinline__ int kth_bin(const int* hist, int k) {
     before += c[j];
     if (before < k) ++bin;
   }
-  return __shfl(bin, __builtin_ctzll(reached), 64);
+  return __builtin_amdgcn_readlane(bin, __builtin_ctzll(reached));
 }
 
 template <int THREADS>
@@ -151,6 +146,7 @@ __device__ __forceinline__ void sort_list(Select& l, int n, int k) {
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint64_t e = l.list[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += l.list[j] > e;
     if (rank < k) l.sorted[rank] = e;
     if (rank == 0) l.first = l.from[i];
@@ -363,12 +359,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     Vec<E>::unpack(w[u], f);
     mine = fmaxf(mine, vec_max<N>(f));
   }
-  float hi = mine, low = mine >= kFloor ? mine : INFINITY;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    hi = fmaxf(hi, __shfl_xor(hi, d, 64));
-    low = fminf(low, __shfl_xor(low, d, 64));
-  }
+  float hi = lane_max(mine), low = lane_min(mine >= kFloor ? mine : INFINITY);
   if ((tid & 63) == 0) {
     wave_hi[tid >> 6] = hi;
     wave_lo[tid >> 6] = low;
@@ -440,6 +431,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   for (; base + U * THREADS <= whole; base += U * THREADS) {
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
+    sched_fence();
 #pragma unroll
     for (int u = 0; u < U; ++u) add(take(w[u], base + tid + u * THREADS));
     flush();
@@ -453,9 +445,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   flush();
 
   // the k largest
-  float m = held_m;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  float m = lane_max(held_m);
   if ((tid & 63) == 0) wave_hi[tid >> 6] = m;
   clear<THREADS>(l);
   __syncthreads();
@@ -530,8 +520,8 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     sum += held.s;
     wsum += held.w;
   }
-  sum = wave_sum(sum);
-  wsum = wave_sum(wsum);
+  sum = lane_total(sum);
+  wsum = lane_total(wsum);
   if ((tid & 63) == 0) {
     wave_s[tid >> 6] = sum;
     wave_w[tid >> 6] = wsum;
@@ -594,18 +584,14 @@ __global__ __launch_bounds__(256) void top_join_kernel(const E* __restrict__ x, 
     const TopStats v = on ? TopStats{piece->m, piece->r, piece->gap} : TopStats{-INFINITY, 0.0, 0.0};
     // what the piece's k-th largest reaches, k entries of the row do
     const uint64_t last = on ? entries[tid * k + k - 1] : 0;
-    float m = v.m, lo = last != 0 ? value_of(static_cast<uint32_t>(last >> 32)) : -INFINITY;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      m = fmaxf(m, __shfl_xor(m, d, 64));
-      lo = fmaxf(lo, __shfl_xor(lo, d, 64));
-    }
+    const float m = lane_max(v.m);
+    const float lo = lane_max(last != 0 ? value_of(static_cast<uint32_t>(last >> 32)) : -INFINITY);
     const uint64_t top = __ballot(v.m == m);
     const bool holds = top != 0 && tid == __builtin_ctzll(top);  // the largest logit, whose 1 is not in r
     const double d = ((double)m - v.m) * out.inv_temperature;
     const double f = holds ? 1.0 : v.m > -INFINITY ? exp(-d) : 0.0;
-    const double r = wave_sum(holds ? v.r : f * (1.0 + v.r));
-    const double gap = wave_sum(f > 0.0 ? f * (v.gap + (holds ? 0.0 : d * (1.0 + v.r))) : 0.0);
+    const double r = lane_total(holds ? v.r : f * (1.0 + v.r));
+    const double gap = lane_total(f > 0.0 ? f * (v.gap + (holds ? 0.0 : d * (1.0 + v.r))) : 0.0);
     if (tid == 0) {
       shared = {m, r, gap / (1.0 + r)};
       shared_lo = lo;
@@ -699,11 +685,13 @@ static int64_t most_elements(const TopShape& v, int k) {
   return k >= lanes ? 0 : static_cast<int64_t>(v.hits * (5.0 / 8) * 32.0 / -std::log(1.0 - (k < 1 ? 1 : k) / lanes));
 }
 
-// The smallest shape that a piece's list fits.
+// The smallest shape that a piece's list fits; a long piece that lists more than
+// 256 has room for takes 8 waves, which list half as many: 2048 x 128256
+// bfloat16, k = 20, 97 us with 8 waves and 106 with 4; 8192 x 32000, k = 64, 168
+// and 147.
 static TopShape top_shape(int64_t piece, int k) {
-  for (const TopShape& v : kShapes)
-    if (piece <= most_elements(v, k)) return v;
-  return kShapes[2];
+  if (piece <= most_elements(kShapes[0], k)) return kShapes[0];
+  return piece <= most_elements(kShapes[1], k) && piece <= 65536 ? kShapes[1] : kShapes[2];
 }
 
 // Pieces of a row: about as many as give 1024 workgroups, of at least 4096

@@ -694,14 +694,20 @@ static TopShape top_shape(int64_t piece, int k) {
   return piece <= most_elements(kShapes[1], k) && piece <= 65536 ? kShapes[1] : kShapes[2];
 }
 
-// Pieces of a row: about as many as give 1024 workgroups, of at least 4096
-// logits each and at most what a list has room for.
+// Pieces of a row: one, or of few long rows about as many as give 1024
+// workgroups, of at least 8192 logits each; at most what a list has room for. us
+// a call in one piece and in such pieces, bfloat16:
+//   128256 columns: 1 row, k = 5, 21.3 and 16.9; 128 rows, k = 20, 22.6 and 20.4; 256 rows 23.5 and 25.9
+//   32000: 64 rows 14.8 and 16.1
 static int64_t top_splits(int64_t T, int64_t V, int k) {
-  const int64_t rows = T < 1 ? 1 : T;
-  int64_t splits = (1024 + rows / 2) / rows;
-  const int64_t most = ceil_div(V, 4096), least = ceil_div(V, most_elements(kShapes[2], k));
-  splits = splits < most ? splits : most;
-  splits = splits < kMaxSplits ? splits : kMaxSplits;
+  const int64_t least = ceil_div(V, most_elements(kShapes[2], k));
+  int64_t splits = 1;
+  if (V > 49152 && T < 192) {
+    const int64_t rows = T < 1 ? 1 : T, most = ceil_div(V, 8192);
+    splits = (1024 + rows / 2) / rows;
+    splits = splits < most ? splits : most;
+    splits = splits < kMaxSplits ? splits : kMaxSplits;
+  }
   return splits > least ? splits : least > 1 ? least : 1;
 }
 

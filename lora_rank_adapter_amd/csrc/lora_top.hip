@@ -428,20 +428,28 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     if (tid + u * THREADS < vecs) add(take(w[u], tid + u * THREADS));
   flush();
   int base = U * THREADS;
-  for (; base + U * THREADS <= whole; base += U * THREADS) {
+  // four vectors at a time, the next four on their way
+  constexpr int B = 4;
+  V4 a[B];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
+  for (int u = 0; u < B; ++u)
+    if (base + tid + u * THREADS < whole) a[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
+  for (; base + B * THREADS <= whole; base += B * THREADS) {
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      w[u] = a[u];
+      if (base + tid + (u + B) * THREADS < whole)
+        a[u] = vload_nt(p + (int64_t)(base + tid + (u + B) * THREADS) * N);
+    }
     sched_fence();
 #pragma unroll
-    for (int u = 0; u < U; ++u) add(take(w[u], base + tid + u * THREADS));
+    for (int u = 0; u < B; ++u) add(take(w[u], base + tid + u * THREADS));
     flush();
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (base + tid + u * THREADS < vecs) w[u] = vec_at(p, base + tid + u * THREADS, n);
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (base + tid + u * THREADS < vecs) add(take(w[u], base + tid + u * THREADS));
+  for (int u = 0; u < B; ++u)
+    if (base + tid + u * THREADS < whole) add(take(a[u], base + tid + u * THREADS));
+  if (U * THREADS < vecs && whole < vecs && tid == 0) add(take(vec_at(p, whole, n), whole));  // the last one, in part
   flush();
 
   // the k largest

@@ -276,13 +276,34 @@ struct OthersPass {
       for (int u = 0; u < U; ++u)
         if (tid + u * THREADS < body) take(w[u], tid + u * THREADS);
       int i = tid + U * THREADS;
-      for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
+      if constexpr (AGAIN) {
+        for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = load(p + (int64_t)(i + u * THREADS) * N);
+          for (int u = 0; u < U; ++u) w[u] = load(p + (int64_t)(i + u * THREADS) * N);
 #pragma unroll
-        for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+          for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+        }
+        for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), i);
+      } else {
+        // the next four vectors on their way; with the held ones beside them that would spill
+        V4 a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i + u * THREADS < body) a[u] = load(p + (int64_t)(i + u * THREADS) * N);
+        for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            w[u] = a[u];
+            if (i + (u + U) * THREADS < body) a[u] = load(p + (int64_t)(i + (u + U) * THREADS) * N);
+          }
+          sched_fence();
+#pragma unroll
+          for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i + u * THREADS < body) take(a[u], i + u * THREADS);
       }
-      for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), i);
 #pragma unroll
       for (int h = 0; h < H; ++h)
         if (body + tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(body + tid + h * THREADS) * N);
@@ -321,7 +342,7 @@ __device__ __forceinline__ void put_row(float* kl, float* state, const Teacher& 
 // for which the row's last H vectors per lane stay in registers and the others
 // are read again, the most recently read first.
 template <class E, int WAVES, bool GRAD>
-__global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : 8) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
+__global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : sizeof(E) == 2 ? 6 : 5) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
                                                                     Exponent s, float* __restrict__ kl,
                                                                     float* __restrict__ state,
                                                                     const float* __restrict__ weights, float scale,

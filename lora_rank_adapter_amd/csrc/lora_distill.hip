@@ -262,10 +262,10 @@ struct OthersPass {
     const float first = m;
     float z = at_max(m);
     double sum = 0.0;
-    auto take = [&](V4 v, int i) {
+    auto take = [&](V4 v, uint32_t off) {
       float f[N];
       Vec<E>::unpack(v, f);
-      leave_out<E>(f, byte[i]);
+      leave_out<E>(f, off);
 #pragma unroll
       for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
       sum += sum_exp<N>(f, z, s);
@@ -274,35 +274,41 @@ struct OthersPass {
     if (body > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (tid + u * THREADS < body) take(w[u], tid + u * THREADS);
+        if (tid + u * THREADS < body) take(w[u], byte[tid + u * THREADS]);
       int i = tid + U * THREADS;
+      uint32_t off[U];  // the vectors' bits, read before the first is used
       if constexpr (AGAIN) {
         for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) w[u] = load(p + (int64_t)(i + u * THREADS) * N);
+          for (int u = 0; u < U; ++u) {
+            w[u] = load(p + (int64_t)(i + u * THREADS) * N);
+            off[u] = byte[i + u * THREADS];
+          }
 #pragma unroll
-          for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+          for (int u = 0; u < U; ++u) take(w[u], off[u]);
         }
-        for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), i);
+        for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
       } else {
-        // the next four vectors on their way; with the held ones beside them that would spill
+        // The next four vectors on their way; with the held ones beside them that would spill. Loads past the last
+        // vector take it once more: behind a condition each would be waited for at once.
         V4 a[U];
+        auto next = [&](int j) { return load(p + (int64_t)(j < body ? j : body - 1) * N); };
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (i + u * THREADS < body) a[u] = load(p + (int64_t)(i + u * THREADS) * N);
+        for (int u = 0; u < U; ++u) a[u] = next(i + u * THREADS);
         for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             w[u] = a[u];
-            if (i + (u + U) * THREADS < body) a[u] = load(p + (int64_t)(i + (u + U) * THREADS) * N);
+            off[u] = byte[i + u * THREADS];
+            a[u] = next(i + (u + U) * THREADS);
           }
           sched_fence();
 #pragma unroll
-          for (int u = 0; u < U; ++u) take(w[u], i + u * THREADS);
+          for (int u = 0; u < U; ++u) take(w[u], off[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (i + u * THREADS < body) take(a[u], i + u * THREADS);
+          if (i + u * THREADS < body) take(a[u], byte[i + u * THREADS]);
       }
 #pragma unroll
       for (int h = 0; h < H; ++h)
@@ -310,12 +316,12 @@ struct OthersPass {
     }
 #pragma unroll
     for (int h = 0; h < H; ++h)
-      if (body + tid + h * THREADS < vecs) take(held[h], body + tid + h * THREADS);
+      if (body + tid + h * THREADS < vecs) take(held[h], byte[body + tid + h * THREADS]);
     m = block_max<WAVES>(m, lds.most);
     if (s.of(m - z) > kAbove || (first == -INFINITY && m > -INFINITY)) {
       z = m;
       sum = left ? __builtin_amdgcn_exp2f(s.of(last - z)) : 0.0;
-      for (int i = tid; i < vecs; i += THREADS) take(load(p + (int64_t)i * N), i);
+      for (int i = tid; i < vecs; i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
     }
     sum = lane_total(sum);
     if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;

@@ -428,18 +428,20 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     if (tid + u * THREADS < vecs) add(take(w[u], tid + u * THREADS));
   flush();
   int base = U * THREADS;
-  // four vectors at a time, the next four on their way
+  // Four vectors at a time, the next four on their way. Loads past the last vector take it once more: behind a
+  // condition each would be waited for at once.
   constexpr int B = 4;
   V4 a[B];
+  auto next = [&](int i) { return vload_nt(p + (int64_t)(i < whole ? i : whole - 1) * N); };
+  if (base < whole) {
 #pragma unroll
-  for (int u = 0; u < B; ++u)
-    if (base + tid + u * THREADS < whole) a[u] = vload_nt(p + (int64_t)(base + tid + u * THREADS) * N);
+    for (int u = 0; u < B; ++u) a[u] = next(base + tid + u * THREADS);
+  }
   for (; base + B * THREADS <= whole; base += B * THREADS) {
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       w[u] = a[u];
-      if (base + tid + (u + B) * THREADS < whole)
-        a[u] = vload_nt(p + (int64_t)(base + tid + (u + B) * THREADS) * N);
+      a[u] = next(base + tid + (u + B) * THREADS);
     }
     sched_fence();
 #pragma unroll

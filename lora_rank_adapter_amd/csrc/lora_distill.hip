@@ -240,19 +240,23 @@ struct OthersPass {
       for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
     };
     V4 w[U];
+    // Loads past the last vector take it once more: behind a condition each would be waited for at once.
+    auto before = [](int i, int end) { return (int64_t)(i < end ? i : end - 1) * N; };
+    auto hold = [&] {
+#pragma unroll
+      for (int h = 0; h < H; ++h) held[h] = vload_nt(p + before(body + tid + h * THREADS, vecs));
+    };
     last = rest < n ? Vec<E>::value(p[rest]) : -INFINITY;
     const bool left = rest < n && !(byte[vecs] >> tid & 1u);
     if (body > 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (tid + u * THREADS < body) w[u] = load(p + (int64_t)(tid + u * THREADS) * N);
+        w[u] = load(p + before(tid + u * THREADS, body));
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (tid + u * THREADS < body) largest(w[u], tid + u * THREADS);
-    } else {
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(tid + h * THREADS) * N);
+    } else if (vecs > 0) {
+      hold();
 #pragma unroll
       for (int h = 0; h < H; ++h)
         if (tid + h * THREADS < vecs) largest(held[h], tid + h * THREADS);
@@ -289,18 +293,16 @@ struct OthersPass {
         }
         for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
       } else {
-        // The next four vectors on their way; with the held ones beside them that would spill. Loads past the last
-        // vector take it once more: behind a condition each would be waited for at once.
+        // the next four vectors on their way; with the held ones beside them that would spill
         V4 a[U];
-        auto next = [&](int j) { return load(p + (int64_t)(j < body ? j : body - 1) * N); };
 #pragma unroll
-        for (int u = 0; u < U; ++u) a[u] = next(i + u * THREADS);
+        for (int u = 0; u < U; ++u) a[u] = load(p + before(i + u * THREADS, body));
         for (; i + (U - 1) * THREADS < body; i += U * THREADS) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             w[u] = a[u];
             off[u] = byte[i + u * THREADS];
-            a[u] = next(i + (u + U) * THREADS);
+            a[u] = load(p + before(i + (u + U) * THREADS, body));
           }
           sched_fence();
 #pragma unroll
@@ -310,9 +312,7 @@ struct OthersPass {
         for (int u = 0; u < U; ++u)
           if (i + u * THREADS < body) take(a[u], byte[i + u * THREADS]);
       }
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (body + tid + h * THREADS < vecs) held[h] = vload_nt(p + (int64_t)(body + tid + h * THREADS) * N);
+      hold();
     }
 #pragma unroll
     for (int h = 0; h < H; ++h)

@@ -342,9 +342,13 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   const int k = out.k < 1 ? 1 : out.k;  // the largest one is needed in any case
   const int kk = k < n ? k : n;
 
+  // Loads past the last vector take it once more: behind a condition each would be waited for at once.
+  auto next = [&](int i) { return vload_nt(p + (int64_t)(i < whole ? i : whole - 1) * N); };
   V4 w[U];
+  if (whole > 0) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = vec_at(p, tid + u * THREADS < vecs ? tid + u * THREADS : vecs, n);
+    for (int u = 0; u < U; ++u) w[u] = next(tid + u * THREADS);
+  }
   if (tid == 0) {
     hits = 0;
     l.low = 0xFFFFFFFFu;
@@ -353,12 +357,16 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   }
   clear<THREADS>(l);
   float mine = -INFINITY;  // the lane's largest
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
+  auto largest = [&](V4 v) {
     float f[N];
-    Vec<E>::unpack(w[u], f);
+    Vec<E>::unpack(v, f);
     mine = fmaxf(mine, vec_max<N>(f));
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid + u * THREADS < whole) largest(w[u]);
+  const bool part_of_one = tid == 0 && whole < vecs;  // the last vector, in part
+  if (part_of_one) largest(vec_at(p, whole, n));
   float hi = lane_max(mine), low = lane_min(mine >= kFloor ? mine : INFINITY);
   if ((tid & 63) == 0) {
     wave_hi[tid >> 6] = hi;
@@ -425,14 +433,13 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (tid + u * THREADS < vecs) add(take(w[u], tid + u * THREADS));
+    if (tid + u * THREADS < whole) add(take(w[u], tid + u * THREADS));
+  if (part_of_one) add(take(vec_at(p, whole, n), whole));
   flush();
   int base = U * THREADS;
-  // Four vectors at a time, the next four on their way. Loads past the last vector take it once more: behind a
-  // condition each would be waited for at once.
+  // four vectors at a time, the next four on their way
   constexpr int B = 4;
   V4 a[B];
-  auto next = [&](int i) { return vload_nt(p + (int64_t)(i < whole ? i : whole - 1) * N); };
   if (base < whole) {
 #pragma unroll
     for (int u = 0; u < B; ++u) a[u] = next(base + tid + u * THREADS);
@@ -451,7 +458,6 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
 #pragma unroll
   for (int u = 0; u < B; ++u)
     if (base + tid + u * THREADS < whole) add(take(a[u], base + tid + u * THREADS));
-  if (U * THREADS < vecs && whole < vecs && tid == 0) add(take(vec_at(p, whole, n), whole));  // the last one, in part
   flush();
 
   // the k largest

@@ -28,6 +28,12 @@ Ops (the addressing arrays are passed as the tensors of lora_addressing):
   pref_loss(logp, seq_offsets, ref_logp, beta, label_smoothing) -> (loss, seq_logp, coef)
   policy_loss(logp, targets, vocab, old_logp, advantages, weights, clip_low, clip_high, ref_logp, kl_coef)
     -> (loss, coef)                                         (both losses differentiable in logp)
+  token_top(logits, targets, k, temperature) -> (logp, entropy, top_ids, top_logp, stats)
+                                                            (logp and entropy differentiable in logits; targets may be
+                                                            None, logp is empty then)
+  token_top_grad(logits, targets, stats, dlogp, dentropy, temperature) -> dlogits
+  distill_kl(logits, top_ids, top_logp, temperature, rest) -> (kl, state)   (kl differentiable in logits)
+  distill_grad(logits, top_ids, state, coef, temperature) -> dlogits
 
 h from shrink and gather_shrink is zero where the op leaves it unspecified
 (inactive tokens, columns past a slot's rank), and sorted_tokens from
@@ -35,9 +41,9 @@ addressing is -1 past the active tokens, so every output is fully defined. lora_
 weights in nn.Linear layout (A_w r x K, B_w L x r); its backward casts the
 incoming float32 gradient to x's dtype for the backward kernels (which take dy
 in the input dtype) and returns gradients in the dtypes and layouts of x, A_w
-and B_w. The losses' other outputs (stats, seq_logp, coef) have no gradient, nor have
-the losses for their other inputs (ref_logp, old_logp, advantages, weights): asking
-for one raises.
+and B_w. The losses' other outputs (stats, seq_logp, coef, top_logp, state) have no
+gradient, nor have the losses for their other inputs (ref_logp, old_logp, advantages,
+weights, a teacher's top_logp): asking for one raises.
 """
 from __future__ import annotations
 
@@ -351,3 +357,95 @@ def _policy_backward(ctx, grad, *others):
 
 torch.library.register_autograd(f"{_NS}::pref_loss", _pref_backward, setup_context=_loss_setup)
 torch.library.register_autograd(f"{_NS}::policy_loss", _policy_backward, setup_context=_loss_setup)
+
+
+@torch.library.custom_op(f"{_NS}::token_top", mutates_args=(), device_types="cuda")
+def token_top(logits: torch.Tensor, targets: torch.Tensor | None, k: int, temperature: float
+              ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    logp, *others = train.lora_token_top(logits, targets, k, temperature)
+    return logits.new_empty(0, dtype=torch.float32) if logp is None else logp, *others
+
+
+@token_top.register_fake
+def _(logits, targets, k, temperature):
+    T = logits.shape[0]
+
+    def f32(*shape):
+        return logits.new_empty(shape, dtype=torch.float32)
+
+    return (f32(0 if targets is None else T), f32(T), logits.new_empty((T, k), dtype=torch.int32), f32(T, k),
+            f32(T, 3))
+
+
+@torch.library.custom_op(f"{_NS}::token_top_grad", mutates_args=(), device_types="cuda")
+def token_top_grad(logits: torch.Tensor, targets: torch.Tensor | None, stats: torch.Tensor,
+                   dlogp: torch.Tensor | None, dentropy: torch.Tensor | None, temperature: float) -> torch.Tensor:
+    return train.lora_token_top_grad(logits, targets, stats, dlogp, dentropy, temperature)
+
+
+@token_top_grad.register_fake
+def _(logits, targets, stats, dlogp, dentropy, temperature):
+    return logits.new_empty(logits.shape)
+
+
+def _top_setup(ctx, inputs, output):
+    logits, targets, _, ctx.temperature = inputs
+    # a copy of stats: what a caller writes over them does not matter here
+    ctx.save_for_backward(logits, targets, output[4].clone())
+    ctx.set_materialize_grads(False)
+
+
+def _top_backward(ctx, dlogp, dentropy, dids, dtop, dstats):
+    _no_grad("what token_top returns beside logp and entropy", dids, dtop, dstats)
+    logits, targets, stats = ctx.saved_tensors
+    if targets is None:
+        dlogp = None
+    if dlogp is None and dentropy is None:
+        return None, None, None, None
+    dlogp, dentropy = (None if g is None else g.contiguous() for g in (dlogp, dentropy))
+    return (torch.ops.lora_amd.token_top_grad(logits, targets, stats, dlogp, dentropy, ctx.temperature), None, None,
+            None)
+
+
+torch.library.register_autograd(f"{_NS}::token_top", _top_backward, setup_context=_top_setup)
+
+
+@torch.library.custom_op(f"{_NS}::distill_kl", mutates_args=(), device_types="cuda")
+def distill_kl(logits: torch.Tensor, top_ids: torch.Tensor, top_logp: torch.Tensor, temperature: float,
+               rest: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    return train.lora_distill_kl(logits, top_ids, top_logp, temperature, rest)
+
+
+@distill_kl.register_fake
+def _(logits, top_ids, top_logp, temperature, rest):
+    T, k = top_ids.shape
+    return logits.new_empty(T, dtype=torch.float32), logits.new_empty((T, k + 2), dtype=torch.float32)
+
+
+@torch.library.custom_op(f"{_NS}::distill_grad", mutates_args=(), device_types="cuda")
+def distill_grad(logits: torch.Tensor, top_ids: torch.Tensor, state: torch.Tensor, coef: torch.Tensor,
+                 temperature: float) -> torch.Tensor:
+    return train.lora_distill_grad(logits, top_ids, state, coef, temperature)
+
+
+@distill_grad.register_fake
+def _(logits, top_ids, state, coef, temperature):
+    return logits.new_empty(logits.shape)
+
+
+def _distill_setup(ctx, inputs, output):
+    logits, top_ids, _, ctx.temperature, _ = inputs
+    ctx.save_for_backward(logits, top_ids, output[1].clone())
+    ctx.set_materialize_grads(False)
+
+
+def _distill_backward(ctx, grad, dstate):
+    _constants(ctx, {2: "a teacher's top_logp"})
+    _no_grad("distill_kl's state", dstate)
+    if grad is None:
+        return (None,) * 5
+    logits, top_ids, state = ctx.saved_tensors
+    return (torch.ops.lora_amd.distill_grad(logits, top_ids, state, grad.contiguous(), ctx.temperature),) + (None,) * 4
+
+
+torch.library.register_autograd(f"{_NS}::distill_kl", _distill_backward, setup_context=_distill_setup)

@@ -37,6 +37,14 @@ def _queue(device: torch.device):
     return _stream(device)
 
 
+def _here(device: torch.device):
+    """_queue for tensors on the current device, which is where a launch goes."""
+    queue = _queue(device)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    return queue
+
+
 def _capturing(stream) -> bool:
     """Whether a graph is being captured on torch's current stream, `stream` (the default stream cannot be)."""
     return stream.value is not None and torch.cuda.is_current_stream_capturing()
@@ -266,7 +274,7 @@ def lora_token_top(logits: torch.Tensor, targets: torch.Tensor | None = None, k:
     ws, nbytes = _given(workspace, lib.lora_token_top_workspace_bytes(T, V, k), dev)
     check("lora_token_top", lib.lora_token_top(
         _matrix("logits", logits, dev), y, k, float(temperature), None if logp is None else logp.data_ptr(),
-        entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes, _queue(dev)))
+        entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes, _here(dev)))
     return logp, entropy, ids, top, stats
 
 
@@ -285,7 +293,7 @@ def lora_token_top_grad(logits: torch.Tensor, targets: torch.Tensor | None, stat
         _matrix("logits", logits, dev), None if targets is None else _vector("targets", targets, T, _I32, dev),
         _vector("stats", stats, 3 * T, _F32, dev), None if dlogp is None else _vector("dlogp", dlogp, T, _F32, dev),
         None if dentropy is None else _vector("dentropy", dentropy, T, _F32, dev), float(temperature),
-        _matrix("dlogits", dlogits, dev), _queue(dev)))
+        _matrix("dlogits", dlogits, dev), _here(dev)))
     return dlogits
 
 
@@ -317,7 +325,7 @@ def lora_distill_kl(logits: torch.Tensor, top_ids: torch.Tensor, top_logp: torch
     state = torch.empty((T, k + 2), dtype=_F32, device=dev)
     ws, nbytes = _given(workspace, lib.lora_distill_workspace_bytes(T, V, k), dev)
     check("lora_distill_kl", lib.lora_distill_kl(_matrix("logits", logits, dev), teacher, kl.data_ptr(),
-                                                 state.data_ptr(), ws.data_ptr(), nbytes, _queue(dev)))
+                                                 state.data_ptr(), ws.data_ptr(), nbytes, _here(dev)))
     return kl, state
 
 
@@ -339,7 +347,7 @@ def lora_distill_grad(logits: torch.Tensor, top_ids: torch.Tensor, state: torch.
         _matrix("logits", logits, dev), _vector("top_ids", top_ids, T * k, _I32, dev), k,
         _vector("state", state, T * (k + 2), _F32, dev), _vector("coef", coef, T, _F32, dev),
         None if grad_out is None else _vector("grad_out", grad_out, 1, _F32, dev), float(scale), float(temperature),
-        _matrix("dlogits", dlogits, dev), _queue(dev)))
+        _matrix("dlogits", dlogits, dev), _here(dev)))
     return dlogits
 
 
@@ -360,7 +368,7 @@ def lora_distill_step(logits: torch.Tensor, top_ids: torch.Tensor, top_logp: tor
     ws, nbytes = _given(workspace, lib.lora_distill_workspace_bytes(T, V, k), dev)
     check("lora_distill_step", lib.lora_distill_step(
         _matrix("logits", logits, dev), teacher, _vector("weights", weights, T, _F32, dev), float(grad_scale),
-        loss.data_ptr(), kl.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _queue(dev)))
+        loss.data_ptr(), kl.data_ptr(), _matrix("dlogits", dlogits, dev), ws.data_ptr(), nbytes, _here(dev)))
     return loss, kl, dlogits
 
 

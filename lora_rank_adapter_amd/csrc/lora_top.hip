@@ -228,9 +228,13 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // elements, which a row's largest one exceeds by little: no running maximum.
 //
 // Where that does not hold the row is read again: for the sums if a logit is 64
-// binary orders above the reference, for the alternatives if the list
-// overflows (logits that rise along the row, ties without end) or holds fewer
-// than k (a vocabulary masked down to a few tokens).
+// binary orders above the reference; for the alternatives if the list overflows
+// (logits that rise along the row, a masked beginning: from the k-th of the
+// lanes' largest in the whole row on) or holds fewer than k (ties without end, a
+// vocabulary masked down to a few tokens: the lowest columns of the next value).
+// us a call of 256 rows of 128256 bfloat16, k = 20: random logits 22.6, rising
+// 40, one value throughout 64, masked down to 5 tokens 41, masked in their first
+// half 34.
 // ---------------------------------------------------------------------------
 
 constexpr float kAbove = 64.0f;         // binary orders that a logit may be above the reference
@@ -314,9 +318,9 @@ struct TopParts {
 };
 
 template <class E, int WAVES, int HITS>
-__global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(const E* __restrict__ x, int64_t stride,
-                                                            const int32_t* __restrict__ targets, int V, int splits,
-                                                            int piece, Exponent s, TopOut out, TopParts parts) {
+__global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(
+    const E* __restrict__ x, int64_t stride, const int32_t* __restrict__ targets, int V, int splits, int piece,
+    Exponent s, TopOut out, TopParts parts) {
   constexpr int N = Vec<E>::N, U = 32 / N, THREADS = 64 * WAVES;
   using V4 = typename Vec<E>::type;
   __shared__ Select l;
@@ -351,7 +355,6 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   }
   if (tid == 0) {
     hits = 0;
-    l.low = 0xFFFFFFFFu;
     l.first = -1;  // of a row without elements
     l.sorted[0] = 0;
   }
@@ -367,33 +370,39 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     if (tid + u * THREADS < whole) largest(w[u]);
   const bool part_of_one = tid == 0 && whole < vecs;  // the last vector, in part
   if (part_of_one) largest(vec_at(p, whole, n));
-  float hi = lane_max(mine), low = lane_min(mine >= kFloor ? mine : INFINITY);
-  if ((tid & 63) == 0) {
-    wave_hi[tid >> 6] = hi;
-    wave_lo[tid >> 6] = low;
-  }
-  __syncthreads();
+  // A value that the k-th largest of the lanes' reaches; kFloor if fewer than k reach that. hi and low are the largest
+  // and the smallest from kFloor on. Starts from a cleared l.
+  float hi, low;
+  auto kth_lane = [&](float v) {
+    hi = lane_max(v);
+    low = lane_min(v >= kFloor ? v : INFINITY);
+    if ((tid & 63) == 0) {
+      wave_hi[tid >> 6] = hi;
+      wave_lo[tid >> 6] = low;
+    }
+    if (tid == 0) l.low = 0xFFFFFFFFu;
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < WAVES; ++v) {
-    hi = fmaxf(hi, wave_hi[v]);
-    low = fminf(low, wave_lo[v]);
-  }
+    for (int w = 0; w < WAVES; ++w) {
+      hi = fmaxf(hi, wave_hi[w]);
+      low = fminf(low, wave_lo[w]);
+    }
+    const int b = Bins(hi, low).of(v);
+    atomicAdd(&l.hist[b], 1);
+    __syncthreads();
+    const int last = kth_bin(l.hist, k);
+    if (b <= last) atomicMin(&l.low, order_of(v));
+    __syncthreads();
+    return last < 255 ? value_of(l.low) : kFloor;
+  };
+  // vectors with an element from here on are listed: all of few
+  float reach = kth_lane(mine);
+  if (vecs <= 2 * k) reach = -INFINITY;
   const float z = at_max(hi);
   // Two products instead of a difference and two: what `shift` lost to rounding moves all exponents alike, the largest
   // logit's too. A reference below kFloor (or nearly that far up) would overflow here: such a piece is read again.
   const float shift = -z * s.hi;
   auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
-  float reach = -INFINITY;  // vectors with an element from here on are listed: all of few
-  if (vecs > 2 * k) {
-    const Bins bins(hi, low);
-    const int b = bins.of(mine);
-    atomicAdd(&l.hist[b], 1);
-    __syncthreads();
-    const int last = kth_bin(l.hist, k);
-    if (b <= last) atomicMin(&l.low, order_of(mine));
-    __syncthreads();
-    reach = last < 255 ? value_of(l.low) : kFloor;
-  }
 
   // a lane keeps the sums of the listed vector that holds its largest logit apart
   double sum = 0.0, wsum = 0.0;
@@ -460,13 +469,46 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     if (base + tid + u * THREADS < whole) add(take(a[u], base + tid + u * THREADS));
   flush();
 
+  // f(vector, its index) once more for the whole piece
+  auto scan = [&](auto f) {
+    for (int i = tid; i - tid < whole; i += B * THREADS) {
+#pragma unroll
+      for (int u = 0; u < B; ++u) w[u] = next(i + u * THREADS);
+      sched_fence();
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        if (i + u * THREADS < whole) f(w[u], i + u * THREADS);
+    }
+    if (part_of_one) f(vec_at(p, whole, n), whole);
+  };
+  auto all = [&](auto f) {
+    scan([&](V4 v, int i) {
+      float e[N];
+      Vec<E>::unpack(v, e);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i * N + j < n) f(e[j], lo + i * N + j, -1);
+    });
+  };
+
   // the k largest
-  float m = lane_max(held_m);
-  if ((tid & 63) == 0) wave_hi[tid >> 6] = m;
   clear<THREADS>(l);
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
+  for (int turn = 0; turn < 2 && hits > HITS; ++turn) {
+    // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on;
+    // if that is a value that many have, from the next one on.
+    reach = turn == 0 ? kth_lane(held_m) : value_of(order_of(reach) + 1);
+    clear<THREADS>(l);
+    __syncthreads();
+    if (tid == 0) hits = 0;
+    __syncthreads();
+    scan([&](V4 v, int i) {
+      float f[N];
+      Vec<E>::unpack(v, f);
+      if (vec_max<N>(f) >= reach) list(v, i);
+    });
+    __syncthreads();
+  }
   auto listed = [&](auto f) {
     for (int i = tid; i < hits; i += THREADS) {
       const uint4 h = hit[i];
@@ -478,46 +520,61 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
         if (e[j] >= reach && hit_at[i] * N + j < n) f(e[j], lo + hit_at[i] * N + j, i);
     }
   };
-  auto all = [&](auto f) {
-    for (int i = tid; i < vecs; i += THREADS) {
+  bool found = hits <= HITS;
+  if (found) {
+    const float most = lane_max(held_m);
+    if ((tid & 63) == 0) wave_hi[tid >> 6] = most;
+    __syncthreads();
+    float m = most;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
+    found = select_top<THREADS>(listed, m, reach > kFloor ? reach : low, kk, l);
+  }
+  // Fewer than k from `reach` on, in order: what comes below, value by value (after a mask mostly one), the lowest columns
+  // of a value first.
+  int have = found ? l.count : 0;
+  for (int turn = 0; found && have < kk; ++turn) {
+    found = turn < 2;
+    if (!found) break;
+    float below = -INFINITY;
+    bool some = false;
+    all([&](float f, int, int) {
+      if (!(f < reach)) return;
+      below = fmaxf(below, f);
+      some = true;
+    });
+    below = lane_max(below);
+    __syncthreads();
+    if ((tid & 63) == 0) wave_hi[tid >> 6] = below;
+    if (!__syncthreads_or(some)) break;  // NaNs: the row has no probabilities
+    for (int v = 0; v < WAVES; ++v) below = fmaxf(below, wave_hi[v]);
+    reach = below;
+    for (int i0 = 0; i0 < vecs && have < kk; i0 += THREADS) {
       float e[N];
-      Vec<E>::unpack(vec_at(p, i, n), e);
+      Vec<E>::unpack(vec_at(p, i0 + tid < vecs ? i0 + tid : vecs, n), e);
+      int mine_too = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) mine_too += e[j] == below && (i0 + tid) * N + j < n;
+      const int upto = lane_sums(mine_too);
+      if ((tid & 63) == 63) l.from[tid >> 6] = upto;
+      __syncthreads();
+      int at = have + upto - mine_too;
+      for (int v = 0; v < WAVES; ++v) {
+        at += v < (tid >> 6) ? l.from[v] : 0;
+        have += l.from[v];
+      }
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (i * N + j < n) f(e[j], lo + i * N + j, -1);
+        if (e[j] == below && (i0 + tid) * N + j < n && at < kk) l.sorted[at++] = entry_of(below, lo + (i0 + tid) * N + j);
+      __syncthreads();
     }
-  };
-  if (hits > HITS) {
-    // too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on
-    const Bins bins(m, reach < kFloor ? kFloor : reach);
-    const int b = bins.of(held_m);
-    atomicAdd(&l.hist[b], 1);
-    __syncthreads();
-    const int last = kth_bin(l.hist, k);
-    if (tid == 0) {
-      hits = last < 255 ? 0 : HITS + 1;
-      l.low = 0xFFFFFFFFu;
-    }
-    __syncthreads();
-    if (b <= last) atomicMin(&l.low, order_of(held_m));
-    clear<THREADS>(l);
-    __syncthreads();
-    if (last < 255) {
-      reach = value_of(l.low);
-      for (int i = tid; i < vecs; i += THREADS) {
-        float f[N];
-        const V4 v = vec_at(p, i, n);
-        Vec<E>::unpack(v, f);
-        if (vec_max<N>(f) >= reach) list(v, i);
-      }
-    }
-    __syncthreads();
   }
-  bool found = hits <= HITS && select_top<THREADS>(listed, m, reach < kFloor ? kFloor : reach, kk, l);
-  if (found && l.count < kk) found = false;
-  if (!found) select_exactly<THREADS>(all, kk, l);
+  if (!found) {
+    select_exactly<THREADS>(all, kk, l);
+    have = kk;
+  }
   const int top = column_of(l.sorted[0]) - lo, top_at = top / N;
-  m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
+  const float m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
 
   // the sums over all but the largest
   const bool again = s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
@@ -525,13 +582,11 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
     sum = wsum = 0.0;
-    for (int i = tid; i < vecs; i += THREADS) {
-      V4 h = vec_at(p, i, n);
-      without_top.template from<1>(&h, i, 1);
-      const VecSums v = vec_sums<E>(h, from_m);
-      sum += v.s;
-      wsum += v.w;
-    }
+    scan([&](V4 v, int i) {
+      without_top.template from<1>(&v, i, 1);
+      add(vec_sums<E>(v, from_m));
+      flush();
+    });
   } else if (held_at != top_at) {
     sum += held.s;
     wsum += held.w;
@@ -569,11 +624,11 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   if (splits > 1) {
     const int64_t at = row * splits + sp;
     if (tid == 0) parts.stats[at] = {v.r, v.gap, v.m};
-    if (tid < k) parts.entries[at * k + tid] = tid < kk ? l.sorted[tid] : 0;
+    if (tid < k) parts.entries[at * k + tid] = tid < have ? l.sorted[tid] : 0;
     return;
   }
   v.gap /= 1.0 + v.r;
-  put_row(out, row, v, target, target ? Vec<E>::value(x[row * stride + y]) : 0.0f, l.sorted, kk);
+  put_row(out, row, v, target, target ? Vec<E>::value(x[row * stride + y]) : 0.0f, l.sorted, have);
 }
 
 // The pieces of a row: their statistics by one wave, the k largest of their

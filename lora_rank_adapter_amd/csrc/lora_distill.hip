@@ -60,7 +60,9 @@ struct Row {
 
 // A row's divergence and gradient factors from the others' sum, by all threads
 // of a workgroup: thread i has the teacher's i-th token `id`, with the row's
-// logit x there and the teacher's log probability. Entries that name a token twice count both, the token once.
+// logit x there and the teacher's log probability. Entries that name a token
+// twice count both, the token once. Logarithms are taken of sums, not of
+// probabilities, which may be too small for float64.
 template <int WAVES>
 __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int id, float x, float logq, Tokens& k) {
   __shared__ float most[2][WAVES];
@@ -98,7 +100,8 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
     }
   }
   __syncthreads();
-  const double others = o.s > 0.0 ? o.s * exp(((double)o.m - top) * t.inv_temperature) : o.s;
+  const double below = ((double)o.m - top) * t.inv_temperature;
+  const double others = o.s > 0.0 ? o.s * exp(below) : o.s;
   double total = others, all = 0.0, named = 0.0;
   for (int w = 0; w * 64 < t.k; ++w) {
     total += sums[0][w];
@@ -113,7 +116,8 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
     lq -= log(all);
     all = all == all ? 1.0 : all;
   }
-  lp -= log(total);
+  const double log_total = log(total);
+  lp -= log_total;
   if (wave * 64 < t.k) {
     if (k.twice && tid < t.k) k.q[tid] = q;
     const double part = lane_total(on && q != 0.0 ? q * (lq - lp) : 0.0);
@@ -126,7 +130,7 @@ __device__ __forceinline__ Row finish_row(const Teacher& t, int V, Others o, int
   double q_rest = 0.0;
   if (t.rest && named < V) {
     q_rest = all < 1.0 ? 1.0 - all : all == all ? 0.0 : all;
-    if (q_rest != 0.0) kl += q_rest * (log(q_rest) - log(p_rest));
+    if (q_rest != 0.0) kl += q_rest * (log(q_rest) - (o.s > 0.0 ? log(o.s) + below - log_total : log(p_rest)));
     all += q_rest;
   }
   double a = o.s == 0.0 ? 0.0 : (all * p_rest - q_rest) / o.s;  // 0: the others hold nothing
@@ -348,12 +352,12 @@ __device__ __forceinline__ void put_row(float* kl, float* state, const Teacher& 
 // for which the row's last H vectors per lane stay in registers and the others
 // are read again, the most recently read first.
 template <class E, int WAVES, bool GRAD>
-__global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : sizeof(E) == 2 ? 6 : 5) void distill_row_kernel(const E* x, int64_t stride, int V, Teacher t,
-                                                                    Exponent s, float* __restrict__ kl,
-                                                                    float* __restrict__ state,
-                                                                    const float* __restrict__ weights, float scale,
-                                                                    E* dx, int64_t dx_stride) {
-  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES, H = !GRAD ? 1 : WAVES == 4 ? 10 : 16;
+__global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : sizeof(E) == 2 ? 6 : 5) void distill_row_kernel(
+    const E* x, int64_t stride, int V, Teacher t, Exponent s, float* __restrict__ kl, float* __restrict__ state,
+    const float* __restrict__ weights, float scale, E* dx, int64_t dx_stride) {
+  // as many vectors as 128 registers leave room for, four waves' share of a row that they hold whole
+  constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
+  constexpr int H = !GRAD ? 1 : WAVES == 4 ? 10 : sizeof(E) == 2 ? 15 : 16;
   using V4 = typename Vec<E>::type;
   extern __shared__ uint4 dynamic[];
   __shared__ Tokens tokens;
@@ -567,19 +571,20 @@ static int piece_splits(int64_t T, int64_t V) {
 // Whether one workgroup takes a whole row. A few long rows leave most of the
 // card idle so; in pieces they take three launches, and a second read of all.
 // us a step of k = 64, no row masked, by rows and in pieces:
-//   bfloat16  128256 columns: 1 row 27, 18; 96 rows 31, 30; 128 rows 32, 34; 256 rows 37, 50
-//            32000: 1 row 16.8, 20.4; 192 rows 17.4, 23.5
-//   float32   128256: 48 rows 32, 29; 96 rows 36, 40
-// and of the divergence alone: 96 rows 20.5, 18.5; 192 rows 21.4, 23.5.
+//   bfloat16  128256 columns: 1 row 27, 18; 96 rows 30.6, 29.2; 128 rows 31.1, 32.6; 256 rows 36, 50
+//            45000: 1 row 16.6, 18.2; 60000: 48 rows 21.2, 19.2; 32000: 192 rows 17.4, 23.5
+//   float32   128256: 48 rows 31, 29; 64 rows 32.4, 32.3; 96 rows 35, 41
+// and of the divergence alone: bfloat16 64 rows 16.9, 15.4; 96 rows 17.0, 17.6.
 static bool by_rows(const lora_mat* x) {
   if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;
   return x->cols <= 49152 || x->rows >= (x->dtype == LORA_F32 ? 64 : 112);
 }
 
-// Waves to a row: with the gradient eight keep 8192 of its vectors in registers,
-// four 2560. 8192 x 128256 bfloat16, k = 64, a third of the rows masked: 690 us
-// with 8 waves, 726 with 16 (one vector kept per lane: more would spill), 728
-// with 4.
+// Waves to a row: with the gradient eight keep 7680 of its vectors in registers
+// (8192 of float32), four 2560. 8192 x 128256 bfloat16, k = 64, a third of the
+// rows masked: 690 us with 8 waves, 727 with 16 (which leave registers for one
+// vector per lane) and 728 with 4. Of these 690 the second read takes 24, the
+// exponentials of the second pass 20; the rest is 3.6 GB at 5.5 TB/s.
 static int row_waves(const lora_mat* x) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
   return vecs <= 2560 ? 4 : 8;

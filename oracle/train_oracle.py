@@ -159,17 +159,21 @@ def token_top(logits, targets, k, tau):
 
 
 def token_top_grad(logits, targets, dlogp, dentropy, tau):
+    """Through log p + entropy = d + gap and 1 - p = -expm1(log p), which do not cancel beside a likely token."""
     x = _f64(logits)
-    _, entropy, _, _, _ = token_top(x, targets, 0, tau)
-    p = softmax(x / tau)
+    g, h = _f64(dlogp), _f64(dentropy)
+    logp, _, _, _, stats = token_top(x, targets, 0, tau)
+    m, r, gap = (stats[:, i:i + 1] for i in range(3))
     with np.errstate(all="ignore"):
-        out = -_f64(dentropy)[:, None] * np.where(p > 0, p * (np.log(p) + entropy[:, None]), 0 * p)
-    out -= _f64(dlogp)[:, None] * p
-    if targets is not None:
-        y, off = np.asarray(targets), masked(targets, x.shape[1])
-        live = np.flatnonzero(~off)
-        out[live, y[live]] += _f64(dlogp)[live]
-        out[off] = 0.0
+        d = (x - m) / tau
+        p = np.exp(d) / (1 + r)
+        by_entropy = np.where(p > 0, -h[:, None] * p * (d + gap), 0 * p)
+        out = by_entropy - g[:, None] * p
+        if targets is not None:
+            y, off = np.asarray(targets), masked(targets, x.shape[1])
+            live = np.flatnonzero(~off)
+            out[live, y[live]] = by_entropy[live, y[live]] - g[live] * np.expm1(logp[live])
+            out[off] = 0.0
     return out / tau
 
 

@@ -15,11 +15,15 @@ carried between them:
     err(gap) <= sum p_j (u_j e_j + 3 H (u_j + reach)) + gap err(r) / (1 + r) + H gap
     err(logp) <= err(log1p(r)) + 2 H |logp|
     err(entropy) <= err(log1p(r)) + err(gap) + H entropy
-The gradient takes r and gap in float32 (3 H more for the factor made of them):
-    tau err(dx_j) <= p_j f_j (|g| + |h| |gap - u_j|) + |h| p_j (err(gap) + 6 H (gap + u_j))
+Each of the V exponentials may be 0 below 2^-126, where u is below 256, as may
+what is made of them below 2^-126: V 2^-126 more for r, V 2^-118 for gap.
+The gradient takes r and gap in float32 (3 H more for the factor made of them);
+at the target 1 - p comes from log p:
+    tau err(dx_j) <= p_j f_j (|g| [j != y] + |h| |gap - u_j|) + |h| p_j (err(gap) + 6 H (gap + u_j))
                      + [j = y] |g| (6 H (1 - p) + p (err(log1p(r)) + 3 H u_y + 4 H |logp|))
     with f_j = 3 H u_j + 2^-23 + 8 H + err(r) / (1 + r)
-and half a step of the output's type, and 1e-37 for flushed denormals."""
+and half a step of the output's type. An exponential below 2^-126 may be 0: it
+counts (|g| + |h| |gap - u_j|) / tau times, and so may an output below 2^-126."""
 import numpy as np
 import pytest
 import torch
@@ -70,9 +74,11 @@ def errors(x64, tau):
     e = 3 * H * (u + reach(x64, tau)[:, None]) + 2.0 ** -23 + 16 * H
     others = w.copy()
     others[np.arange(len(u)), x64.argmax(1)] = 0.0
-    err_r = ((others * e).sum(1) + H * others.sum(1)) / total
+    V = x64.shape[1]
+    err_r = ((others * e).sum(1) + H * others.sum(1) + V * 2.0 ** -126) / total
     gap = (p * u).sum(1)
     err_gap = (p * (u * e + 3 * H * (u + reach(x64, tau)[:, None]) * (u > 0))).sum(1) + gap * err_r + H * gap
+    err_gap += V * 2.0 ** -118
     return u, p, err_r, err_gap
 
 
@@ -102,26 +108,26 @@ def check(x, y, k, tau, out):
     close(f64(out[4])[:, 2], stats[:, 2], live * e_gap, "gap")
 
 
-def grad_bounds(x64, y, g, h, tau):
+def check_grad(dx, x64, y, g, h, tau, dtype, what=""):
     u, p, e_r, e_gap = errors(x64, tau)
     gap = (p * u).sum(1, keepdims=True)
+    want = O.token_top_grad(x64, y, g, h, tau)
+    logp = O.token_top(x64, y, 0, tau)[0]
     g, h = np.abs(g)[:, None], np.abs(h)[:, None]
     f = 3 * H * u + 2.0 ** -23 + 8 * H + e_r[:, None]
-    tol = p * f * (g + h * np.abs(gap - u)) + h * p * (e_gap[:, None] + 6 * H * (gap + u))
+    by_logp = p * f * g
+    lost = 2.0 ** -126 * ((g + h * np.abs(gap - u)) / tau + 1)
     if y is not None:
-        live = np.flatnonzero(~O.masked(y, x64.shape[1]))
-        at = (live, y[live])
-        lp = np.log(p[at])
-        tol[at] += g[live, 0] * (6 * H * (1 - p[at]) + p[at] * (e_r[live] + 3 * H * u[at] + 4 * H * np.abs(lp)))
-    return tol / tau
-
-
-def check_grad(dx, x64, y, g, h, tau, dtype, what=""):
-    want = O.token_top_grad(x64, y, g, h, tau)
-    tol = grad_bounds(x64, y, g, h, tau)
+        off = O.masked(y, x64.shape[1])
+        live = np.flatnonzero(~off)
+        at, lp = (live, y[live]), logp[live]
+        lp = np.where(np.isfinite(lp), lp, 0.0)
+        by_logp[at] = g[live, 0] * (-6 * H * np.expm1(logp[live]) + p[at] * (e_r[live] + 3 * H * u[at] + 4 * H * np.abs(lp)))
+        lost[off] = 0.0
+    tol = (by_logp + p * f * h * np.abs(gap - u) + h * p * (e_gap[:, None] + 6 * H * (gap + u))) / tau
     if y is not None:
-        tol[O.masked(y, x64.shape[1])] = 0.0
-    tol = np.where(tol > 0, tol + 1e-37, 0.0)
+        tol[off] = 0.0
+    tol = np.where(np.isfinite(x64) & ((g > 0) | (h > 0)), tol + lost, 0.0)
     close(f64(dx), want, tol + torch.finfo(dtype).eps / 2 * (np.abs(want) + tol), what)
 
 

@@ -169,3 +169,24 @@ def test_gradients_of_shared_rows():
     g = torch.randn(6, device=DEV)
     dx = L.lora_token_top_grad(wide.contiguous(), y, out[4], g, g, 1.0)
     check_grad(dx, f64(wide), y.cpu().numpy(), f64(g), f64(g), 1.0, F)
+
+
+@pytest.mark.parametrize("tau", [1e-6, 0.01, 60.0, 1e6])
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T,V", [(6, 3000), (5, 50001), (195, 70001)])
+def test_temperatures(dtype, T, V, tau):
+    note(f"temperatures {dtype} {T} {V} {tau}")
+    k = 12
+    x, y = make(T, V, dtype, 7)
+    out = L.lora_token_top(x, y, k, tau)
+    at = torch.tensor([0, 1, 2, T - 1], device=DEV)
+    check(x[at], y[at], k, tau, tuple(t[at] for t in out))
+    g = torch.randn(T, device=DEV)
+    dx = L.lora_token_top_grad(x, y, out[4], g, g, tau)
+    check_grad(dx[at], f64(x[at]), y[at].cpu().numpy(), f64(g[at]), f64(g[at]), tau, dtype)
+    x, ids, logp = make_teacher(T, V, k, dtype, tau, 9)
+    for rest in (True, False):
+        want, e_kl, wx, ex = bounds(f64(x[at]), ids[at].cpu().numpy(), f64(logp[at]), tau, rest, f64(g[at]), dtype)
+        _, kl, dx = L.lora_distill_step(x, ids, logp, g, tau, rest)
+        close(f64(kl[at]), want, e_kl, "kl")
+        close(f64(dx[at]), wx, ex, "dx")

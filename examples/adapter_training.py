@@ -4,11 +4,13 @@ One step runs the library's operators as a training loop would: the embedding
 lookup, a linear layer with its adapter, the loss on the next token's logits
 with their gradient, the adapter's backward, the table's gradient and one
 AdamW step over all three weights. The frozen projections around them are
-torch products. Two vocabularies of tokens answer the prompts; the loss learns
-to prefer the first.
+torch products. Two vocabularies of tokens answer the prompts; the preference
+and the policy loss learn to prefer the first, distillation learns the top
+tokens of a teacher, a model with other weights.
 
     python examples/adapter_training.py --loss pref --steps 40
     python examples/adapter_training.py --loss policy --state-bits 8
+    python examples/adapter_training.py --loss distill
 """
 import argparse
 import os
@@ -100,6 +102,17 @@ class AdapterTrainer:
         self.opt.step()
         return loss
 
+    def top(self, ids, targets, k, temperature):
+        """What a student is given of this model: its k top tokens of each unmasked place at a temperature."""
+        return L.lora_token_top(self.logits(ids)[1], targets, k, temperature)[2:4]
+
+    def distill_step(self, ids, top_ids, top_logp, weights, temperature):
+        x, logits = self.logits(ids)
+        loss, _, dlogits = L.lora_distill_step(logits, top_ids, top_logp, weights, temperature, dlogits=logits)
+        self.backward(ids, x, dlogits)
+        self.opt.step()
+        return loss
+
 
 def sequence_sums(logp, offsets):
     o = offsets.tolist()
@@ -128,17 +141,32 @@ def train(loss="pref", steps=40, state_bits=32, pairs=6, length=40, vocab=1000, 
     return torch.stack(losses).tolist(), (gain[:, 0] - gain[:, 1]).tolist()
 
 
+def distill(steps=40, state_bits=32, pairs=6, length=40, vocab=1000, width=256, rank=8, k=16, temperature=2.0, seed=0):
+    """A student learns from a teacher that differs from it in the table and the adapter. Returns the losses."""
+    t = AdapterTrainer(vocab, width, rank, state_bits=state_bits, seed=seed)
+    teacher = AdapterTrainer(vocab, width, rank, seed=seed + 1)
+    teacher.base, teacher.head = t.base, t.head
+    ids, targets, _ = make_batch(pairs, length, vocab, "cuda", seed)
+    top_ids, top_logp = teacher.top(ids, targets, k, temperature)
+    weights = torch.full((len(ids),), temperature ** 2 / int((targets >= 0).sum()), device="cuda")
+    return torch.stack([t.distill_step(ids, top_ids, top_logp, weights, temperature) for _ in range(steps)]).tolist()
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--loss", choices=("pref", "policy"), default="pref")
+    ap.add_argument("--loss", choices=("pref", "policy", "distill"), default="pref")
     ap.add_argument("--steps", type=int, default=40)
     ap.add_argument("--state-bits", type=int, choices=(8, 32), default=32)
     a = ap.parse_args()
-    losses, gains = train(a.loss, a.steps, a.state_bits)
+    if a.loss == "distill":
+        losses, gains = distill(a.steps, a.state_bits), None
+    else:
+        losses, gains = train(a.loss, a.steps, a.state_bits)
     for i in range(0, a.steps, max(1, a.steps // 10)):
         print(f"step {i:4d}  loss {losses[i]:.4f}")
     print(f"step {a.steps - 1:4d}  loss {losses[-1]:.4f}")
-    print("log-probability gain of the preferred answers:", " ".join(f"{g:.1f}" for g in gains))
+    if gains is not None:
+        print("log-probability gain of the preferred answers:", " ".join(f"{g:.1f}" for g in gains))
 
 
 if __name__ == "__main__":

@@ -526,6 +526,9 @@ int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float gr
  *            (m - x) / tau under p (0, 0, 0).
  * A row that holds a NaN or +inf, or nothing above -inf, has no probabilities:
  * NaN in every output, ids -1.
+ * One pass over the logits, but for rows in orders or with masks that a list of
+ * some hundred candidates does not hold. V at most 2^22, below 2^23 rows where k
+ * and V ask for long lists (2^24 otherwise); LORA_ERR_LIMIT above.
  *
  * Workspace: 256-byte aligned; 0 for sizes beyond the limits.
  */
@@ -570,7 +573,8 @@ typedef struct {
  *   kl     float[T], out.
  *   state  float[T][k + 2], out or NULL: what lora_distill_grad takes.
  * A row whose x holds a NaN or +inf, or nothing above -inf, gives NaN.
- * Rules of logits as above.
+ * Rules of logits as above; V at most 2^23, below 2^23 rows of more than 2560
+ * vectors of 16 bytes (LORA_ERR_LIMIT above).
  *   workspace: lora_distill_workspace_bytes(T, V, k), 256-byte aligned; 0 for
  *   sizes beyond the limits.
  */
@@ -594,7 +598,8 @@ int lora_distill_grad(const lora_mat* logits, const int32_t* top_ids, int64_t k,
  *   loss = sum over t of weights_t kl_t (one float, out, summed in float64;
  *   a weight of 0 drops its term, also where kl is infinite or NaN), kl as
  *   above, dlogits the gradient of the loss times grad_scale. Also with T = 0
- *   the loss is written.
+ *   the loss is written. A row's sums may be taken in another order than by
+ *   lora_distill_kl (a long row is read from memory once).
  */
 int lora_distill_step(const lora_mat* logits, const lora_teacher* teacher, const float* weights, float grad_scale,
                       float* loss, float* kl, const lora_mat* dlogits, void* workspace, size_t workspace_bytes,

@@ -58,6 +58,32 @@ def test_top(lib):
     assert top(x, nbytes=need(4, 9, 5)) == LAUNCH and top(x, ws=FAKE + 16) == WORKSPACE
 
 
+def test_largest_sizes(lib):
+    def top(T, V, k, dtype=1):
+        assert (lib.lora_token_top_workspace_bytes(T, V, k) > 0) == (T <= MOST)
+        return lib.lora_token_top(by(m(T, V, dtype)), FAKE, k, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, HUGE, None)
+
+    assert top(3, 2 ** 22, 128) == LAUNCH
+    assert lib.lora_token_top_workspace_bytes(3, 2 ** 22 + 1, 1) == 0
+    assert lib.lora_token_top(by(m(3, 2 ** 22 + 1)), FAKE, 1, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, HUGE, None) == LIMIT
+    assert top(MOST, 1000, 5) == LAUNCH
+    # eight waves to a row, two pieces of a row
+    assert top(2 ** 23 - 1, 70001, 20) == LAUNCH
+    for T, V, k in ((2 ** 23, 70001, 20), (2 ** 22, 128256, 128)):
+        assert lib.lora_token_top_workspace_bytes(T, V, k) == 0
+        assert lib.lora_token_top(by(m(T, V)), FAKE, k, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, HUGE, None) == LIMIT
+
+    def kl(T, V, dtype=1):
+        t = LoraTeacher(FAKE, FAKE, 64, 1.0, 1)
+        return lib.lora_distill_kl(by(m(T, V, dtype)), by(t), FAKE, None, FAKE, HUGE, None)
+
+    assert kl(3, 2 ** 23) == LAUNCH and kl(3, 2 ** 23 + 1) == LIMIT
+    assert lib.lora_distill_workspace_bytes(3, 2 ** 23, 1) > 0 and lib.lora_distill_workspace_bytes(3, 2 ** 23 + 1, 1) == 0
+    assert kl(MOST, 2560 * 8) == LAUNCH and kl(2 ** 23 - 1, 2561 * 8) == LAUNCH and kl(2 ** 23, 2561 * 8) == LIMIT
+    # rows longer than one workgroup takes: three pieces of 131072
+    assert kl(MOST // 3, 3 * 131072) == LAUNCH and kl(MOST // 3 + 1, 3 * 131072) == LIMIT
+
+
 def check_gradients(grad):
     """What every gradient of logits refuses."""
     for v, status in bad_logits():

@@ -48,7 +48,7 @@ struct Others {
 
 // The teacher's tokens of one row, in LDS.
 struct Tokens {
-  int id[kMaxTeacher];   // -1: none
+  __attribute__((aligned(16))) int id[kMaxTeacher];  // -1: none
   double q[kMaxTeacher]; // if an id occurs twice
   int twice;
 };
@@ -476,9 +476,14 @@ __global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Te
   const float m = at_max(lane_max(v.s > 0.0 ? v.m : -INFINITY));
   const Others all{m, lane_total(v.s > 0.0 ? v.s * exp(((double)v.m - m) * t.inv_temperature) : v.s)};
   __syncthreads();
-  if (id >= 0)
-    for (int e = 0; e < tid; ++e)
-      if (tokens.id[e] == id) tokens.twice = 1;
+  bool before = false;
+#pragma unroll 4
+  for (int e = 0; e < t.k; e += 4) {  // ids past the last are -1
+    const int4 v = *reinterpret_cast<const int4*>(tokens.id + e);
+    before |= (v.x == id) & (e < tid) | (v.y == id) & (e + 1 < tid) | (v.z == id) & (e + 2 < tid) |
+              (v.w == id) & (e + 3 < tid);
+  }
+  if (before && id >= 0) tokens.twice = 1;
   __syncthreads();
   put_row(kl, state, t, row, m, finish_row<4>(t, V, all, id, mine, logq, tokens));
 }

@@ -671,8 +671,15 @@ __global__ __launch_bounds__(256) void top_join_kernel(const E* __restrict__ x, 
   __syncthreads();
   const TopStats v = shared;
   auto each = [&](auto f) {
-    for (int i = tid; i < splits * k; i += 256)
-      if (entries[i] != 0) f(value_of(static_cast<uint32_t>(entries[i] >> 32)), column_of(entries[i]), -1);
+    const int n = splits * k;
+    for (int i = tid; i < n; i += 4 * 256) {
+      uint64_t e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e[u] = entries[i + u * 256 < n ? i + u * 256 : n - 1];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * 256 < n && e[u] != 0) f(value_of(static_cast<uint32_t>(e[u] >> 32)), column_of(e[u]), -1);
+    }
   };
   if (out.k > 0 && !select_top<256>(each, v.m, shared_lo < kFloor ? kFloor : shared_lo, kk, l))
     select_exactly<256>(each, kk, l);

@@ -58,6 +58,7 @@ struct TopOut {
 // order, `count` of them.
 __device__ __forceinline__ void put_row(const TopOut& o, int64_t row, const TopStats& v, bool target, float x,
                                         const uint64_t* entries, int count) {
+  if (threadIdx.x >> 6 > 0 && (int)threadIdx.x >= o.k) return;
   const bool ok = v.defined();
   const double ls = log1p(v.r);
   if (threadIdx.x == 0) {
@@ -94,17 +95,24 @@ __device__ __forceinline__ void put_masked(const TopOut& o, int64_t row) {
 // selection of the k largest of a set of entries by a workgroup
 // ---------------------------------------------------------------------------
 
-constexpr int kList = 512;         // entries that are put in order at most
+constexpr int kList = 512;    // entries that are put in order at most
+constexpr int kDirect = 192;  // and so many without a look at their bins first
 constexpr float kFloor = -1e30f;   // logits below (-inf, a mask's lowest values) share one bin
 
 struct Select {
   int hist[256];
-  int count;                 // entries in the list
+  int count;  // entries in the list
   uint32_t low;
-  int first;                 // where the largest entry came from
   uint64_t list[kList], sorted[kMaxTop];
-  int from[kList];
 };
+
+// Room for n more of each lane behind *count, by the whole wave at once.
+__device__ __forceinline__ int reserve(int n, int* count) {
+  const int upto = lane_sums(n), total = __builtin_amdgcn_readlane(upto, 63);
+  int at = 0;
+  if (total > 0 && (threadIdx.x & 63) == 63) at = atomicAdd(count, total);
+  return __builtin_amdgcn_readlane(at, 63) + upto - n;
+}
 
 // 255 bins of equal width from hi down to lo and below, and the one of kFloor.
 struct Bins {
@@ -140,39 +148,35 @@ __device__ __forceinline__ void clear(Select& l) {
   if (threadIdx.x == 0) l.count = 0;
 }
 
-// Puts l.list in order, the first k of it into l.sorted.
+// The first k of n entries in order.
 template <int THREADS>
-__device__ __forceinline__ void sort_list(Select& l, int n, int k) {
+__device__ __forceinline__ void sort_list(const uint64_t* list, int n, int k, uint64_t* sorted) {
   for (int i = threadIdx.x; i < n; i += THREADS) {
-    const uint64_t e = l.list[i];
+    const uint64_t e = list[i];
     int rank = 0;
 #pragma unroll 8
-    for (int j = 0; j < n; ++j) rank += l.list[j] > e;
-    if (rank < k) l.sorted[rank] = e;
-    if (rank == 0) l.first = l.from[i];
+    for (int j = 0; j < n; ++j) rank += list[j] > e;
+    if (rank < k) sorted[rank] = e;
   }
   __syncthreads();
 }
 
-// The k largest of the entries that each(f) gives f(value, column, from) of,
-// in order; hi is the largest value, lo one that k entries reach. False if too
+// The k largest of the entries that each(f) gives f(value, column) of, in order; hi is the largest value, lo one that k entries reach. False if too
 // many share the k-th's bin. Starts from a cleared l, with a barrier behind it.
 template <int THREADS, class Each>
 __device__ __forceinline__ bool select_top(Each each, float hi, float lo, int k, Select& l) {
   const Bins bins(hi, lo);
-  each([&](float f, int, int) { atomicAdd(&l.hist[bins.of(f)], 1); });
+  each([&](float f, int) { atomicAdd(&l.hist[bins.of(f)], 1); });
   __syncthreads();
   const int last = kth_bin(l.hist, k);
-  each([&](float f, int column, int from) {
+  each([&](float f, int column) {
     if (bins.of(f) > last) return;
     const int at = atomicAdd(&l.count, 1);
-    if (at >= kList) return;
-    l.list[at] = entry_of(f, column);
-    l.from[at] = from;
+    if (at < kList) l.list[at] = entry_of(f, column);
   });
   __syncthreads();
   if (l.count > kList) return false;
-  sort_list<THREADS>(l, l.count, k);
+  sort_list<THREADS>(l.list, l.count, k, l.sorted);
   return true;
 }
 
@@ -188,7 +192,7 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
     __syncthreads();
     // neighbours are often equal: a thread counts a run of them before it adds it
     int run_bin = 0, run = 0;
-    each([&](float f, int column, int) {
+    each([&](float f, int column) {
       const uint64_t e = entry_of(f, column);
       if ((e & mask) != kth) return;
       const int bin = 255 - (int)(e >> shift & 255);
@@ -206,16 +210,14 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
     kth |= static_cast<uint64_t>(255 - bin) << shift;
     mask |= static_cast<uint64_t>(255) << shift;
   }
-  each([&](float f, int column, int) {
+  each([&](float f, int column) {
     const uint64_t e = entry_of(f, column);
     if (e < kth) return;
     const int at = atomicAdd(&l.count, 1);
-    if (at >= kList) return;
-    l.list[at] = e;
-    l.from[at] = -1;
+    if (at < kList) l.list[at] = e;
   });
   __syncthreads();
-  sort_list<THREADS>(l, l.count < kList ? l.count : kList, k);
+  sort_list<THREADS>(l.list, l.count < kList ? l.count : kList, k, l.sorted);
 }
 
 // ---------------------------------------------------------------------------
@@ -330,9 +332,10 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   constexpr int N = Vec<E>::N, U = 32 / N, THREADS = 64 * WAVES;
   using V4 = typename Vec<E>::type;
   __shared__ Select l;
-  __shared__ uint4 hit[HITS];
   __shared__ int hit_at[HITS];
-  __shared__ int hits;
+  __shared__ int hits, candidates;
+  __shared__ uint64_t candidate[HITS];
+  __shared__ int wave_n[WAVES];
   __shared__ float wave_hi[WAVES], wave_lo[WAVES];
   __shared__ double wave_s[WAVES], wave_w[WAVES];
   __shared__ TopStats shared;
@@ -360,9 +363,8 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     for (int u = 0; u < U; ++u) w[u] = next(tid + u * THREADS);
   }
   if (tid == 0) {
-    hits = 0;
-    l.first = -1;  // of a row without elements
-    l.sorted[0] = 0;
+    hits = candidates = 0;
+    l.sorted[0] = 0;  // of a row without elements
   }
   clear<THREADS>(l);
   float mine = -INFINITY;  // the lane's largest
@@ -410,33 +412,32 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   const float shift = -z * s.hi;
   auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
 
-  // a lane keeps the sums of the listed vector that holds its largest logit apart
+  // A bit for each of a lane's 32 last vectors says which are listed. One that reaches the largest of the first elements
+  // may hold the row's largest: its sums are left to the end, when that is known.
+  const float first = hi;
   double sum = 0.0, wsum = 0.0;
-  VecSums held{0.0f, 0.0f};
-  float held_m = -INFINITY;
-  int held_at = -1;
-  auto list = [&](V4 v, int i) {
-    const int at = atomicAdd(&hits, 1);
-    if (at >= HITS) return;
-    hit[at] = make_uint4(v[0], v[1], v[2], v[3]);
-    hit_at[at] = i;
-  };
-  auto take = [&](V4 v, int i) -> VecSums {
+  uint32_t marks = 0;
+  auto take = [&](V4 v, int slot) -> VecSums {
     float f[N];
     Vec<E>::unpack(v, f);
     const float m = vec_max<N>(f);
     VecSums t = vec_sums<E>(v, exponent);
     if (m >= reach) {
-      list(v, i);
-      if (m > held_m) {
-        const VecSums before = held;
-        held = t;
-        t = before;
-        held_m = m;
-        held_at = i;
-      }
+      marks |= 1u << slot;
+      mine = fmaxf(mine, m);
+      if (m >= first) t = {0.0f, 0.0f};
     }
     return t;
+  };
+  // the marks of the vectors from `at` on, THREADS apart
+  auto list_marks = [&](int at) {
+    if (!__any(marks != 0)) return;
+    int to = reserve(__popc(marks), &hits);
+    while (marks != 0) {
+      if (to < HITS) hit_at[to] = at + __builtin_ctz(marks) * THREADS;
+      ++to;
+      marks &= marks - 1;
+    }
   };
   // the sums of a lane's 32 elements are float32, those of all of them float64
   VecSums part{0.0f, 0.0f};
@@ -448,10 +449,17 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (tid + u * THREADS < whole) add(take(w[u], tid + u * THREADS));
-  if (part_of_one) add(take(vec_at(p, whole, n), whole));
+    if (tid + u * THREADS < whole) add(take(w[u], u));
+  if (part_of_one) {
+    add(take(vec_at(p, whole, n), 31));
+    if (marks >> 31 != 0) {
+      const int to = atomicAdd(&hits, 1);
+      if (to < HITS) hit_at[to] = whole;
+      marks &= 0x7FFFFFFFu;
+    }
+  }
   flush();
-  int base = U * THREADS;
+  int base = U * THREADS, begin = 0;  // the vectors not read yet, those of the marks
   // four vectors at a time, the next four on their way
   constexpr int B = 4;
   V4 a[B];
@@ -459,7 +467,12 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
 #pragma unroll
     for (int u = 0; u < B; ++u) a[u] = next(base + tid + u * THREADS);
   }
-  for (; base + B * THREADS <= whole; base += B * THREADS) {
+  for (int slot = U; base + B * THREADS <= whole; base += B * THREADS, slot += B) {
+    if (slot == 32) {
+      list_marks(begin + tid);
+      begin = base;
+      slot = 0;
+    }
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       w[u] = a[u];
@@ -467,13 +480,15 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     }
     sched_fence();
 #pragma unroll
-    for (int u = 0; u < B; ++u) add(take(w[u], base + tid + u * THREADS));
+    for (int u = 0; u < B; ++u) add(take(w[u], slot + u));
     flush();
   }
+  list_marks(begin + tid);
 #pragma unroll
   for (int u = 0; u < B; ++u)
-    if (base + tid + u * THREADS < whole) add(take(a[u], base + tid + u * THREADS));
+    if (base + tid + u * THREADS < whole) add(take(a[u], u));
   flush();
+  list_marks(base + tid);
 
   // f(vector, its index) once more for the whole piece
   auto scan = [&](auto f) {
@@ -493,17 +508,18 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
       Vec<E>::unpack(v, e);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (i * N + j < n) f(e[j], lo + i * N + j, -1);
+        if (i * N + j < n) f(e[j], lo + i * N + j);
     });
   };
 
   // the k largest
   clear<THREADS>(l);
   __syncthreads();
+  bool over = false;
   for (int turn = 0; turn < 2 && hits > HITS; ++turn) {
     // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on;
     // if that is a value that many have, from the next one on.
-    reach = turn == 0 ? kth_lane(held_m) : value_of(order_of(reach) + 1);
+    reach = turn == 0 ? kth_lane(mine) : value_of(order_of(reach) + 1);
     clear<THREADS>(l);
     __syncthreads();
     if (tid == 0) hits = 0;
@@ -511,30 +527,83 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     scan([&](V4 v, int i) {
       float f[N];
       Vec<E>::unpack(v, f);
-      if (vec_max<N>(f) >= reach) list(v, i);
+      if (!(vec_max<N>(f) >= reach)) return;
+      const int at = atomicAdd(&hits, 1);
+      if (at < HITS) hit_at[at] = i;
     });
     __syncthreads();
+    over = !(reach <= first);
   }
-  auto listed = [&](auto f) {
-    for (int i = tid; i < hits; i += THREADS) {
-      const uint4 h = hit[i];
-      const V4 v = {h.x, h.y, h.z, h.w};
+  const bool listed = hits <= HITS;
+  over = over || !listed;  // not all that the sums lack are at hand
+  auto vector_at = [&](int i) { return i < whole ? vload(p + (int64_t)i * N) : vec_at(p, i, n); };
+  // of the listed vectors that reach `first`, a lane keeps the one with its largest logit apart
+  VecSums held{0.0f, 0.0f};
+  V4 held_v;
+  float held_m = -INFINITY;
+  int held_at = -1;
+  bool found = listed;
+  if (listed) {
+    // the elements from `reach` on
+    for (int i0 = 0; i0 < hits; i0 += THREADS) {
+      const int at = i0 + tid < hits ? hit_at[i0 + tid] : -1;
       float e[N];
-      Vec<E>::unpack(v, e);
+      uint32_t bits = 0;
+      if (at >= 0) {
+        const V4 v = vector_at(at);
+        Vec<E>::unpack(v, e);
+        const float m = vec_max<N>(e);
+#pragma unroll
+        for (int j = 0; j < N; ++j) bits |= e[j] >= reach && at * N + j < n ? 1u << j : 0u;
+        if (m >= first) {
+          VecSums t = vec_sums<E>(v, exponent);
+          if (m > held_m || (m == held_m && at < held_at)) {
+            const VecSums before = held;
+            held = t;
+            t = before;
+            held_v = v;
+            held_m = m;
+            held_at = at;
+          }
+          add(t);
+          flush();
+        }
+      }
+      int to = reserve(__popc(bits), &candidates);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (e[j] >= reach && hit_at[i] * N + j < n) f(e[j], lo + hit_at[i] * N + j, i);
+        if (bits >> j & 1u) {
+          if (to < HITS) candidate[to] = entry_of(e[j], lo + at * N + j);
+          ++to;
+        }
     }
-  };
-  bool found = hits <= HITS;
-  if (found) {
-    const float most = lane_max(held_m);
+    const float most = lane_max(mine);
     if ((tid & 63) == 0) wave_hi[tid >> 6] = most;
     __syncthreads();
-    float m = most;
+    if (candidates <= kDirect) {
+      sort_list<THREADS>(candidate, candidates, kk, l.sorted);
+      if (tid == 0) l.count = candidates;
+      __syncthreads();
+    } else {
+      float m = most;
 #pragma unroll
-    for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
-    found = select_top<THREADS>(listed, m, reach > kFloor ? reach : low, kk, l);
+      for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
+      auto each = [&](auto f) {
+        if (candidates <= HITS) {
+          for (int i = tid; i < candidates; i += THREADS)
+            f(value_of(static_cast<uint32_t>(candidate[i] >> 32)), column_of(candidate[i]));
+          return;
+        }
+        for (int i = tid; i < hits; i += THREADS) {
+          float e[N];
+          Vec<E>::unpack(vector_at(hit_at[i]), e);
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (e[j] >= reach && hit_at[i] * N + j < n) f(e[j], lo + hit_at[i] * N + j);
+        }
+      };
+      found = select_top<THREADS>(each, m, reach > kFloor ? reach : low, kk, l);
+    }
   }
   // Fewer than k from `reach` on, in order: what comes below, value by value (after a mask mostly one), the lowest columns
   // of a value first.
@@ -544,7 +613,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     if (!found) break;
     float below = -INFINITY;
     bool some = false;
-    all([&](float f, int, int) {
+    all([&](float f, int) {
       if (!(f < reach)) return;
       below = fmaxf(below, f);
       some = true;
@@ -562,12 +631,12 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
 #pragma unroll
       for (int j = 0; j < N; ++j) mine_too += e[j] == below && (i0 + tid) * N + j < n;
       const int upto = lane_sums(mine_too);
-      if ((tid & 63) == 63) l.from[tid >> 6] = upto;
+      if ((tid & 63) == 63) wave_n[tid >> 6] = upto;
       __syncthreads();
       int at = have + upto - mine_too;
       for (int v = 0; v < WAVES; ++v) {
-        at += v < (tid >> 6) ? l.from[v] : 0;
-        have += l.from[v];
+        at += v < (tid >> 6) ? wave_n[v] : 0;
+        have += wave_n[v];
       }
 #pragma unroll
       for (int j = 0; j < N; ++j)
@@ -579,11 +648,11 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     select_exactly<THREADS>(all, kk, l);
     have = kk;
   }
-  const int top = column_of(l.sorted[0]) - lo, top_at = top / N;
+  const int top = column_of(l.sorted[0]) - lo;
   const float m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
 
   // the sums over all but the largest
-  const bool again = s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
+  const bool again = over || s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
   const LeftOut<E> without_top(top, vecs);
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
@@ -593,7 +662,11 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
       add(vec_sums<E>(v, from_m));
       flush();
     });
-  } else if (held_at != top_at) {
+  } else {
+    if (held_at >= 0 && held_at == top / N) {
+      without_top.template from<1>(&held_v, held_at, 1);
+      held = vec_sums<E>(held_v, exponent);
+    }
     sum += held.s;
     wsum += held.w;
   }
@@ -610,18 +683,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
       wsum += wave_w[v];
     }
     double d = 0.0;  // the largest logit's exponent
-    if (!again && m > -INFINITY) {
-      V4 h;
-      if (l.first >= 0)
-        h = V4{hit[l.first].x, hit[l.first].y, hit[l.first].z, hit[l.first].w};
-      else
-        h = vec_at(p, top_at, n);
-      without_top.template from<1>(&h, top_at, 1);
-      const VecSums others = vec_sums<E>(h, exponent);
-      sum += others.s;
-      wsum += others.w;
-      d = (double)m * s.hi + ((double)m * s.lo + shift);
-    }
+    if (!again && m > -INFINITY) d = (double)m * s.hi + ((double)m * s.lo + shift);
     const double one = exp2(d);
     shared = m > -INFINITY ? TopStats{m, sum / one, (sum * d - wsum) * kLn2 / one} : TopStats{m, sum, 0.0};
   }
@@ -684,7 +746,7 @@ __global__ __launch_bounds__(256) void top_join_kernel(const E* __restrict__ x, 
       for (int u = 0; u < 4; ++u) e[u] = entries[i + u * 256 < n ? i + u * 256 : n - 1];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (i + u * 256 < n && e[u] != 0) f(value_of(static_cast<uint32_t>(e[u] >> 32)), column_of(e[u]), -1);
+        if (i + u * 256 < n && e[u] != 0) f(value_of(static_cast<uint32_t>(e[u] >> 32)), column_of(e[u]));
     }
   };
   if (out.k > 0 && !select_top<256>(each, v.m, shared_lo < kFloor ? kFloor : shared_lo, kk, l))

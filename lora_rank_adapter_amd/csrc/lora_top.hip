@@ -261,31 +261,42 @@ __device__ __forceinline__ float tree(const float* f) {
     return tree<N / 2>(f) + tree<N / 2>(f + N / 2);
 }
 
-// a(f) is the exponent of a logit. 0 times -inf is not 0: a vector with such an
-// exponent (a logit of -inf) is summed once more without it, which costs less
-// than a bound on every exponent (8192 x 128256: 251 -> 238 us).
+// The sums of a vector added to t; a(f) is the exponent of a logit.
 template <class E, class F>
-__device__ __forceinline__ VecSums vec_sums(typename Vec<E>::type v, F a) {
+__device__ __forceinline__ VecSums add_sums(typename Vec<E>::type v, F a, VecSums t) {
   constexpr int N = Vec<E>::N;
-  float f[N], w = 0.0f;
+  float f[N];
   Vec<E>::unpack(v, f);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float b = a(f[i]);
     f[i] = __builtin_amdgcn_exp2f(b);
-    w = fmaf(f[i], b, w);
+    t.w = fmaf(f[i], b, t.w);
   }
-  const float sum = tree<N>(f);
-  if (w != w) {
-    Vec<E>::unpack(v, f);
-    w = 0.0f;
+  t.s += tree<N>(f);
+  return t;
+}
+
+// 0 times -inf is not 0: where a vector holds such an exponent (a logit of
+// -inf) w is summed once more with bounds, which costs less than to have them
+// everywhere (8192 x 128256: 251 -> 238 us).
+template <class E, class F>
+__device__ __forceinline__ float bound_w(typename Vec<E>::type v, F a, float w) {
+  constexpr int N = Vec<E>::N;
+  float f[N];
+  Vec<E>::unpack(v, f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float b = a(f[i]);
-      w = fmaf(__builtin_amdgcn_exp2f(b), fmaxf(b, -256.0f), w);
-    }
+  for (int i = 0; i < N; ++i) {
+    const float b = a(f[i]);
+    w = fmaf(__builtin_amdgcn_exp2f(b), fmaxf(b, -256.0f), w);
   }
-  return {sum, w};
+  return w;
+}
+template <class E, class F>
+__device__ __forceinline__ VecSums vec_sums(typename Vec<E>::type v, F a) {
+  VecSums t = add_sums<E>(v, a, {0.0f, 0.0f});
+  if (t.w != t.w) t.w = bound_w<E>(v, a, 0.0f);
+  return t;
 }
 
 // Vector i of n elements; -inf past the last.
@@ -306,11 +317,18 @@ __device__ __forceinline__ typename Vec<E>::type vec_at(const E* p, int i, int n
   return w;
 }
 
+// fmaxf three at a time, without the instruction that makes a signalling NaN a
+// quiet one first (such a row has no probabilities whatever its maximum).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
 template <int N>
 __device__ __forceinline__ float vec_max(const float* f) {
   float m = f[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, f[i]);
+  for (int i = 1; i < N; i += 2) m = max3(m, f[i], f[i + 1 < N ? i + 1 : i]);
   return m;
 }
 
@@ -329,19 +347,21 @@ template <class E, int WAVES, int HITS>
 __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(
     const E* __restrict__ x, int64_t stride, const int32_t* __restrict__ targets, int V, int splits, int piece,
     Exponent s, TopOut out, TopParts parts) {
-  constexpr int N = Vec<E>::N, U = 32 / N, THREADS = 64 * WAVES;
+  constexpr int N = Vec<E>::N, U = 32 / N, B = 4, THREADS = 64 * WAVES, ROOM = HITS / WAVES;
+  constexpr int FEW = WAVES == 4 && HITS > 512 ? 512 : HITS;  // more than 512 and LDS would hold a workgroup less
   using V4 = typename Vec<E>::type;
   __shared__ Select l;
+  __shared__ uint4 hit[HITS];  // a part for each wave
   __shared__ int hit_at[HITS];
-  __shared__ int hits, candidates;
-  __shared__ uint64_t candidate[HITS];
+  __shared__ int overflow, candidates;
+  __shared__ uint64_t candidate[FEW];
   __shared__ int wave_n[WAVES];
   __shared__ float wave_hi[WAVES], wave_lo[WAVES];
   __shared__ double wave_s[WAVES], wave_w[WAVES];
   __shared__ TopStats shared;
   const int64_t row = blockIdx.x / (unsigned)splits;
   const int sp = (int)(blockIdx.x % (unsigned)splits);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int y = targets != nullptr ? targets[row] : -1;
   const bool target = y >= 0 && y < V;
   if (targets != nullptr && !target) {
@@ -357,13 +377,16 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
 
   // Loads past the last vector take it once more: behind a condition each would be waited for at once.
   auto next = [&](int i) { return vload_nt(p + (int64_t)(i < whole ? i : whole - 1) * N); };
-  V4 w[U];
+  V4 w[U], a[B];  // four vectors are summed at a time, the next four on their way
   if (whole > 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = next(tid + u * THREADS);
+#pragma unroll
+    for (int u = 0; u < B; ++u) a[u] = next(tid + (U + u) * THREADS);
   }
+  sched_fence();
   if (tid == 0) {
-    hits = candidates = 0;
+    overflow = candidates = 0;
     l.sorted[0] = 0;  // of a row without elements
   }
   clear<THREADS>(l);
@@ -379,7 +402,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   const bool part_of_one = tid == 0 && whole < vecs;  // the last vector, in part
   if (part_of_one) largest(vec_at(p, whole, n));
   // A value that the k-th largest of the lanes' reaches; kFloor if fewer than k reach that. hi and low are the largest
-  // and the smallest from kFloor on. Starts from a cleared l.
+  // and the smallest from kFloor on. l is clear before and after.
   float hi, low;
   auto kth_lane = [&](float v) {
     hi = lane_max(v);
@@ -401,7 +424,9 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     const int last = kth_bin(l.hist, k);
     if (b <= last) atomicMin(&l.low, order_of(v));
     __syncthreads();
-    return last < 255 ? value_of(l.low) : kFloor;
+    const float kth = last < 255 ? value_of(l.low) : kFloor;
+    clear<THREADS>(l);
+    return kth;
   };
   // vectors with an element from here on are listed: all of few
   float reach = kth_lane(mine);
@@ -412,150 +437,156 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   const float shift = -z * s.hi;
   auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
 
-  // A bit for each of a lane's 32 last vectors says which are listed. One that reaches the largest of the first elements
-  // may hold the row's largest: its sums are left to the end, when that is known.
+  // Every wave lists for itself. A vector that reaches the largest of the first elements may hold the row's largest: its
+  // sums are left to the end, when that is known.
   const float first = hi;
   double sum = 0.0, wsum = 0.0;
-  uint32_t marks = 0;
-  auto take = [&](V4 v, int slot) -> VecSums {
-    float f[N];
-    Vec<E>::unpack(v, f);
-    const float m = vec_max<N>(f);
-    VecSums t = vec_sums<E>(v, exponent);
-    if (m >= reach) {
-      marks |= 1u << slot;
-      mine = fmaxf(mine, m);
-      if (m >= first) t = {0.0f, 0.0f};
+  int hits = 0;
+  auto list = [&](V4 v, int i, bool on) {
+    const uint64_t those = __ballot(on);
+    if (on) {
+      const int at = hits + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(those >> 32),
+                                                           __builtin_amdgcn_mbcnt_lo((uint32_t)those, 0));
+      if (at < ROOM) {
+        hit[wave * ROOM + at] = make_uint4(v[0], v[1], v[2], v[3]);
+        hit_at[wave * ROOM + at] = i;
+      }
     }
-    return t;
-  };
-  // the marks of the vectors from `at` on, THREADS apart
-  auto list_marks = [&](int at) {
-    if (!__any(marks != 0)) return;
-    int to = reserve(__popc(marks), &hits);
-    while (marks != 0) {
-      if (to < HITS) hit_at[to] = at + __builtin_ctz(marks) * THREADS;
-      ++to;
-      marks &= marks - 1;
-    }
+    hits += __popcll(those);
   };
   // the sums of a lane's 32 elements are float32, those of all of them float64
   VecSums part{0.0f, 0.0f};
-  auto add = [&](VecSums t) { part = {part.s + t.s, part.w + t.w}; };
   auto flush = [&] {
     sum += part.s;
     wsum += part.w;
     part = {0.0f, 0.0f};
   };
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (tid + u * THREADS < whole) add(take(w[u], u));
-  if (part_of_one) {
-    add(take(vec_at(p, whole, n), 31));
-    if (marks >> 31 != 0) {
-      const int to = atomicAdd(&hits, 1);
-      if (to < HITS) hit_at[to] = whole;
-      marks &= 0x7FFFFFFFu;
+  auto late = [&](float m) { return m >= reach && m >= first; };
+  // `there` is false for what a lane loaded past the last vector
+  auto take = [&](V4 v, int i, bool there) {
+    float f[N];
+    Vec<E>::unpack(v, f);
+    const float m = vec_max<N>(f);
+    const VecSums before = part;
+    part = add_sums<E>(v, exponent, part);
+    const bool on = there && m >= reach;
+    if (__any(on)) {
+      list(v, i, on);
+      mine = on ? max3(mine, m, m) : mine;
+      if (on && m >= first) part = before;
     }
-  }
+    if (!there) part = before;
+  };
+  // part.w of the vectors that were just taken, where one holds a logit of -inf
+  auto bound = [&](const V4* v, auto count, auto taken) {
+    if (part.w == part.w) return;
+    part.w = 0.0f;
+#pragma unroll
+    for (int u = 0; u < count(); ++u) {
+      V4 x = v[u];
+      asm volatile("" : "+v"(x));  // unpacked anew: values kept from above would take registers from all
+      float f[N];
+      Vec<E>::unpack(x, f);
+      if (taken(u) && !late(vec_max<N>(f))) part.w = bound_w<E>(x, exponent, part.w);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) take(w[u], tid + u * THREADS, tid + u * THREADS < whole);
+  bound(w, std::integral_constant<int, U>(), [&](int u) { return tid + u * THREADS < whole; });
   flush();
-  int base = U * THREADS, begin = 0;  // the vectors not read yet, those of the marks
-  // four vectors at a time, the next four on their way
-  constexpr int B = 4;
-  V4 a[B];
-  if (base < whole) {
-#pragma unroll
-    for (int u = 0; u < B; ++u) a[u] = next(base + tid + u * THREADS);
+  if (whole < vecs && wave == 0) {
+    const V4 v = vec_at(p, whole, n);
+    take(v, whole, tid == 0);
+    bound(&v, std::integral_constant<int, 1>(), [&](int) { return tid == 0; });
+    flush();
   }
-  for (int slot = U; base + B * THREADS <= whole; base += B * THREADS, slot += B) {
-    if (slot == 32) {
-      list_marks(begin + tid);
-      begin = base;
-      slot = 0;
-    }
+  int base = U * THREADS;
+  for (; base + B * THREADS <= whole; base += B * THREADS) {
 #pragma unroll
-    for (int u = 0; u < B; ++u) {
-      w[u] = a[u];
-      a[u] = next(base + tid + (u + B) * THREADS);
+    for (int u = 0; u < B; ++u) w[u] = a[u];
+    if (base + 2 * B * THREADS <= whole) {  // an address of the whole workgroup
+#pragma unroll
+      for (int u = 0; u < B; ++u) a[u] = vload_nt(p + (int64_t)(base + (u + B) * THREADS) * N + tid * N);
+    } else {
+#pragma unroll
+      for (int u = 0; u < B; ++u) a[u] = next(base + tid + (u + B) * THREADS);
     }
     sched_fence();
 #pragma unroll
-    for (int u = 0; u < B; ++u) add(take(w[u], slot + u));
+    for (int u = 0; u < B; ++u) take(w[u], base + tid + u * THREADS, true);
+    bound(w, std::integral_constant<int, B>(), [](int) { return true; });
     flush();
   }
-  list_marks(begin + tid);
+  if (base < whole) {
 #pragma unroll
-  for (int u = 0; u < B; ++u)
-    if (base + tid + u * THREADS < whole) add(take(a[u], u));
-  flush();
-  list_marks(base + tid);
+    for (int u = 0; u < B; ++u) take(a[u], base + tid + u * THREADS, base + tid + u * THREADS < whole);
+    bound(a, std::integral_constant<int, B>(), [&](int u) { return base + tid + u * THREADS < whole; });
+    flush();
+  }
 
-  // f(vector, its index) once more for the whole piece
+  // f(vector, its index, whether the lane has one) once more for the whole piece
   auto scan = [&](auto f) {
     for (int i = tid; i - tid < whole; i += B * THREADS) {
 #pragma unroll
       for (int u = 0; u < B; ++u) w[u] = next(i + u * THREADS);
       sched_fence();
 #pragma unroll
-      for (int u = 0; u < B; ++u)
-        if (i + u * THREADS < whole) f(w[u], i + u * THREADS);
+      for (int u = 0; u < B; ++u) f(w[u], i + u * THREADS, i + u * THREADS < whole);
     }
-    if (part_of_one) f(vec_at(p, whole, n), whole);
+    if (whole < vecs && wave == 0) f(vec_at(p, whole, n), whole, tid == 0);
   };
   auto all = [&](auto f) {
-    scan([&](V4 v, int i) {
+    scan([&](V4 v, int i, bool there) {
       float e[N];
       Vec<E>::unpack(v, e);
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        if (i * N + j < n) f(e[j], lo + i * N + j);
+        if (there && i * N + j < n) f(e[j], lo + i * N + j);
     });
   };
 
-  // the k largest
-  clear<THREADS>(l);
-  __syncthreads();
-  bool over = false;
-  for (int turn = 0; turn < 2 && hits > HITS; ++turn) {
-    // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on;
-    // if that is a value that many have, from the next one on.
-    reach = turn == 0 ? kth_lane(mine) : value_of(order_of(reach) + 1);
-    clear<THREADS>(l);
-    __syncthreads();
-    if (tid == 0) hits = 0;
-    __syncthreads();
-    scan([&](V4 v, int i) {
-      float f[N];
-      Vec<E>::unpack(v, f);
-      if (!(vec_max<N>(f) >= reach)) return;
-      const int at = atomicAdd(&hits, 1);
-      if (at < HITS) hit_at[at] = i;
-    });
-    __syncthreads();
-    over = !(reach <= first);
-  }
-  const bool listed = hits <= HITS;
-  over = over || !listed;  // not all that the sums lack are at hand
-  auto vector_at = [&](int i) { return i < whole ? vload(p + (int64_t)i * N) : vec_at(p, i, n); };
-  // of the listed vectors that reach `first`, a lane keeps the one with its largest logit apart
-  VecSums held{0.0f, 0.0f};
+  // The k largest, and the sums of the late vectors: of those a lane keeps the one with its largest logit apart.
+  double late_sum, late_wsum;
+  VecSums held;
   V4 held_v;
-  float held_m = -INFINITY;
-  int held_at = -1;
-  bool found = listed;
-  if (listed) {
-    // the elements from `reach` on
-    for (int i0 = 0; i0 < hits; i0 += THREADS) {
-      const int at = i0 + tid < hits ? hit_at[i0 + tid] : -1;
-      float e[N];
-      uint32_t bits = 0;
-      if (at >= 0) {
-        const V4 v = vector_at(at);
+  float held_m;
+  int held_at;
+  bool listed, over = false;  // over: the late vectors are not all listed
+  for (int turn = 0;; ++turn) {
+    if (turn > 0) {
+      // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on;
+      // if that is a value that many have, from the next one on.
+      __syncthreads();
+      reach = turn == 1 ? kth_lane(mine) : value_of(order_of(reach) + 1);
+      over = !(reach <= first);
+      if (tid == 0) overflow = candidates = 0;
+      __syncthreads();
+      hits = 0;
+      scan([&](V4 v, int i, bool there) {
+        float f[N];
+        Vec<E>::unpack(v, f);
+        list(v, i, there && vec_max<N>(f) >= reach);
+      });
+    }
+    late_sum = late_wsum = 0.0;
+    held = {0.0f, 0.0f};
+    held_m = -INFINITY;
+    held_at = -1;
+    if (hits > ROOM) {
+      if (lane == 0) overflow = 1;
+    } else {
+      for (int i0 = 0; i0 < hits; i0 += 64) {
+        const bool there = i0 + lane < hits;
+        const uint4 h = hit[wave * ROOM + (there ? i0 + lane : 0)];
+        const int at = hit_at[wave * ROOM + (there ? i0 + lane : 0)];
+        const V4 v = {h.x, h.y, h.z, h.w};
+        float e[N];
         Vec<E>::unpack(v, e);
         const float m = vec_max<N>(e);
+        uint32_t bits = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) bits |= e[j] >= reach && at * N + j < n ? 1u << j : 0u;
-        if (m >= first) {
+        for (int j = 0; j < N; ++j) bits |= there && e[j] >= reach && at * N + j < n ? 1u << j : 0u;
+        if (there && m >= first) {
           VecSums t = vec_sums<E>(v, exponent);
           if (m > held_m || (m == held_m && at < held_at)) {
             const VecSums before = held;
@@ -565,18 +596,25 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
             held_m = m;
             held_at = at;
           }
-          add(t);
-          flush();
+          late_sum += t.s;
+          late_wsum += t.w;
         }
-      }
-      int to = reserve(__popc(bits), &candidates);
+        int to = reserve(__popc(bits), &candidates);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (bits >> j & 1u) {
-          if (to < HITS) candidate[to] = entry_of(e[j], lo + at * N + j);
-          ++to;
-        }
+        for (int j = 0; j < N; ++j)
+          if (bits >> j & 1u) {
+            if (to < FEW) candidate[to] = entry_of(e[j], lo + at * N + j);
+            ++to;
+          }
+      }
     }
+    __syncthreads();
+    listed = overflow == 0;
+    if (listed || turn == 2) break;
+  }
+  over = over || !listed;
+  bool found = listed;
+  if (listed) {
     const float most = lane_max(mine);
     if ((tid & 63) == 0) wave_hi[tid >> 6] = most;
     __syncthreads();
@@ -589,17 +627,19 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
 #pragma unroll
       for (int v = 0; v < WAVES; ++v) m = fmaxf(m, wave_hi[v]);
       auto each = [&](auto f) {
-        if (candidates <= HITS) {
+        if (candidates <= FEW) {
           for (int i = tid; i < candidates; i += THREADS)
             f(value_of(static_cast<uint32_t>(candidate[i] >> 32)), column_of(candidate[i]));
           return;
         }
-        for (int i = tid; i < hits; i += THREADS) {
+        for (int i = lane; i < hits; i += 64) {
+          const uint4 h = hit[wave * ROOM + i];
+          const int at = hit_at[wave * ROOM + i];
           float e[N];
-          Vec<E>::unpack(vector_at(hit_at[i]), e);
+          Vec<E>::unpack(V4{h.x, h.y, h.z, h.w}, e);
 #pragma unroll
           for (int j = 0; j < N; ++j)
-            if (e[j] >= reach && hit_at[i] * N + j < n) f(e[j], lo + hit_at[i] * N + j);
+            if (e[j] >= reach && at * N + j < n) f(e[j], lo + at * N + j);
         }
       };
       found = select_top<THREADS>(each, m, reach > kFloor ? reach : low, kk, l);
@@ -657,18 +697,19 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
     sum = wsum = 0.0;
-    scan([&](V4 v, int i) {
+    scan([&](V4 v, int i, bool there) {
       without_top.template from<1>(&v, i, 1);
-      add(vec_sums<E>(v, from_m));
-      flush();
+      const VecSums t = vec_sums<E>(v, from_m);
+      sum += there ? t.s : 0.0;
+      wsum += there ? t.w : 0.0;
     });
   } else {
     if (held_at >= 0 && held_at == top / N) {
       without_top.template from<1>(&held_v, held_at, 1);
       held = vec_sums<E>(held_v, exponent);
     }
-    sum += held.s;
-    wsum += held.w;
+    sum += late_sum + held.s;
+    wsum += late_wsum + held.w;
   }
   sum = lane_total(sum);
   wsum = lane_total(wsum);

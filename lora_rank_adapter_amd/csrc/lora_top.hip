@@ -229,8 +229,8 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // found among them. The sums are relative to the largest logit of these first
 // elements, which a row's largest one exceeds by little: no running maximum.
 //
-// Where that does not hold the row is read again: for the sums if a logit is 64
-// binary orders above the reference; for the alternatives if the list overflows
+// Where that does not hold the row is read again: for the sums if the largest
+// logit is 64 binary orders away from the reference; for the alternatives if the list overflows
 // (logits that rise along the row, a masked beginning: from the k-th of the
 // lanes' largest in the whole row on) or holds fewer than k (ties without end, a
 // vocabulary masked down to a few tokens: the lowest columns of the next value).
@@ -245,7 +245,8 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // the selection and the launch the rest.
 // ---------------------------------------------------------------------------
 
-constexpr float kAbove = 64.0f;         // binary orders that a logit may be above the reference
+constexpr float kAbove = 64.0f;         // binary orders that the largest logit may be away from the reference
+constexpr float kFar = 0x1p24f;         // binary orders that the reference may be away from 0
 constexpr int kMaxSplits = 64;
 
 // Sums of a vector's exponentials e = 2^a and of e a.
@@ -433,7 +434,7 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   if (vecs <= 2 * k) reach = -INFINITY;
   const float z = at_max(hi);
   // Two products instead of a difference and two: what `shift` lost to rounding moves all exponents alike, the largest
-  // logit's too. A reference below kFloor (or nearly that far up) would overflow here: such a piece is read again.
+  // logit's too (by at most two orders up to kFar, beyond which a piece is read again).
   const float shift = -z * s.hi;
   auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
 
@@ -692,7 +693,8 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
   const float m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
 
   // the sums over all but the largest
-  const bool again = over || s.of(m - z) > kAbove || !(fabsf(z) <= -kFloor) || (m < kFloor && m > -INFINITY);
+  const bool far = !(fabsf(s.of(m - z)) <= kAbove) || !(fabsf(shift) <= kFar);
+  const bool again = m > -INFINITY && (over || far);
   const LeftOut<E> without_top(top, vecs);
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
@@ -726,7 +728,11 @@ __global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) 
     double d = 0.0;  // the largest logit's exponent
     if (!again && m > -INFINITY) d = (double)m * s.hi + ((double)m * s.lo + shift);
     const double one = exp2(d);
-    shared = m > -INFINITY ? TopStats{m, sum / one, (sum * d - wsum) * kLn2 / one} : TopStats{m, sum, 0.0};
+    // with nothing above -inf the sum is 0 or NaN; m is NaN where nothing could be compared
+    if (m > -INFINITY)
+      shared = {m, sum / one, (sum * d - wsum) * kLn2 / one};
+    else
+      shared = {m, m == -INFINITY ? sum : NAN, 0.0};
   }
   __syncthreads();
   TopStats v = shared;

@@ -79,6 +79,10 @@ def errors(x64, tau):
     gap = (p * u).sum(1)
     err_gap = (p * (u * e + 3 * H * (u + reach(x64, tau)[:, None]) * (u > 0))).sum(1) + gap * err_r + H * gap
     err_gap += V * 2.0 ** -118
+    # An exponent is fl(fl(x hi + shift) + x lo), shift = -fl(z hi) for a z near the largest logit: at the largest ones
+    # themselves it is not 0 but d = z hi + z lo + shift, |d| <= 2^-23 |z| hi, rounded twice: 2 H |d| orders, so
+    # ln(2) hi = 1 / tau, 4 H^2 |z| / tau, in the mean of (m - x) / tau also where that is 0. Beyond 2^24 orders: exact.
+    err_gap += 4 * H * H * np.minimum(np.abs(x64.max(1)) / tau, 2.0 ** 24)
     return u, p, err_r, err_gap
 
 

@@ -81,6 +81,29 @@ def test_lists_that_overflow(dtype, V, k):
         assert all(torch.equal(t[:12], t[i:i + 12]) for i in range(12, 192, 12))
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("T", [9, 198])
+@pytest.mark.parametrize("V,k", [(3001, 5), (128256, 20)])
+def test_logits_far_from_zero(dtype, T, V, k):
+    """Logits around 3e7, 1e10, -1e10 and 1e20, and a few far below zero behind a masked beginning."""
+    note(f"top far from zero {dtype} {T} {V} {k}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V + k)
+    n = torch.arange(V, device=DEV)
+    r = torch.randn(V, device=DEV, generator=g)
+    few = (n > V // 2) & (n % (V // 250) == 1)
+    rows = [3e7 + 8 * r, 1e10 + 4096 * r, -1e10 + 4096 * r, 1e20 + 1e14 * r, 3e5 + r] + [
+        torch.where(few, c + r, -float("inf")) for c in (-60.0, -100.0, -2000.0, 1e9)]
+    x = torch.stack(rows).to(dtype).repeat(T // 9, 1).contiguous()
+    y = x.argmax(1).to(torch.int32)
+    y[3::9] = int(few.nonzero()[1])
+    out = L.lora_token_top(x, y, k, 0.7)
+    assert torch.equal(out[2], ranked(x, k))
+    check(x[:9], y[:9], k, 0.7, tuple(t[:9] for t in out))
+    for t in out:
+        assert all(torch.equal(t[:9], t[i:i + 9]) for i in range(9, T, 9))
+
+
 # rows that registers hold in part or whole, the same in pieces, rows longer than one workgroup takes
 DISTILLS = [(112, 70003, 64), (130, 128256, 33), (64, 40009, 100), (70, 128259, 8), (111, 128256, 16), (63, 50001, 256),
             (3, 262144, 5), (2, 300007, 64), (120, 20481, 3), (1, 49152, 1), (5, 8, 3)]

@@ -234,15 +234,16 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // (logits that rise along the row, a masked beginning: from the k-th of the
 // lanes' largest in the whole row on) or holds fewer than k (ties without end, a
 // vocabulary masked down to a few tokens: the lowest columns of the next value).
-// us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21.9, rising
-// 40, one value throughout 64, masked down to 5 tokens 41, masked in their first
-// half 34.
+// us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21, rising 50,
+// one value throughout 73, masked down to 5 tokens 44, masked in their first
+// half 46.
 //
 // Memory bounds many rows: 5744 of 8192 x 128256 bfloat16 without alternatives
-// 234 us (6.3 TB/s), 4096 with k = 64 201 us (5.2 TB/s; the rest goes into the
-// selection, whose phases other workgroups' loads do not cover whole). 256 rows
-// are one workgroup per CU: their 66 MB take 13 of the 21.9 us, the first loads,
-// the selection and the launch the rest.
+// 232 us (6.3 TB/s, with a quarter fewer instructions the same), 4096 with k =
+// 64 190 us (5.5 TB/s: of a workgroup's 40 us half go into the threshold and the
+// selection, when only others load). 256 rows are one workgroup per CU: reading
+// takes 13 of the 21 us, the first loads, the threshold and the selection the
+// rest.
 // ---------------------------------------------------------------------------
 
 constexpr float kAbove = 64.0f;         // binary orders that the largest logit may be away from the reference
@@ -345,7 +346,7 @@ struct TopParts {
 };
 
 template <class E, int WAVES, int HITS>
-__global__ __launch_bounds__(64 * WAVES, HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(
+__global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof(E) == 2 ? 6 : 5) void top_kernel(
     const E* __restrict__ x, int64_t stride, const int32_t* __restrict__ targets, int V, int splits, int piece,
     Exponent s, TopOut out, TopParts parts) {
   constexpr int N = Vec<E>::N, U = 32 / N, B = 4, THREADS = 64 * WAVES, ROOM = HITS / WAVES;
@@ -866,7 +867,7 @@ __global__ __launch_bounds__(kGradVecs) void top_grad_kernel(GradArgs<E> a, cons
 // host side
 // ---------------------------------------------------------------------------
 
-// Workgroups of 4 or 8 waves with room for so many vectors in their list.
+// Workgroups of 4, 8 or (see very_few) 16 waves with room for so many vectors in their list.
 struct TopShape {
   int waves, hits;
 };
@@ -889,12 +890,21 @@ static TopShape top_shape(int64_t piece, int k) {
   return piece <= most_elements(kShapes[1], k) && piece <= 65536 ? kShapes[1] : kShapes[2];
 }
 
+// Whether 16 waves take each of very few rows whole: one launch in place of two,
+// which the host's time decides; kernels of rows in pieces take about as long.
+// us a call so and in pieces, bfloat16: 1 x 128256, k = 5, 16.2 and 19.1, k = 20
+// 17.1 and 19.1, k = 64 18.5 and 19.2, k = 128 20.1 and 19.0; 1 x 60000, k = 20,
+// 16.2 and 19.2; 8 x 128256, k = 64, 19.9 and 19.4; 1 x 200000, k = 5, 21.7 and
+// 19.1; float32 1 x 128256, k = 5, 17.1 and 19.1.
+static bool very_few(int64_t T, int64_t V, int64_t k) { return T <= 4 && V > 49152 && V <= 131072 && k <= 64; }
+
 // Pieces of a row: one, or of few long rows about as many as give 1024
 // workgroups, of at least 8192 logits each; at most what a list has room for. us
 // a call in one piece and in such pieces, bfloat16:
-//   128256 columns: 1 row, k = 5, 21.3 and 16.9; 128 rows, k = 20, 22.6 and 20.4; 256 rows 23.5 and 25.9
+//   128256 columns: 128 rows, k = 20, 22.6 and 20.4; 256 rows 23.5 and 25.9
 //   32000: 64 rows 14.8 and 16.1
 static int64_t top_splits(int64_t T, int64_t V, int k) {
+  if (very_few(T, V, k)) return 1;
   const int64_t least = ceil_div(V, most_elements(kShapes[2], k));
   int64_t splits = 1;
   if (V > 49152 && T < 192) {
@@ -919,7 +929,7 @@ static TopPlan plan_top(int64_t T, int64_t V, int64_t k, void* ws) {
   const int64_t splits = top_splits(T, V, static_cast<int>(k));
   l.splits = static_cast<int>(splits);
   l.piece = static_cast<int>(round_up(ceil_div(V, l.splits), 8));
-  l.shape = top_shape(l.piece, static_cast<int>(k));
+  l.shape = very_few(T, V, k) ? TopShape{16, 1024} : top_shape(l.piece, static_cast<int>(k));
   l.fits = splits <= kMaxSplits && T * splits <= max_blocks(64 * l.shape.waves);
   Carver w(ws);
   const int64_t pieces = l.splits > 1 ? T * l.splits : 0;
@@ -960,9 +970,10 @@ extern "C" int lora_token_top(const lora_mat* logits, const int32_t* targets, in
   auto st = static_cast<hipStream_t>(stream);
   by_type(logits, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    auto* kernel = l.shape.hits == 256    ? top_kernel<E, 4, 256>
-                   : l.shape.waves == 4 ? top_kernel<E, 4, 1024>
-                                        : top_kernel<E, 8, 1024>;
+    auto* kernel = l.shape.hits == 256     ? top_kernel<E, 4, 256>
+                   : l.shape.waves == 4  ? top_kernel<E, 4, 1024>
+                   : l.shape.waves == 16 ? top_kernel<E, 16, 1024>
+                                         : top_kernel<E, 8, 1024>;
     launch(kernel, dim3(T * l.splits), dim3(64 * l.shape.waves), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
            static_cast<int>(V), l.splits, l.piece, exponent_of(temperature), out, l.parts);
     if (l.splits > 1)

@@ -26,9 +26,10 @@ def framed(x, pad=9, shift=3):
 
 
 # rows, columns, k: one piece with 4 waves and short or long lists, with 8, pieces because the list has no room for
-# more, few rows in pieces, a long vocabulary
+# more, few rows in pieces, a long vocabulary, very few rows with 16 waves and what lies beside that
 TOPS = [(192, 49153, 1), (192, 49153, 20), (200, 32003, 64), (195, 70001, 20), (193, 128256, 100), (192, 128256, 128),
-        (190, 60000, 20), (3, 300007, 64), (2, 49152, 128), (1, 2 ** 20 + 3, 5), (600, 3001, 128)]
+        (190, 60000, 20), (3, 300007, 64), (2, 49152, 128), (1, 2 ** 20 + 3, 5), (600, 3001, 128),
+        (1, 49153, 1), (4, 128256, 64), (3, 131071, 20), (5, 128256, 64), (2, 131073, 20), (1, 131072, 65)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
@@ -79,10 +80,16 @@ def test_lists_that_overflow(dtype, V, k):
     close(f64(out[1][:12]), f64(lse + gap)[:, 0], f64(e + e_gap + H * (lse + gap))[:, 0], "entropy")
     for t in out[1:]:
         assert all(torch.equal(t[:12], t[i:i + 12]) for i in range(12, 192, 12))
+    # very few rows at a time
+    for i in range(0, 12, 3):
+        few = L.lora_token_top(x[i:i + 3], None, k, 1.0)
+        assert torch.equal(few[2], out[2][i:i + 3])
+        close(f64(few[3]), f64(want[i:i + 3]), (f64(e) + 2 * H * np.abs(f64(want)))[i:i + 3], "top of few")
+        close(f64(few[1]), f64(lse + gap)[i:i + 3, 0], f64(e + e_gap + H * (lse + gap))[i:i + 3, 0], "entropy of few")
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
-@pytest.mark.parametrize("T", [9, 198])
+@pytest.mark.parametrize("T", [1, 9, 198])
 @pytest.mark.parametrize("V,k", [(3001, 5), (128256, 20)])
 def test_logits_far_from_zero(dtype, T, V, k):
     """Logits around 3e7, 1e10, -1e10 and 1e20, and a few far below zero behind a masked beginning."""
@@ -94,10 +101,14 @@ def test_logits_far_from_zero(dtype, T, V, k):
     few = (n > V // 2) & (n % (V // 250) == 1)
     rows = [3e7 + 8 * r, 1e10 + 4096 * r, -1e10 + 4096 * r, 1e20 + 1e14 * r, 3e5 + r] + [
         torch.where(few, c + r, -float("inf")) for c in (-60.0, -100.0, -2000.0, 1e9)]
-    x = torch.stack(rows).to(dtype).repeat(T // 9, 1).contiguous()
+    x = torch.stack(rows).to(dtype).repeat(max(1, T // 9), 1).contiguous()
     y = x.argmax(1).to(torch.int32)
     y[3::9] = int(few.nonzero()[1])
-    out = L.lora_token_top(x, y, k, 0.7)
+    if T == 1:  # a call for each row
+        parts = [L.lora_token_top(x[i:i + 1], y[i:i + 1], k, 0.7) for i in range(9)]
+        out = tuple(torch.cat(p) for p in zip(*parts))
+    else:
+        out = L.lora_token_top(x, y, k, 0.7)
     assert torch.equal(out[2], ranked(x, k))
     check(x[:9], y[:9], k, 0.7, tuple(t[:9] for t in out))
     for t in out:

@@ -161,8 +161,9 @@ __device__ __forceinline__ void sort_list(const uint64_t* list, int n, int k, ui
   __syncthreads();
 }
 
-// The k largest of the entries that each(f) gives f(value, column) of, in order; hi is the largest value, lo one that k entries reach. False if too
-// many share the k-th's bin. Starts from a cleared l, with a barrier behind it.
+// The k largest of the entries that each(f) gives f(value, column) of, in order;
+// hi is the largest value, lo one that k entries reach. False if too many share
+// the k-th's bin. Starts from a cleared l, with a barrier behind it.
 template <int THREADS, class Each>
 __device__ __forceinline__ bool select_top(Each each, float hi, float lo, int k, Select& l) {
   const Bins bins(hi, lo);
@@ -230,10 +231,11 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // elements, which a row's largest one exceeds by little: no running maximum.
 //
 // Where that does not hold the row is read again: for the sums if the largest
-// logit is 64 binary orders away from the reference; for the alternatives if the list overflows
-// (logits that rise along the row, a masked beginning: from the k-th of the
-// lanes' largest in the whole row on) or holds fewer than k (ties without end, a
-// vocabulary masked down to a few tokens: the lowest columns of the next value).
+// logit is 64 binary orders away from the reference, or that far from 0; for the
+// alternatives if the list overflows (logits that rise along the row, a masked
+// beginning: from the k-th of the lanes' largest in the whole row on) or holds
+// fewer than k (ties without end, a vocabulary masked down to a few tokens: the
+// lowest columns of the next value).
 // us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21, rising 50,
 // one value throughout 73, masked down to 5 tokens 44, masked in their first
 // half 46.
@@ -246,8 +248,8 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // rest.
 // ---------------------------------------------------------------------------
 
-constexpr float kAbove = 64.0f;         // binary orders that the largest logit may be away from the reference
-constexpr float kFar = 0x1p24f;         // binary orders that the reference may be away from 0
+constexpr float kAbove = 64.0f;  // binary orders that the largest logit may be away from the reference
+constexpr float kFar = 0x1p24f;  // binary orders that the reference may be away from 0
 constexpr int kMaxSplits = 64;
 
 // Sums of a vector's exponentials e = 2^a and of e a.
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (tid + u * THREADS < whole) largest(w[u]);
-  const bool part_of_one = tid == 0 && whole < vecs;  // the last vector, in part
+  const bool part_of_one = tid == THREADS - 1 && whole < vecs;  // the last vector, in part
   if (part_of_one) largest(vec_at(p, whole, n));
   // A value that the k-th largest of the lanes' reaches; kFloor if fewer than k reach that. hi and low are the largest
   // and the smallest from kFloor on. l is clear before and after.
@@ -439,8 +441,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   const float shift = -z * s.hi;
   auto exponent = [&](float f) { return fmaf(f, s.lo, fmaf(f, s.hi, shift)); };
 
-  // Every wave lists for itself. A vector that reaches the largest of the first elements may hold the row's largest: its
-  // sums are left to the end, when that is known.
+  // Every wave lists for itself. A vector that reaches the largest of the first elements may hold the row's largest:
+  // its sums are left to the end, when that is known.
   const float first = hi;
   double sum = 0.0, wsum = 0.0;
   int hits = 0;
@@ -496,10 +498,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   for (int u = 0; u < U; ++u) take(w[u], tid + u * THREADS, tid + u * THREADS < whole);
   bound(w, std::integral_constant<int, U>(), [&](int u) { return tid + u * THREADS < whole; });
   flush();
-  if (whole < vecs && wave == 0) {
+  if (whole < vecs && wave == WAVES - 1) {
     const V4 v = vec_at(p, whole, n);
-    take(v, whole, tid == 0);
-    bound(&v, std::integral_constant<int, 1>(), [&](int) { return tid == 0; });
+    take(v, whole, part_of_one);
+    bound(&v, std::integral_constant<int, 1>(), [&](int) { return part_of_one; });
     flush();
   }
   int base = U * THREADS;
@@ -535,7 +537,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
 #pragma unroll
       for (int u = 0; u < B; ++u) f(w[u], i + u * THREADS, i + u * THREADS < whole);
     }
-    if (whole < vecs && wave == 0) f(vec_at(p, whole, n), whole, tid == 0);
+    if (whole < vecs && wave == WAVES - 1) f(vec_at(p, whole, n), whole, part_of_one);
   };
   auto all = [&](auto f) {
     scan([&](V4 v, int i, bool there) {
@@ -556,8 +558,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   bool listed, over = false;  // over: the late vectors are not all listed
   for (int turn = 0;; ++turn) {
     if (turn > 0) {
-      // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece on;
-      // if that is a value that many have, from the next one on.
+      // Too many, as in logits that rise along the row: anew, from the k-th of the lanes' largest in the whole piece
+      // on; if that is a value that many have, from the next one on.
       __syncthreads();
       reach = turn == 1 ? kth_lane(mine) : value_of(order_of(reach) + 1);
       over = !(reach <= first);
@@ -647,8 +649,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
       found = select_top<THREADS>(each, m, reach > kFloor ? reach : low, kk, l);
     }
   }
-  // Fewer than k from `reach` on, in order: what comes below, value by value (after a mask mostly one), the lowest columns
-  // of a value first.
+  // Fewer than k from `reach` on, in order: what comes below, value by value (after a mask mostly one), the lowest
+  // columns of a value first.
   int have = found ? l.count : 0;
   for (int turn = 0; found && have < kk; ++turn) {
     found = turn < 2;
@@ -681,8 +683,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
         have += wave_n[v];
       }
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (e[j] == below && (i0 + tid) * N + j < n && at < kk) l.sorted[at++] = entry_of(below, lo + (i0 + tid) * N + j);
+      for (int j = 0; j < N; ++j) {
+        const int column = (i0 + tid) * N + j;
+        if (e[j] == below && column < n && at < kk) l.sorted[at++] = entry_of(below, lo + column);
+      }
       __syncthreads();
     }
   }
@@ -974,8 +978,8 @@ extern "C" int lora_token_top(const lora_mat* logits, const int32_t* targets, in
                    : l.shape.waves == 4  ? top_kernel<E, 4, 1024>
                    : l.shape.waves == 16 ? top_kernel<E, 16, 1024>
                                          : top_kernel<E, 8, 1024>;
-    launch(kernel, dim3(T * l.splits), dim3(64 * l.shape.waves), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
-           static_cast<int>(V), l.splits, l.piece, exponent_of(temperature), out, l.parts);
+    launch(kernel, dim3(T * l.splits), dim3(64 * l.shape.waves), 0, st, (const E*)logits->ptr, logits->stride_row,
+           targets, static_cast<int>(V), l.splits, l.piece, exponent_of(temperature), out, l.parts);
     if (l.splits > 1)
       launch(top_join_kernel<E>, dim3(T), dim3(256), 0, st, (const E*)logits->ptr, logits->stride_row, targets,
              static_cast<int>(V), l.splits, out, l.parts);

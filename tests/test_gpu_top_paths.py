@@ -29,7 +29,8 @@ def framed(x, pad=9, shift=3):
 # more, few rows in pieces, a long vocabulary, very few rows with 16 waves and what lies beside that
 TOPS = [(192, 49153, 1), (192, 49153, 20), (200, 32003, 64), (195, 70001, 20), (193, 128256, 100), (192, 128256, 128),
         (190, 60000, 20), (3, 300007, 64), (2, 49152, 128), (1, 2 ** 20 + 3, 5), (600, 3001, 128),
-        (1, 49153, 1), (4, 128256, 64), (3, 131071, 20), (5, 128256, 64), (2, 131073, 20), (1, 131072, 65)]
+        (1, 49153, 1), (4, 128256, 64), (3, 131071, 20), (5, 128256, 64), (2, 131073, 20), (1, 131072, 65),
+        (5, 2047, 128), (5, 1023, 128), (300, 2041, 127)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F])

@@ -116,6 +116,34 @@ def test_logits_far_from_zero(dtype, T, V, k):
         assert all(torch.equal(t[:9], t[i:i + 9]) for i in range(9, T, 9))
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("k", [0, 5, 100])
+@pytest.mark.parametrize("T", [2, 8, 200])
+def test_undefined_rows(dtype, T, k):
+    """NaN and infinities in rows of 16 waves, in rows of pieces (some of a piece whole) and in rows of one."""
+    note(f"top undefined {dtype} {T} {k}")
+    V = 128256
+    x, _ = make(8, V, dtype, 5)
+    x[0] = -float("inf")
+    x[1, V // 3] = float("inf")
+    x[2, V - 1] = NAN
+    x[3] = NAN
+    x[4, 50000:70000] = float("inf")
+    x[5, 50000:70000] = NAN
+    x[6, :V - 3] = -float("inf")
+    y = torch.full((8,), V - 2, device=DEV, dtype=torch.int32)
+    if T < 8:
+        parts = [L.lora_token_top(x[i:i + T], y[i:i + T], k, 1.5) for i in range(0, 8, T)]
+        out = tuple(torch.cat(p) for p in zip(*parts))
+    else:
+        out = L.lora_token_top(x.repeat(T // 8, 1), y.repeat(T // 8), k, 1.5)
+    for t in out:
+        for i in range(0, len(t), 8):
+            assert ((t[i:i + 6] == -1).all() if t.dtype == torch.int32 else torch.isnan(t[i:i + 6]).all())
+            assert torch.equal(t[i + 6:i + 8], t[6:8])
+    check(x[6:], y[6:], k, 1.5, tuple(t[6:8] for t in out))
+
+
 # rows that registers hold in part or whole, the same in pieces, rows longer than one workgroup takes
 DISTILLS = [(112, 70003, 64), (130, 128256, 33), (64, 40009, 100), (70, 128259, 8), (111, 128256, 16), (63, 50001, 256),
             (3, 262144, 5), (2, 300007, 64), (120, 20481, 3), (1, 49152, 1), (5, 8, 3)]

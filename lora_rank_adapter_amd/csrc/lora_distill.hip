@@ -261,8 +261,10 @@ struct OthersPass {
         if (tid + u * THREADS < body) largest(w[u], tid + u * THREADS);
     } else if (vecs > 0) {
       hold();
+      // of bfloat16 the first ones suffice; us a step, the first four and all: 2048 x 20000 bfloat16 42.2 and 44.1,
+      // 2048 x 10000 float32 42.2 and 39.3
 #pragma unroll
-      for (int h = 0; h < H; ++h)
+      for (int h = 0; h < (sizeof(E) == 2 && U < H ? U : H); ++h)
         if (tid + h * THREADS < vecs) largest(held[h], tid + h * THREADS);
     }
     if (left) m = fmaxf(m, last);
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(64 * WAVES, GRAD ? 4 : sizeof(E) == 2 ? 6 : 5) void
     const float* __restrict__ weights, float scale, E* dx, int64_t dx_stride) {
   // as many vectors as 128 registers leave room for, four waves' share of a row that they hold whole
   constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
-  constexpr int H = !GRAD ? 1 : WAVES == 4 ? 10 : sizeof(E) == 2 ? 15 : 16;
+  constexpr int H = !GRAD ? 1 : WAVES == 4 ? 10 : WAVES == 16 ? 14 : sizeof(E) == 2 ? 15 : 16;
   using V4 = typename Vec<E>::type;
   extern __shared__ uint4 dynamic[];
   __shared__ Tokens tokens;
@@ -590,9 +592,13 @@ static bool by_rows(const lora_mat* x) {
 // rows masked: 690 us with 8 waves, 727 with 16 (which leave registers for one
 // vector per lane) and 728 with 4. Of these 690 the second read takes 24, the
 // exponentials of the second pass 20; the rest is 3.6 GB at 5.5 TB/s.
-static int row_waves(const lora_mat* x) {
+// Up to 256 long rows, one to a CU, take 16 waves with 14 vectors per lane. us a
+// step of k = 64, 128256 columns, by 16 and by 8: bfloat16 128 rows 28.2 and
+// 30.2, 256 rows 33.8 and 35.2; float32 64 rows 28.0 and 30.4, 256 rows 56.6 and
+// 61.5. Without the gradient: bfloat16 128 rows 17.8 and 16.3.
+static int row_waves(const lora_mat* x, bool grad) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
-  return vecs <= 2560 ? 4 : 8;
+  return vecs <= 2560 ? 4 : grad && vecs > 8192 && x->rows <= 256 ? 16 : 8;
 }
 
 struct DistillPlan {
@@ -631,9 +637,11 @@ static void run_rows(const lora_mat* x, const lora_teacher* t, float* kl, float*
                      float scale, const lora_mat* dx, hipStream_t st) {
   by_type(x, [&](auto* e) {
     using E = std::remove_pointer_t<decltype(e)>;
-    const int waves = row_waves(x);
+    const int waves = row_waves(x, dx != nullptr);
     auto* kernel = dx == nullptr ? (waves == 4 ? distill_row_kernel<E, 4, false> : distill_row_kernel<E, 8, false>)
-                                 : (waves == 4 ? distill_row_kernel<E, 4, true> : distill_row_kernel<E, 8, true>);
+                   : waves == 4  ? distill_row_kernel<E, 4, true>
+                   : waves == 8  ? distill_row_kernel<E, 8, true>
+                                 : distill_row_kernel<E, 16, true>;
     launch(kernel, dim3(x->rows), dim3(64 * waves), bit_bytes(x->cols, Vec<E>::N), st, (const E*)x->ptr, x->stride_row,
            static_cast<int>(x->cols), teacher_of(t), exponent_of(t->temperature), kl, state, weights, scale,
            dx == nullptr ? (E*)nullptr : (E*)dx->ptr, dx == nullptr ? int64_t(0) : dx->stride_row);
@@ -674,13 +682,14 @@ extern "C" size_t lora_distill_workspace_bytes(int64_t T, int64_t V, int64_t k) 
   return plan_distill(T, V, k, nullptr).bytes;
 }
 
-// The checks that the divergence and the step share; `blocks`: workgroups of 64 * waves of the largest launch.
+// The checks that the divergence and the step share; `blocks`: workgroups of 64 * waves of the largest launch (16
+// waves take 256 rows at most).
 static int check_distill(const lora_mat* x, const lora_teacher* t) {
   if (int e = check_teacher(t, x->rows)) return e;
   if (x->cols > kMaxVocab) return LORA_ERR_LIMIT;
   const bool rows = by_rows(x);
   const int64_t blocks = rows ? x->rows : x->rows * piece_splits(x->rows, x->cols);
-  return blocks > max_blocks(rows ? 64 * row_waves(x) : 256) ? LORA_ERR_LIMIT : LORA_OK;
+  return blocks > max_blocks(rows ? 64 * row_waves(x, false) : 256) ? LORA_ERR_LIMIT : LORA_OK;
 }
 
 static int check_plan(const DistillPlan& l, void* ws, size_t bytes) {

@@ -146,7 +146,8 @@ def test_undefined_rows(dtype, T, k):
 
 # rows that registers hold in part or whole, the same in pieces, rows longer than one workgroup takes
 DISTILLS = [(112, 70003, 64), (130, 128256, 33), (64, 40009, 100), (70, 128259, 8), (111, 128256, 16), (63, 50001, 256),
-            (3, 262144, 5), (2, 300007, 64), (120, 20481, 3), (1, 49152, 1), (5, 8, 3)]
+            (3, 262144, 5), (2, 300007, 64), (120, 20481, 3), (1, 49152, 1), (5, 8, 3), (256, 128256, 64),
+             (257, 70001, 5), (113, 114696, 7), (112, 131100, 256), (64, 130001, 3)]
 
 
 @pytest.mark.parametrize("rest", [True, False])

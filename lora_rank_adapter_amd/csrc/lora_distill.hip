@@ -578,9 +578,10 @@ static int piece_splits(int64_t T, int64_t V) {
 // Whether one workgroup takes a whole row. A few long rows leave most of the
 // card idle so; in pieces they take three launches, and a second read of all.
 // us a step of k = 64, no row masked, by rows and in pieces:
-//   bfloat16  128256 columns: 1 row 27, 18; 96 rows 30.6, 29.2; 128 rows 31.1, 32.6; 256 rows 36, 50
+//   bfloat16  128256 columns: 1 row 27, 18; 80 rows 27.6, 24.9; 104 rows 27.6, 28.3; 128 rows 28.1, 32.6; 256 rows
+//            34, 50
 //            45000: 1 row 16.6, 18.2; 60000: 48 rows 21.2, 19.2; 32000: 192 rows 17.4, 23.5
-//   float32   128256: 48 rows 31, 29; 64 rows 32.4, 32.3; 96 rows 35, 41
+//   float32   128256: 32 rows 27.2, 21.5; 48 rows 27.8, 25.0; 64 rows 27.9, 32.3; 96 rows 35, 41
 // and of the divergence alone: bfloat16 64 rows 16.9, 15.4; 96 rows 17.0, 17.6.
 static bool by_rows(const lora_mat* x) {
   if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;

@@ -243,9 +243,9 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // Memory bounds many rows: 5744 of 8192 x 128256 bfloat16 without alternatives
 // 234 us (6.3 TB/s; the loop's vector instructions went from 69 to 53 for 8
 // logits without a change), 4096 with k = 64 195 us (5.4 TB/s: of a workgroup's
-// 40 us half go into the threshold and the selection, when only others load). 256 rows are one workgroup per CU: reading
-// takes 13 of the 21 us, the first loads, the threshold and the selection the
-// rest.
+// 40 us half go into the threshold and the selection, when only others load).
+// 256 rows are one workgroup per CU: reading takes 13 of the 21 us, the first
+// loads, the threshold and the selection the rest.
 // ---------------------------------------------------------------------------
 
 constexpr float kAbove = 64.0f;  // binary orders that the largest logit may be away from the reference

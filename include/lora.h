@@ -527,7 +527,8 @@ int lora_policy_step(const lora_mat* logits, const lora_policy* policy, float gr
  * A row that holds a NaN or +inf, or nothing above -inf, has no probabilities:
  * NaN in every output, ids -1.
  * One pass over the logits, but for rows in orders or with masks that a list of
- * some hundred candidates does not hold. V at most 2^22, below 2^23 rows where k
+ * some hundred candidates does not hold, and for logits of more than some 10^7
+ * temperatures. V at most 2^22, below 2^23 rows where k
  * and V ask for long lists (2^24 otherwise); LORA_ERR_LIMIT above.
  *
  * Workspace: 256-byte aligned; 0 for sizes beyond the limits.

@@ -490,14 +490,31 @@ __global__ __launch_bounds__(256) void distill_join_kernel(int V, int splits, Te
   put_row(kl, state, t, row, m, finish_row<4>(t, V, all, id, mine, logq, tokens));
 }
 
+// A row without a token is masked: its divergence is 0 and its weight is not
+// used, which shows only where that is not finite. Such a weight on a divergence
+// of 0 is rare, and only then the row's ids are looked at.
 template <int WAVES>
-__device__ __forceinline__ void sum_losses(const float* kl, const float* weights, int64_t T, float* loss) {
+__device__ __forceinline__ void sum_losses(const float* kl, const float* weights, int64_t T, const int32_t* ids, int k,
+                                           int V, float* loss) {
   __shared__ double lds[WAVES];
   double sum = 0.0;
+  bool ask = false;
 #pragma unroll 8
   for (int64_t t = threadIdx.x; t < T; t += 64 * WAVES) {
     const float w = weights[t];
-    if (w != 0.0f) sum += (double)w * kl[t];
+    if (w != 0.0f) {
+      const float v = kl[t];
+      const bool plain = v != 0.0f || fabsf(w) < INFINITY;
+      sum += plain ? (double)w * v : 0.0;
+      ask = ask || !plain;
+    }
+  }
+  if (ask) {
+    for (int64_t t = threadIdx.x; t < T; t += 64 * WAVES) {
+      if (kl[t] != 0.0f || fabsf(weights[t]) < INFINITY) continue;
+      for (int i = 0; i < k; ++i)
+        if (static_cast<unsigned>(ids[t * k + i]) < (unsigned)V) sum = NAN;  // not masked: 0 times NaN or infinity
+    }
   }
   sum = block_sum<WAVES>(sum, lds);
   if (threadIdx.x == 0) *loss = static_cast<float>(sum);
@@ -505,8 +522,9 @@ __device__ __forceinline__ void sum_losses(const float* kl, const float* weights
 
 __global__ __launch_bounds__(1024) void distill_sum_kernel(const float* __restrict__ kl,
                                                            const float* __restrict__ weights, int64_t T,
+                                                           const int32_t* __restrict__ ids, int k, int V,
                                                            float* __restrict__ loss) {
-  sum_losses<16>(kl, weights, T, loss);
+  sum_losses<16>(kl, weights, T, ids, k, V, loss);
 }
 
 // A workgroup takes one piece of a row, a vector per lane; the entries at the
@@ -521,7 +539,7 @@ __global__ __launch_bounds__(kGradVecs) void distill_grad_kernel(GradArgs<E> a, 
                                                                  float* __restrict__ loss) {
   constexpr int N = Vec<E>::N;
   const int64_t row = blockIdx.x / (unsigned)a.pieces;
-  if (row == T) return sum_losses<kGradVecs / 64>(kl, coef, T, loss);
+  if (row == T) return sum_losses<kGradVecs / 64>(kl, coef, T, ids, k, a.V, loss);
   const int lo = (blockIdx.x % (unsigned)a.pieces) * kGradVecs * N;
   const int n = a.V - lo < kGradVecs * N ? a.V - lo : kGradVecs * N;
   const int tid = threadIdx.x;
@@ -753,6 +771,7 @@ extern "C" int lora_distill_step(const lora_mat* logits, const lora_teacher* tea
   if (T > 0)
     run_rows(logits, teacher, kl, nullptr, weights, static_cast<float>((double)grad_scale / teacher->temperature),
              dlogits, st);
-  launch(distill_sum_kernel, dim3(1), dim3(1024), 0, st, (const float*)kl, weights, T, loss);
+  launch(distill_sum_kernel, dim3(1), dim3(1024), 0, st, (const float*)kl, weights, T, teacher->ids,
+         static_cast<int>(teacher->k), static_cast<int>(V), loss);
   return launch_status();
 }

@@ -228,14 +228,15 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // vectors that reach it can matter. They go to a list in LDS, together with
 // those of the rest of the row, a few hundred in all, and the k largest are
 // found among them. The sums are relative to the largest logit of these first
-// elements, which a row's largest one exceeds by little: no running maximum.
+// elements, no running maximum, but for the vectors that reach it: these are
+// listed, and summed behind the loop relative to the largest of their wave. So no
+// exponent is far above its reference, which would cost it precision.
 //
-// Where that does not hold the row is read again: for the sums if the largest
-// logit is 64 binary orders away from the reference, or that far from 0; for the
-// alternatives if the list overflows (logits that rise along the row, a masked
-// beginning: from the k-th of the lanes' largest in the whole row on) or holds
-// fewer than k (ties without end, a vocabulary masked down to a few tokens: the
-// lowest columns of the next value).
+// The row is read again: for the sums if the reference is 2^24 binary orders away
+// from 0, or not all that reach it are listed; for the alternatives if the list
+// overflows (logits that rise along the row, a masked beginning: from the k-th of
+// the lanes' largest in the whole row on) or holds fewer than k (ties without end,
+// a vocabulary masked down to a few tokens: the lowest columns of the next value).
 // us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21, rising 50,
 // one value throughout 73, masked down to 5 tokens 44, masked in their first
 // half 46.
@@ -248,7 +249,6 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // loads, the threshold and the selection the rest.
 // ---------------------------------------------------------------------------
 
-constexpr float kAbove = 64.0f;  // binary orders that the largest logit may be away from the reference
 constexpr float kFar = 0x1p24f;  // binary orders that the reference may be away from 0
 constexpr int kMaxSplits = 64;
 
@@ -549,7 +549,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
     });
   };
 
-  // The k largest, and the sums of the late vectors: of those a lane keeps the one with its largest logit apart.
+  // The k largest, and the sums of the late vectors, relative to the wave's largest: of those a lane keeps the one with
+  // its largest logit apart.
+  const float most = lane_max(mine), ref = at_max(most);
+  auto from_most = [&](float f) { return s.of(f - ref); };
   double late_sum, late_wsum;
   VecSums held;
   V4 held_v;
@@ -591,7 +594,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
 #pragma unroll
         for (int j = 0; j < N; ++j) bits |= there && e[j] >= reach && at * N + j < n ? 1u << j : 0u;
         if (there && m >= first) {
-          VecSums t = vec_sums<E>(v, exponent);
+          VecSums t = vec_sums<E>(v, from_most);
           if (m > held_m || (m == held_m && at < held_at)) {
             const VecSums before = held;
             held = t;
@@ -619,7 +622,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   over = over || !listed;
   bool found = listed;
   if (listed) {
-    const float most = lane_max(mine);
     if ((tid & 63) == 0) wave_hi[tid >> 6] = most;
     __syncthreads();
     if (candidates <= kDirect) {
@@ -698,8 +700,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   const float m = n > 0 ? value_of(static_cast<uint32_t>(l.sorted[0] >> 32)) : -INFINITY;
 
   // the sums over all but the largest
-  const bool far = !(fabsf(s.of(m - z)) <= kAbove) || !(fabsf(shift) <= kFar);
-  const bool again = m > -INFINITY && (over || far);
+  // below kFloor nothing was listed behind a beginning of -inf
+  const bool again = m > -INFINITY && (over || m < kFloor || !(fabsf(shift) <= kFar));
   const LeftOut<E> without_top(top, vecs);
   auto from_m = [&](float f) { return s.of(f - m); };
   if (again) {
@@ -713,10 +715,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
   } else {
     if (held_at >= 0 && held_at == top / N) {
       without_top.template from<1>(&held_v, held_at, 1);
-      held = vec_sums<E>(held_v, exponent);
+      held = vec_sums<E>(held_v, from_most);
     }
-    sum += late_sum + held.s;
-    wsum += late_wsum + held.w;
+    // Both to the largest logit: its exponent relative to the first elements' is d, where there are some above -inf
+    // (all is late otherwise); the wave's, relative to it, is b, where there is a late vector.
+    const float d = first > -INFINITY ? (float)((double)m * s.hi + ((double)m * s.lo + shift)) : 0.0f;
+    const float by = __builtin_amdgcn_exp2f(-d);
+    late_sum += held.s;
+    late_wsum += held.w;
+    const float b = late_sum == 0.0 ? 0.0f : s.of(ref - m), late_by = __builtin_amdgcn_exp2f(b);
+    wsum = by == 0.0f ? 0.0 : (wsum - d * sum) * by;
+    sum *= by;
+    if (late_by > 0.0f) wsum += (late_wsum + b * late_sum) * late_by;
+    sum += late_sum * late_by;
   }
   sum = lane_total(sum);
   wsum = lane_total(wsum);
@@ -730,12 +741,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
       sum += wave_s[v];
       wsum += wave_w[v];
     }
-    double d = 0.0;  // the largest logit's exponent
-    if (!again && m > -INFINITY) d = (double)m * s.hi + ((double)m * s.lo + shift);
-    const double one = exp2(d);
     // with nothing above -inf the sum is 0 or NaN; m is NaN where nothing could be compared
     if (m > -INFINITY)
-      shared = {m, sum / one, (sum * d - wsum) * kLn2 / one};
+      shared = {m, sum, -wsum * kLn2};
     else
       shared = {m, m == -INFINITY ? sum : NAN, 0.0};
   }

@@ -23,6 +23,7 @@
 //   distill_grad_kernel   the gradient's rows from that
 //   distill_sum_kernel    the weighted sum of the rows' divergences
 
+#include <cfloat>
 #include <type_traits>
 
 #include "lora_softmax.hpp"
@@ -42,7 +43,7 @@ struct Teacher {
 
 // A row's elements that the teacher did not name.
 struct Others {
-  float m;   // what the exponents are relative to
+  float m;   // what the exponents are relative to: the largest x, or kStep binary orders below it at most
   double s;  // sum of exp((x - m) / tau)
 };
 
@@ -203,20 +204,22 @@ __device__ __forceinline__ float block_max(float v, float* lds) {
   return v;
 }
 
-constexpr float kAbove = 64.0f;  // binary orders that a logit may be above the reference
-
 template <int WAVES>
 struct PassLds {
-  float first[WAVES], most[WAVES];
+  float first[WAVES], refs[WAVES];
   double sum[WAVES];
 };
 
 // One pass over n elements from p on, but for those whose bits are set. The
 // exponents are relative to the largest of the first vectors, which the others
-// exceed by little: no running maximum. Where one is kAbove binary orders
-// larger the elements are read anew. The last H vectors per lane stay in
-// `held` (as read), the elements past the last vector in `last`. AGAIN: the
-// elements will be read once more.
+// seldom exceed: no running maximum. An exponent far above the reference loses
+// precision, so a lane that meets a logit more than kStep binary orders above its
+// own takes that instead, scales its sum and reads those vectors anew. At a step
+// of one order that happens about twice in a row of 128256 random logits, which
+// costs 2048 such rows 2.5 of 71 us; at two it is not to be measured. The last H
+// vectors per lane stay in `held` (as read), the elements past the last vector in
+// `last`. AGAIN: the elements will be read once more.
+constexpr float kStep = 2.0f;
 template <class E, int WAVES, int H, bool AGAIN>
 struct OthersPass {
   static constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
@@ -269,8 +272,10 @@ struct OthersPass {
     }
     if (left) m = fmaxf(m, last);
     m = block_max<WAVES>(m, lds.first);
-    const float first = m;
-    float z = at_max(m);
+    // with nothing above -inf so far the first logit that is replaces it
+    m = fmaxf(m, -FLT_MAX);
+    float z = m;
+    const float step = kStep / s.hi;
     double sum = 0.0;
     auto take = [&](V4 v, uint32_t off) {
       float f[N];
@@ -280,10 +285,19 @@ struct OthersPass {
       for (int e = 0; e < N; ++e) m = fmaxf(m, f[e]);
       sum += sum_exp<N>(f, z, s);
     };
+    // Behind some vectors, `count` of them from i on and up to `end`: the sum anew from what it was before them, if one
+    // is a step above the reference. Read again for it: kept until here they would spill, or take the next ones' room.
+    auto settle = [&](double was, int i, int count, int end) {
+      if (!(m > z + step)) return;
+      sum = was * __builtin_amdgcn_exp2f(s.of(z - m));
+      z = m;
+#pragma unroll 1
+      for (int u = 0; u < count && i < end; ++u, i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
+    };
     if (left) sum += __builtin_amdgcn_exp2f(s.of(last - z));
     if (body > 0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u)  // none is above the reference
         if (tid + u * THREADS < body) take(w[u], byte[tid + u * THREADS]);
       int i = tid + U * THREADS;
       uint32_t off[U];  // the vectors' bits, read before the first is used
@@ -294,10 +308,16 @@ struct OthersPass {
             w[u] = load(p + (int64_t)(i + u * THREADS) * N);
             off[u] = byte[i + u * THREADS];
           }
+          const double was = sum;
 #pragma unroll
           for (int u = 0; u < U; ++u) take(w[u], off[u]);
+          settle(was, i, U, body);
         }
-        for (; i < body; i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
+        for (; i < body; i += THREADS) {
+          const double was = sum;
+          take(load(p + (int64_t)i * N), byte[i]);
+          settle(was, i, 1, body);
+        }
       } else {
         // the next four vectors on their way; with the held ones beside them that would spill
         V4 a[U];
@@ -311,30 +331,35 @@ struct OthersPass {
             a[u] = load(p + before(i + (u + U) * THREADS, body));
           }
           sched_fence();
+          const double was = sum;
 #pragma unroll
           for (int u = 0; u < U; ++u) take(w[u], off[u]);
+          settle(was, i, U, body);
         }
+        const double was = sum;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (i + u * THREADS < body) take(a[u], byte[i + u * THREADS]);
+        settle(was, i, U, body);
       }
       hold();
     }
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (body + tid + h * THREADS < vecs) take(held[h], byte[body + tid + h * THREADS]);
-    m = block_max<WAVES>(m, lds.most);
-    if (s.of(m - z) > kAbove || (first == -INFINITY && m > -INFINITY)) {
-      z = m;
-      sum = left ? __builtin_amdgcn_exp2f(s.of(last - z)) : 0.0;
-      for (int i = tid; i < vecs; i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
+    for (int g = 0; g < H; g += U) {
+      const double was = sum;
+#pragma unroll
+      for (int h = g; h < g + U && h < H; ++h)
+        if (body + tid + h * THREADS < vecs) take(held[h], byte[body + tid + h * THREADS]);
+      settle(was, body + tid + g * THREADS, U, vecs);
     }
+    m = block_max<WAVES>(z, lds.refs);
+    if (sum > 0.0) sum *= __builtin_amdgcn_exp2f(s.of(z - m));
     sum = lane_total(sum);
     if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;
     __syncthreads();
     sum = 0.0;
     for (int v = 0; v < WAVES; ++v) sum += lds.sum[v];
-    return {z, sum};
+    return {m, sum};
   }
 };
 

@@ -619,16 +619,30 @@ static int piece_splits(int64_t T, int64_t V) {
 }
 
 // Whether one workgroup takes a whole row. A few long rows leave most of the
-// card idle so; in pieces they take three launches, and a second read of all.
-// us a step of k = 64, no row masked, by rows and in pieces:
-//   bfloat16  128256 columns: 1 row 27, 18; 80 rows 27.6, 24.9; 104 rows 27.6, 28.3; 128 rows 28.1, 32.6; 256 rows
-//            34, 50
-//            45000: 1 row 16.6, 18.2; 60000: 48 rows 21.2, 19.2; 32000: 192 rows 17.4, 23.5
-//   float32   128256: 32 rows 27.2, 21.5; 48 rows 27.8, 25.0; 64 rows 27.9, 32.3; 96 rows 35, 41
-// and of the divergence alone: bfloat16 64 rows 16.9, 15.4; 96 rows 17.0, 17.6.
-static bool by_rows(const lora_mat* x) {
+// card idle so; in pieces they take two launches, and three with the gradient,
+// which reads all for a second time. us by rows and in pieces, k = 64, no row
+// masked; the divergence alone:
+//   bfloat16   80000 columns: 8 rows 13.2, 14.1; 96 rows 14.1, 15.0
+//             100000: 64 rows 15.3, 14.3; 96 rows 15.5, 15.7; 128 rows 16.1, 16.5; 160 rows 16.3, 18.2
+//             128256: 64 rows 17.5, 14.7; 112 rows 18.0, 16.9; 128 rows 17.7, 17.6; 160 rows 18.2, 19.3
+//             200000: 128 rows 23.0, 20.7; 160 rows 23.4, 23.5; 192 rows 23.9, 24.6
+//   float32    64000: 8 rows 13.0, 14.2; 96 rows 14.6, 15.5
+//              80000: 64 rows 15.8, 14.7; 96 rows 16.1, 15.9; 128 rows 16.8, 17.0
+//             128256: 96 rows 20.5, 18.9; 128 rows 21.4, 20.9; 160 rows 22.2, 23.8
+// and a step:
+//   bfloat16   32000: 8 rows 15.7, 17.9; 50000: 8 rows 17.3, 17.5; 48 rows 18.2, 17.8; 96 rows 18.5, 20.7
+//              64000: 48 rows 20.4, 17.9; 96 rows 21.0, 22.0
+//             100000: 80 rows 26.6, 24.1; 96 rows 26.6, 26.0; 112 rows 27.1, 27.6; 128 rows 27.2, 29.3
+//             128256: 80 rows 28.1, 26.1; 96 rows 27.9, 28.4; 112 rows 28.4, 30.0
+//             200000: 96 rows 37.5, 36.1; 112 rows 38.3, 38.3; 128 rows 38.6, 41.7
+//   float32    32000: 8 rows 16.0, 17.5; 50000: 24 rows 20.5, 17.7; 48 rows 21.0, 19.9; 64 rows 21.0, 21.5
+//             128256: 48 rows 28.6, 26.0; 64 rows 28.5, 29.6
+// Rows of kMaxPieceVecs vectors and more go in pieces however many they are.
+static bool by_rows(const lora_mat* x, bool grad) {
+  const bool f32 = x->dtype == LORA_F32;
   if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;
-  return x->cols <= 49152 || x->rows >= (x->dtype == LORA_F32 ? 64 : 112);
+  if (grad) return x->cols <= 49152 || x->rows >= (f32 ? 64 : 104);
+  return x->cols <= (f32 ? 65536 : 81920) || x->rows >= 144;
 }
 
 // Waves to a row: with the gradient eight keep 7680 of its vectors in registers
@@ -728,10 +742,10 @@ extern "C" size_t lora_distill_workspace_bytes(int64_t T, int64_t V, int64_t k) 
 
 // The checks that the divergence and the step share; `blocks`: workgroups of 64 * waves of the largest launch (16
 // waves take 256 rows at most).
-static int check_distill(const lora_mat* x, const lora_teacher* t) {
+static int check_distill(const lora_mat* x, const lora_teacher* t, bool grad) {
   if (int e = check_teacher(t, x->rows)) return e;
   if (x->cols > kMaxVocab) return LORA_ERR_LIMIT;
-  const bool rows = by_rows(x);
+  const bool rows = by_rows(x, grad);
   const int64_t blocks = rows ? x->rows : x->rows * piece_splits(x->rows, x->cols);
   return blocks > max_blocks(rows ? 64 * row_waves(x, false) : 256) ? LORA_ERR_LIMIT : LORA_OK;
 }
@@ -744,14 +758,14 @@ extern "C" int lora_distill_kl(const lora_mat* logits, const lora_teacher* teach
                                void* workspace, size_t workspace_bytes, void* stream) {
   if (!logits) return LORA_ERR_NULL;
   if (int e = check_logits(logits)) return e;
-  if (int e = check_distill(logits, teacher)) return e;
+  if (int e = check_distill(logits, teacher, false)) return e;
   const int64_t T = logits->rows, V = logits->cols;
   if (T == 0) return LORA_OK;
   if (!kl || (V > 0 && !logits->ptr)) return LORA_ERR_NULL;
   const DistillPlan l = plan_distill(T, V, teacher->k, workspace);
   if (int e = check_plan(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
-  if (by_rows(logits))
+  if (by_rows(logits, false))
     run_rows(logits, teacher, kl, state, nullptr, 0.0f, nullptr, st);
   else
     run_pieces(logits, teacher, l, kl, state, st);
@@ -781,13 +795,13 @@ extern "C" int lora_distill_step(const lora_mat* logits, const lora_teacher* tea
   if (int e = check_logits(logits)) return e;
   if (int e = check_dlogits(logits, dlogits)) return e;
   const int64_t T = logits->rows, V = logits->cols;
-  if (int e = check_distill(logits, teacher)) return e;
+  if (int e = check_distill(logits, teacher, true)) return e;
   if (!loss || (T > 0 && (!weights || !kl || (V > 0 && (!logits->ptr || !dlogits->ptr))))) return LORA_ERR_NULL;
   const DistillPlan l = plan_distill(T, V, teacher->k, workspace);
   if (T > 0)
     if (int e = check_plan(l, workspace, workspace_bytes)) return e;
   auto st = static_cast<hipStream_t>(stream);
-  if (T > 0 && V > 0 && !by_rows(logits)) {
+  if (T > 0 && V > 0 && !by_rows(logits, true)) {
     run_pieces(logits, teacher, l, kl, l.state, st);
     run_grad(logits, teacher->ids, static_cast<int>(teacher->k), l.state, weights, nullptr, grad_scale,
              teacher->temperature, dlogits, kl, loss, st);

@@ -903,12 +903,18 @@ static TopShape top_shape(int64_t piece, int k) {
 }
 
 // Whether 16 waves take each of very few rows whole: one launch in place of two,
-// which the host's time decides; kernels of rows in pieces take about as long.
-// us a call so and in pieces, bfloat16: 1 x 128256, k = 5, 16.2 and 19.1, k = 20
-// 17.1 and 19.1, k = 64 18.5 and 19.2, k = 128 20.1 and 19.0; 1 x 60000, k = 20,
-// 16.2 and 19.2; 8 x 128256, k = 64, 19.9 and 19.4; 1 x 200000, k = 5, 21.7 and
-// 19.1; float32 1 x 128256, k = 5, 17.1 and 19.1.
-static bool very_few(int64_t T, int64_t V, int64_t k) { return T <= 4 && V > 49152 && V <= 131072 && k <= 64; }
+// which the host's time decides (15 us a call, and 18 with the second launch);
+// kernels of rows in pieces take about as long. us a call so and in pieces:
+//   bfloat16   65536 columns: 1 row, k 20, 15.4 and 18.2; 16 rows, k 5, 15.1 and 18.0, k 128 17.5 and 18.7
+//             100000: 1 row, k 5, 15.8 and 17.9, k 20 17.5 and 18.2, k 64 19.0 and 17.9; 16 rows, k 5, 17.6 and 17.9
+//             128256: 1 row, k 5, 16.4 and 17.8, k 20 18.2 and 18.2, k 64 19.3 and 18.1; 16 rows, k 5, 17.8 and 17.9,
+//             k 20 19.3 and 18.2
+//             140000: 1 row, k 5, 18.3 and 17.9
+//   float32    65536: 1 row, k 20, 15.2 and 18.3; 16 rows, k 128, 18.3 and 18.7
+//             128256: 1 row, k 5, 17.3 and 17.8, k 20 18.6 and 18.2; 16 rows, k 5, 18.3 and 18.1
+static bool very_few(int64_t T, int64_t V, int64_t k) {
+  return T <= 16 && V > 49152 && V <= (k <= 8 ? 131072 : 65536);
+}
 
 // Pieces of a row: one, or of few long rows about as many as give 1024
 // workgroups, of at least 8192 logits each; at most what a list has room for. us

@@ -600,8 +600,9 @@ int lora_distill_grad(const lora_mat* logits, const int32_t* top_ids, int64_t k,
  *   a weight of 0 drops its term, also where kl is infinite or NaN, and a
  *   masked row's weight is not used), kl as above, dlogits the gradient of the
  *   loss times grad_scale. Also with T = 0 the loss is written. A row's sums may
- *   be taken in another order than by lora_distill_kl (a long row is read from
- *   memory once).
+ *   be taken in another order than by lora_distill_kl. Many rows, of less than
+ *   32768 vectors of 16 bytes each, are read from memory once; longer ones, and
+ *   few long ones, twice.
  */
 int lora_distill_step(const lora_mat* logits, const lora_teacher* teacher, const float* weights, float grad_scale,
                       float* loss, float* kl, const lora_mat* dlogits, void* workspace, size_t workspace_bytes,

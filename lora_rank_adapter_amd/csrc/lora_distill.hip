@@ -637,7 +637,10 @@ static int piece_splits(int64_t T, int64_t V) {
 //             200000: 96 rows 37.5, 36.1; 112 rows 38.3, 38.3; 128 rows 38.6, 41.7
 //   float32    32000: 8 rows 16.0, 17.5; 50000: 24 rows 20.5, 17.7; 48 rows 21.0, 19.9; 64 rows 21.0, 21.5
 //             128256: 48 rows 28.6, 26.0; 64 rows 28.5, 29.6
-// Rows of kMaxPieceVecs vectors and more go in pieces however many they are.
+// Rows of kMaxPieceVecs vectors and more (131072 float32, 262144 bfloat16) go in
+// pieces however many they are: a workgroup's bits have no room for them. That
+// costs many rows a second read from memory; us a step of 4096 rows right below
+// and at that limit: float32 970, 1063; bfloat16 976, 1093.
 static bool by_rows(const lora_mat* x, bool grad) {
   const bool f32 = x->dtype == LORA_F32;
   if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;
@@ -646,14 +649,14 @@ static bool by_rows(const lora_mat* x, bool grad) {
 }
 
 // Waves to a row: with the gradient eight keep 7680 of its vectors in registers
-// (8192 of float32), four 2560. 8192 x 128256 bfloat16, k = 64, a third of the
-// rows masked: 690 us with 8 waves, 727 with 16 (which leave registers for one
-// vector per lane) and 728 with 4. Of these 690 the second read takes 24, the
-// exponentials of the second pass 20; the rest is 3.6 GB at 5.5 TB/s.
-// Up to 256 long rows, one to a CU, take 16 waves with 14 vectors per lane. us a
-// step of k = 64, 128256 columns, by 16 and by 8: bfloat16 128 rows 28.2 and
-// 30.2, 256 rows 33.8 and 35.2; float32 64 rows 28.0 and 30.4, 256 rows 56.6 and
-// 61.5. Without the gradient: bfloat16 128 rows 17.8 and 16.3.
+// (8192 of float32), four 2560, sixteen 14336. us a step of 8192 x 128256
+// bfloat16, k = 64, a third of the rows masked, by 4, 8 and 16 waves: 758, 690
+// and 785 (one workgroup of 16 to a CU leaves nothing beside its serial part).
+// Of these 690 the second read takes 24, the exponentials of the second pass 20;
+// the rest is 3.6 GB at 5.5 TB/s. Up to 256 long rows, one to a CU, take 16
+// waves. us a step of k = 64, 128256 columns, by 16 and by 8: bfloat16 128 rows
+// 26.9 and 28.4, 256 rows 31.1 and 36.0; float32 64 rows 27.9 and 32.5, 256 rows
+// 57.5 and 62.8. Without the gradient: bfloat16 128 rows 17.8 and 16.3.
 static int row_waves(const lora_mat* x, bool grad) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
   return vecs <= 2560 ? 4 : grad && vecs > 8192 && x->rows <= 256 ? 16 : 8;

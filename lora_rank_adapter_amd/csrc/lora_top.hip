@@ -237,13 +237,13 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // overflows (logits that rise along the row, a masked beginning: from the k-th of
 // the lanes' largest in the whole row on) or holds fewer than k (ties without end,
 // a vocabulary masked down to a few tokens: the lowest columns of the next value).
-// us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21, rising 50,
-// one value throughout 73, masked down to 5 tokens 44, masked in their first
+// us a call of 256 rows of 128256 bfloat16, k = 20: random logits 21, rising 48,
+// one value throughout 71, masked down to 5 tokens 44, masked in their first
 // half 46.
 //
 // Memory bounds many rows: 5744 of 8192 x 128256 bfloat16 without alternatives
-// 234 us (6.3 TB/s; the loop's vector instructions went from 69 to 53 for 8
-// logits without a change), 4096 with k = 64 195 us (5.4 TB/s: of a workgroup's
+// 233 us (6.3 TB/s; the loop's vector instructions went from 69 to 53 for 8
+// logits without a change), 4096 with k = 64 197 us (5.3 TB/s: of a workgroup's
 // 40 us half go into the threshold and the selection, when only others load).
 // 256 rows are one workgroup per CU: reading takes 13 of the 21 us, the first
 // loads, the threshold and the selection the rest.

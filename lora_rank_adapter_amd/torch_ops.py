@@ -34,6 +34,8 @@ Ops (the addressing arrays are passed as the tensors of lora_addressing):
   token_top_grad(logits, targets, stats, dlogp, dentropy, temperature) -> dlogits
   distill_kl(logits, top_ids, top_logp, temperature, rest) -> (kl, state)   (kl differentiable in logits)
   distill_grad(logits, top_ids, state, coef, temperature) -> dlogits
+                                                            (divergence and gradient read the logits once each;
+                                                            train.lora_distill_step, which is no op here, once in all)
 
 h from shrink and gather_shrink is zero where the op leaves it unspecified
 (inactive tokens, columns past a slot's rank), and sorted_tokens from

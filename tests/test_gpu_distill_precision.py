@@ -52,7 +52,8 @@ def tight(x64, ids, logp, tau, rest, coef, dtype):
         p_r = p[other].sum()
         q_r = max(0.0, 1 - q.sum()) if rest and other.any() else 0.0
         Q = q.sum() + q_r
-        u = np.where(other, (z[other].max() if other.any() else 0.0) - z, 0.0)
+        with np.errstate(invalid="ignore"):  # -inf less -inf
+            u = np.where(other, (z[other].max() if other.any() else 0.0) - z, 0.0)
         u = np.where(np.isfinite(u), u, 0.0)
         share = np.where(other & (p_r > 0), p / (p_r or 1.0), 0.0)
         e_o = (share * (9 * H * u + 18 * H)).sum()

@@ -43,7 +43,7 @@ struct Teacher {
 
 // A row's elements that the teacher did not name.
 struct Others {
-  float m;   // what the exponents are relative to: the largest x, or kStep binary orders below it at most
+  float m;   // what the exponents are relative to: the largest x
   double s;  // sum of exp((x - m) / tau)
 };
 
@@ -206,20 +206,21 @@ __device__ __forceinline__ float block_max(float v, float* lds) {
 
 template <int WAVES>
 struct PassLds {
-  float first[WAVES], refs[WAVES];
+  float first[WAVES], most[WAVES];
   double sum[WAVES];
 };
 
 // One pass over n elements from p on, but for those whose bits are set. The
-// exponents are relative to the largest of the first vectors, which the others
-// seldom exceed: no running maximum. An exponent far above the reference loses
-// precision, so a lane that meets a logit more than kStep binary orders above its
-// own takes that instead, scales its sum and reads those vectors anew. At a step
-// of one order that happens about twice in a row of 128256 random logits, which
-// costs 2048 such rows 2.5 of 71 us; at two it is not to be measured. The last H
-// vectors per lane stay in `held` (as read), the elements past the last vector in
+// exponents are relative to kAbove binary orders above the largest of the first
+// vectors, which the others seldom reach: no running maximum. An exponent far
+// above the reference loses precision, so a lane that meets a logit above its own
+// moves it kAbove orders above that one, scales its sum and reads those vectors
+// anew. At 3 orders one in eight rows of 128256 random logits has such a lane; at
+// one nearly every row had, which took 2.5 of the 71 us of 2048 such rows. The last
+// H vectors per lane stay in `held` (as read), the elements past the last vector in
 // `last`. AGAIN: the elements will be read once more.
-constexpr float kStep = 2.0f;
+constexpr float kAbove = 3.0f;
+
 template <class E, int WAVES, int H, bool AGAIN>
 struct OthersPass {
   static constexpr int N = Vec<E>::N, U = 4, THREADS = 64 * WAVES;
@@ -274,8 +275,8 @@ struct OthersPass {
     m = block_max<WAVES>(m, lds.first);
     // with nothing above -inf so far the first logit that is replaces it
     m = fmaxf(m, -FLT_MAX);
-    float z = m;
-    const float step = kStep / s.hi;
+    const float above = kAbove / s.hi;
+    float z = m + above;
     double sum = 0.0;
     auto take = [&](V4 v, uint32_t off) {
       float f[N];
@@ -286,13 +287,22 @@ struct OthersPass {
       sum += sum_exp<N>(f, z, s);
     };
     // Behind some vectors, `count` of them from i on and up to `end`: the sum anew from what it was before them, if one
-    // is a step above the reference. Read again for it: kept until here they would spill, or take the next ones' room.
+    // is above the reference. Read again for it: kept until here they would spill, or take the next ones' room.
     auto settle = [&](double was, int i, int count, int end) {
-      if (!(m > z + step)) return;
-      sum = was * __builtin_amdgcn_exp2f(s.of(z - m));
-      z = m;
+      if (!(m > z)) return;
+      sum = was * __builtin_amdgcn_exp2f(s.of(z - (m + above)));
+      z = m + above;
+      if constexpr (AGAIN) {
 #pragma unroll 1
-      for (int u = 0; u < count && i < end; ++u, i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
+        for (int u = 0; u < count && i < end; ++u, i += THREADS) take(load(p + (int64_t)i * N), byte[i]);
+      } else {
+        V4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = load(p + before(i + u * THREADS, end));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u < count && i + u * THREADS < end) take(v[u], byte[i + u * THREADS]);
+      }
     };
     if (left) sum += __builtin_amdgcn_exp2f(s.of(last - z));
     if (body > 0) {
@@ -352,7 +362,7 @@ struct OthersPass {
         if (body + tid + h * THREADS < vecs) take(held[h], byte[body + tid + h * THREADS]);
       settle(was, body + tid + g * THREADS, U, vecs);
     }
-    m = block_max<WAVES>(z, lds.refs);
+    m = block_max<WAVES>(m, lds.most);
     if (sum > 0.0) sum *= __builtin_amdgcn_exp2f(s.of(z - m));
     sum = lane_total(sum);
     if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;

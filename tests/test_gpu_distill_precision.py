@@ -2,12 +2,14 @@
 however little the tokens outside the teacher's hold.
 
 Bounds (H = 2^-24), none of them absolute but for underflow. The others'
-exponentials are float32, relative to a logit within two binary orders of the
-largest that its lane has seen, in trees of eight terms (3 H); a lane that meets
-a larger one scales what it has, and all are scaled to one reference at the end.
-u is an other logit's distance (over tau) below the largest of the others:
-    one term: exponents of 2 H by what they bridge, its own u and two orders, the steps' together as much, the last one
-    two orders: 2 H (2 u + 4.2); 2 H for each exponential: its own, the steps' (u / ln(4) + 1), the last; the tree's 3 H:
+exponentials are float32, relative to a reference that no logit of the lane so
+far exceeds and that lies three binary orders above the largest of them or of the
+row's beginning, in trees of eight terms (3 H); a lane that meets a larger logit
+moves its reference and scales what it has, and all are scaled to the largest at
+the end. u is an other logit's distance (over tau) below that:
+    one term: exponents of 2 H by what they bridge, in all from the logit up to its lane's last reference and from there
+    to the largest: 2 H (u + 4.2); 2 H for each exponential: its own, the steps' (u / ln(8) + 1), the last; the tree's
+    3 H:
     e_j = 9 H u_j + 18 H                            (relative)
     e_o = sum of their shares' e_j                  (relative, of the others' sum)
 What is made of it is float64, within 2^-45 of its own terms; q_r = 1 - sum q,

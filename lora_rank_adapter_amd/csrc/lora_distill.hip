@@ -43,7 +43,7 @@ struct Teacher {
 
 // A row's elements that the teacher did not name.
 struct Others {
-  float m;   // what the exponents are relative to: the largest x
+  float m;   // what the exponents are relative to: kAbove binary orders above the largest x at most
   double s;  // sum of exp((x - m) / tau)
 };
 
@@ -206,7 +206,7 @@ __device__ __forceinline__ float block_max(float v, float* lds) {
 
 template <int WAVES>
 struct PassLds {
-  float first[WAVES], most[WAVES];
+  float first[WAVES], refs[WAVES];
   double sum[WAVES];
 };
 
@@ -362,14 +362,15 @@ struct OthersPass {
         if (body + tid + h * THREADS < vecs) take(held[h], byte[body + tid + h * THREADS]);
       settle(was, body + tid + g * THREADS, U, vecs);
     }
-    m = block_max<WAVES>(m, lds.most);
-    if (sum > 0.0) sum *= __builtin_amdgcn_exp2f(s.of(z - m));
+    // to the largest reference (not to the largest logit: that factor's rounding would be all rows' and all terms')
+    const float ref = block_max<WAVES>(z, lds.refs);
+    if (sum > 0.0) sum *= __builtin_amdgcn_exp2f(s.of(z - ref));
     sum = lane_total(sum);
     if ((tid & 63) == 0) lds.sum[tid >> 6] = sum;
     __syncthreads();
     sum = 0.0;
     for (int v = 0; v < WAVES; ++v) sum += lds.sum[v];
-    return {m, sum};
+    return {ref, sum};
   }
 };
 

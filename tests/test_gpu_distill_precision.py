@@ -5,18 +5,19 @@ Bounds (H = 2^-24), none of them absolute but for underflow. The others'
 exponentials are float32, relative to a reference that no logit of the lane so
 far exceeds and that lies three binary orders above the largest of them or of the
 row's beginning, in trees of eight terms (3 H); a lane that meets a larger logit
-moves its reference and scales what it has, and all are scaled to the largest at
-the end. u is an other logit's distance (over tau) below that:
-    one term: exponents of 2 H by what they bridge, in all from the logit up to its lane's last reference and from there
-    to the largest: 2 H (u + 4.2); 2 H for each exponential: its own, the steps' (u / ln(8) + 1), the last; the tree's
-    3 H:
+moves its reference and scales what it has, and all are scaled to the largest
+reference at the end. u is an other logit's distance (over tau) below the largest
+of the others:
+    one term: exponents of 2 H by what they bridge, in all from the logit up to that reference: 2 H (u + 2.1); 2 H for
+    each exponential: its own, the steps' (u / ln(8) + 1), the last; the tree's 3 H:
     e_j = 9 H u_j + 18 H                            (relative)
     e_o = sum of their shares' e_j                  (relative, of the others' sum)
-What is made of it is float64, within 2^-45 of its own terms; q_r = 1 - sum q,
+The gradient's exponents are relative to that reference too: 2 H (u + 2.1), 2 H for the exponential and 5 H for the
+factors. What is made of the sum is float64, within 2^-45 of its own terms; q_r = 1 - sum q,
 where it is above 0, is off by 2^-46 besides. With t = p / p_r, F = Q p_r - q_r:
     err(kl) <= p_r e_o sum q + (1 - p_r) e_o q_r + H |kl| + 2^-45 (sum q (|log q| + |log p|) + q_r (|log q_r| + |log p_r|))
                + 2^-46 (1 + |log q_r| + |log p_r|) [q_r > 0]
-    tau err(dx_j) <= t_j (|F| (3 H u_j + 10 H) + max(Q p_r^2, q_r) e_o + 2^-45 (Q p_r + q_r) + 2^-46 [q_r > 0])  elsewhere
+    tau err(dx_j) <= t_j (|F| (3 H u_j + 12 H) + max(Q p_r^2, q_r) e_o + 2^-45 (Q p_r + q_r) + 2^-46 [q_r > 0])  elsewhere
                      Q p_k p_r e_o + 4 H |b_k| + 2^-45 (Q p_k + q_k)                at the teacher's tokens
 times |coef|, half a step of the output's type, and 2^-126 (|coef| / tau + 1) for what is below that."""
 import numpy as np
@@ -68,7 +69,7 @@ def tight(x64, ids, logp, tau, rest, coef, dtype):
             e_kl[t] += (1 - p_r) * e_o * q_r + 2.0 ** -46 * (1 + logs)
         e_kl[t] += 2.0 ** -45 * size
         slack = 2.0 ** -45 * (Q * p_r + q_r) + (2.0 ** -46 if q_r > 0 else 0.0)
-        e_dx[t] = np.where(other, share * (abs(Q * p_r - q_r) * (3 * H * u + 10 * H) + max(Q * p_r ** 2, q_r) * e_o + slack),
+        e_dx[t] = np.where(other, share * (abs(Q * p_r - q_r) * (3 * H * u + 12 * H) + max(Q * p_r ** 2, q_r) * e_o + slack),
                            Q * p * p_r * e_o + 4 * H * np.abs(dx[t] * tau) + 2.0 ** -45 * (Q * p + named)) / tau
     c = np.abs(coef)[:, None]
     dx, e_dx = dx * coef[:, None], e_dx * c

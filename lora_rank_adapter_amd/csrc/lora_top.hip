@@ -718,13 +718,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 16 ? 4 : HITS == 256 || sizeof
       held = vec_sums<E>(held_v, from_most);
     }
     // Both to the largest logit: its exponent relative to the first elements' is d, where there are some above -inf
-    // (all is late otherwise); the wave's, relative to it, is b, where there is a late vector.
-    const float d = first > -INFINITY ? (float)((double)m * s.hi + ((double)m * s.lo + shift)) : 0.0f;
-    const float by = __builtin_amdgcn_exp2f(-d);
+    // (all is late otherwise); the wave's, relative to it, is b, where there is a late vector. The first factor is
+    // float64: it is all terms', so that its rounding would not average out (4096 x 128256, k = 64, 189 -> 191 us).
+    const double d = first > -INFINITY ? (double)m * s.hi + ((double)m * s.lo + shift) : 0.0;
+    const double by = exp2(-d);
     late_sum += held.s;
     late_wsum += held.w;
     const float b = late_sum == 0.0 ? 0.0f : s.of(ref - m), late_by = __builtin_amdgcn_exp2f(b);
-    wsum = by == 0.0f ? 0.0 : (wsum - d * sum) * by;
+    wsum = by == 0.0 ? 0.0 : (wsum - d * sum) * by;
     sum *= by;
     if (late_by > 0.0f) wsum += (late_wsum + b * late_sum) * late_by;
     sum += late_sum * late_by;

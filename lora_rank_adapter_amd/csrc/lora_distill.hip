@@ -633,41 +633,42 @@ static int piece_splits(int64_t T, int64_t V) {
 // card idle so; in pieces they take two launches, and three with the gradient,
 // which reads all for a second time. us by rows and in pieces, k = 64, no row
 // masked; the divergence alone:
-//   bfloat16   80000 columns: 8 rows 13.2, 14.1; 96 rows 14.1, 15.0
-//             100000: 64 rows 15.3, 14.3; 96 rows 15.5, 15.7; 128 rows 16.1, 16.5; 160 rows 16.3, 18.2
-//             128256: 64 rows 17.5, 14.7; 112 rows 18.0, 16.9; 128 rows 17.7, 17.6; 160 rows 18.2, 19.3
-//             200000: 128 rows 23.0, 20.7; 160 rows 23.4, 23.5; 192 rows 23.9, 24.6
-//   float32    64000: 8 rows 13.0, 14.2; 96 rows 14.6, 15.5
-//              80000: 64 rows 15.8, 14.7; 96 rows 16.1, 15.9; 128 rows 16.8, 17.0
-//             128256: 96 rows 20.5, 18.9; 128 rows 21.4, 20.9; 160 rows 22.2, 23.8
+//   bfloat16   80000 columns: 8 rows 14.0, 15.8; 96 rows 14.7, 16.0
+//             100000: 64 rows 15.8, 16.1; 128 rows 16.1, 17.1
+//             128256: 64 rows 17.3, 15.9; 112 rows 17.5, 17.2; 128 rows 17.6, 17.9; 160 rows 17.7, 19.2
+//             200000: 128 rows 22.3, 20.2; 160 rows 22.7, 22.6; 192 rows 23.2, 23.8
+//   float32    80000: 8 rows 15.0, 15.9; 96 rows 16.0, 16.6
+//             100000: 64 rows 17.4, 16.1; 112 rows 18.0, 17.7; 128 rows 18.2, 18.9
+//             128256: 96 rows 19.7, 19.2; 128 rows 20.3, 20.5; 160 rows 21.2, 23.0
 // and a step:
-//   bfloat16   32000: 8 rows 15.7, 17.9; 50000: 8 rows 17.3, 17.5; 48 rows 18.2, 17.8; 96 rows 18.5, 20.7
-//              64000: 48 rows 20.4, 17.9; 96 rows 21.0, 22.0
-//             100000: 80 rows 26.6, 24.1; 96 rows 26.6, 26.0; 112 rows 27.1, 27.6; 128 rows 27.2, 29.3
-//             128256: 80 rows 28.1, 26.1; 96 rows 27.9, 28.4; 112 rows 28.4, 30.0
-//             200000: 96 rows 37.5, 36.1; 112 rows 38.3, 38.3; 128 rows 38.6, 41.7
-//   float32    32000: 8 rows 16.0, 17.5; 50000: 24 rows 20.5, 17.7; 48 rows 21.0, 19.9; 64 rows 21.0, 21.5
-//             128256: 48 rows 28.6, 26.0; 64 rows 28.5, 29.6
+//   bfloat16   32000: 8 rows 17.3, 20.3; 50000: 8 rows 18.2, 20.4; 96 rows 19.6, 22.6
+//              64000: 48 rows 20.8, 20.8; 96 rows 21.2, 23.4
+//             100000: 80 rows 26.9, 25.1; 96 rows 27.2, 26.6; 112 rows 27.6, 28.2
+//             128256: 80 rows 29.0, 26.8; 96 rows 28.9, 28.9; 112 rows 29.4, 30.3
+//             200000: 96 rows 38.2, 36.0; 112 rows 39.2, 38.2; 128 rows 39.4, 41.1
+//   float32    32000: 8 rows 17.3, 20.2; 50000: 24 rows 21.0, 20.3; 48 rows 21.9, 21.3; 64 rows 21.9, 22.5
+//             128256: 48 rows 29.0, 26.7; 64 rows 29.0, 29.7
+// Few rows in pieces wait for the host, which made that 15 to 16 us of a
+// divergence and 18 to 20 of a step from run to run.
 // Rows of kMaxPieceVecs vectors and more (131072 float32, 262144 bfloat16) go in
 // pieces however many they are: a workgroup's bits have no room for them. That
 // costs many rows a second read from memory; us a step of 4096 rows right below
-// and at that limit: float32 970, 1063; bfloat16 976, 1093.
+// and at that limit: float32 968, 1063; bfloat16 970, 1088.
 static bool by_rows(const lora_mat* x, bool grad) {
-  const bool f32 = x->dtype == LORA_F32;
   if (x->cols / vec_elems(x->dtype) >= kMaxPieceVecs) return false;
-  if (grad) return x->cols <= 49152 || x->rows >= (f32 ? 64 : 104);
-  return x->cols <= (f32 ? 65536 : 81920) || x->rows >= 144;
+  if (grad) return x->cols <= 49152 || x->rows >= (x->dtype == LORA_F32 ? 64 : 104);
+  return x->cols <= 81920 || x->rows >= 144;
 }
 
 // Waves to a row: with the gradient eight keep 7680 of its vectors in registers
 // (8192 of float32), four 2560, sixteen 14336. us a step of 8192 x 128256
-// bfloat16, k = 64, a third of the rows masked, by 4, 8 and 16 waves: 758, 690
-// and 785 (one workgroup of 16 to a CU leaves nothing beside its serial part).
-// Of these 690 the second read takes 24, the exponentials of the second pass 20;
+// bfloat16, k = 64, a third of the rows masked, by 4, 8 and 16 waves: 755, 697
+// and 848 (one workgroup of 16 to a CU leaves nothing beside its serial part).
+// Of these 697 the second read takes 24, the exponentials of the second pass 20;
 // the rest is 3.6 GB at 5.5 TB/s. Up to 256 long rows, one to a CU, take 16
 // waves. us a step of k = 64, 128256 columns, by 16 and by 8: bfloat16 128 rows
-// 26.9 and 28.4, 256 rows 31.1 and 36.0; float32 64 rows 27.9 and 32.5, 256 rows
-// 57.5 and 62.8. Without the gradient: bfloat16 128 rows 17.8 and 16.3.
+// 27.8 and 28.8, 256 rows 32.0 and 37.0; float32 64 rows 28.0 and 32.5, 256 rows
+// 57.6 and 62.8. Without the gradient: bfloat16 128 rows 17.8 and 16.3.
 static int row_waves(const lora_mat* x, bool grad) {
   const int64_t vecs = x->cols / vec_elems(x->dtype);
   return vecs <= 2560 ? 4 : grad && vecs > 8192 && x->rows <= 256 ? 16 : 8;

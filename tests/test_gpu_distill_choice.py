@@ -12,7 +12,7 @@ from tests.test_gpu_top import BF, F
 pytestmark = pytest.mark.gpu
 
 SIZES = [(BF, 3, 81920), (BF, 3, 81921), (BF, 143, 81921), (BF, 144, 81921), (BF, 103, 49153), (BF, 104, 49153),
-         (BF, 3, 49152), (F, 3, 65536), (F, 3, 65537), (F, 143, 65537), (F, 144, 65537), (F, 63, 49153), (F, 64, 49153),
+         (BF, 3, 49152), (F, 3, 81920), (F, 3, 81921), (F, 143, 81921), (F, 144, 81921), (F, 63, 49153), (F, 64, 49153),
          (F, 3, 49152), (F, 70, 131071), (F, 70, 131072), (BF, 104, 262143), (BF, 104, 262144)]
 
 

@@ -242,8 +242,8 @@ __device__ __forceinline__ void select_exactly(Each each, int k, Select& l) {
 // half 46.
 //
 // Memory bounds many rows: 5744 of 8192 x 128256 bfloat16 without alternatives
-// 233 us (6.3 TB/s; the loop's vector instructions went from 69 to 53 for 8
-// logits without a change), 4096 with k = 64 197 us (5.3 TB/s: of a workgroup's
+// 231 us (6.4 TB/s; the loop's vector instructions went from 69 to 53 for 8
+// logits without a change), 4096 with k = 64 193 us (5.5 TB/s: of a workgroup's
 // 40 us half go into the threshold and the selection, when only others load).
 // 256 rows are one workgroup per CU: reading takes 13 of the 21 us, the first
 // loads, the threshold and the selection the rest.
@@ -906,13 +906,13 @@ static TopShape top_shape(int64_t piece, int k) {
 // Whether 16 waves take each of very few rows whole: one launch in place of two,
 // which the host's time decides (15 us a call, and 18 with the second launch);
 // kernels of rows in pieces take about as long. us a call so and in pieces:
-//   bfloat16   65536 columns: 1 row, k 20, 15.4 and 18.2; 16 rows, k 5, 15.1 and 18.0, k 128 17.5 and 18.7
-//             100000: 1 row, k 5, 15.8 and 17.9, k 20 17.5 and 18.2, k 64 19.0 and 17.9; 16 rows, k 5, 17.6 and 17.9
-//             128256: 1 row, k 5, 16.4 and 17.8, k 20 18.2 and 18.2, k 64 19.3 and 18.1; 16 rows, k 5, 17.8 and 17.9,
-//             k 20 19.3 and 18.2
-//             140000: 1 row, k 5, 18.3 and 17.9
-//   float32    65536: 1 row, k 20, 15.2 and 18.3; 16 rows, k 128, 18.3 and 18.7
-//             128256: 1 row, k 5, 17.3 and 17.8, k 20 18.6 and 18.2; 16 rows, k 5, 18.3 and 18.1
+//   bfloat16   65536 columns: 1 row, k 20, 15.4 and 18.2; 16 rows, k 5, 15.3 and 18.0, k 128 17.9 and 18.9
+//             100000: 1 row, k 5, 15.8 and 17.9, k 20 17.8 and 18.0, k 64 19.5 and 18.1; 16 rows, k 5, 17.9 and 17.9
+//             128256: 1 row, k 5, 16.9 and 17.6, k 20 18.3 and 18.1, k 64 19.5 and 17.9; 16 rows, k 5, 18.1 and 18.0,
+//             k 20 19.5 and 18.2
+//             140000: 1 row, k 5, 18.5 and 17.8
+//   float32    65536: 1 row, k 20, 15.3 and 18.5; 16 rows, k 128, 18.5 and 19.0
+//             128256: 1 row, k 5, 17.3 and 18.1, k 20 18.7 and 18.4; 16 rows, k 5, 18.7 and 18.0
 static bool very_few(int64_t T, int64_t V, int64_t k) {
   return T <= 16 && V > 49152 && V <= (k <= 8 ? 131072 : 65536);
 }
